@@ -293,6 +293,156 @@ int w12_file_load(const char *path, int32_t count, const int32_t *which, const w
 int w12_read_probe(const void *buf, uint64_t bytes, int32_t loads_per_lane, int32_t groups_per_cu,
                    uint32_t *sink, hipStream_t stream);
 
+/*
+ * Operators around the products in one step of speculative decoding: a layer's residual addition
+ * and RMS norm, rotary positions with the write into a paged cache, attention of a chain or tree
+ * of drafted tokens over that cache, and an 8-bit product for layers that are kept in 8 bits (a
+ * drafter's; the target's weights are W12).  All conventions above apply.  Matrices here are
+ * accessed with 16-byte vectors: base pointers are 16-byte aligned and pitches are multiples of
+ * 16 bytes unless an argument says otherwise; no byte past the last element of a row is read or
+ * written.  E4M3 is the 8-bit OCP format with 3 mantissa bits (largest value 448).
+ */
+#define W12_DTYPE_BF16 0
+#define W12_DTYPE_F32 1
+#define W12_DTYPE_E4M3 2
+#define W12_QUANT_BLOCK 128   /* values that share a scale along a row */
+
+/*
+ * r = residual + delta (delta NULL: r = residual), y[m][n] = r[m][n] / sqrt(mean_n(r[m]^2) + eps)
+ * * weight[n].  Sums and the norm are FP32; the norm takes r before it is rounded for storage.
+ *   residual_out  r rounded to the residual's type; NULL: not stored; may be residual itself
+ *                 (in place) but may not overlap it otherwise.
+ *   y             BF16 (an operand of w12_gemm), or NULL.
+ *   yq, yq_scale  E4M3 with one FP32 scale per row and block of 128 columns (an operand of
+ *                 w12_gemm_e4m3), or both NULL: yq_scale[m][b] = max|y| of the block / 448 (1 for
+ *                 a block of zeros), yq = y / yq_scale rounded to nearest even.  y is taken before
+ *                 it is rounded to BF16.  A NaN or infinity in a block makes its scale NaN or
+ *                 infinite.
+ * At least one of y, yq and residual_out with a delta is wanted.  1 <= M <= 2^20, 1 <= N <= 65536.
+ */
+typedef struct w12_norm_args {
+  int32_t M, N;
+  int32_t residual_dtype;        /* W12_DTYPE_BF16 or W12_DTYPE_F32: residual, residual_out */
+  int32_t delta_dtype;           /* W12_DTYPE_BF16 or W12_DTYPE_F32                          */
+  const void *residual;          /* [M][ld_residual]                                         */
+  int64_t ld_residual;
+  const void *delta;             /* [M][ld_delta] or NULL                                    */
+  int64_t ld_delta;
+  const uint16_t *weight;        /* BF16 [N]                                                 */
+  void *residual_out;            /* [M][ld_residual_out] or NULL                             */
+  int64_t ld_residual_out;
+  uint16_t *y;                   /* BF16 [M][ldy] or NULL                                    */
+  int64_t ldy;
+  uint8_t *yq;                   /* E4M3 [M][ldyq] or NULL                                   */
+  int64_t ldyq;
+  float *yq_scale;               /* [M][ld_scale], ld_scale >= ceil(N / 128), 4-byte aligned */
+  int64_t ld_scale;
+  float eps;                     /* >= 0                                                     */
+  int32_t reserved;              /* must be 0                                                */
+} w12_norm_args;
+int w12_add_rmsnorm(const w12_norm_args *a, hipStream_t stream);
+
+/*
+ * A paged key / value cache.  Element (page p, token t of the page, head h, i) of K and of V is at
+ * p * page_stride + t * token_stride + h * head_stride + i elements (so tokens or heads may come
+ * first in a page).  E4M3 caches hold value / scale[h]; the scales are fixed when the cache is made.
+ */
+typedef struct w12_kv_cache {
+  int32_t dtype;                 /* W12_DTYPE_BF16 or W12_DTYPE_E4M3                         */
+  int32_t pages;                 /* 1 .. 2^31 - 1                                            */
+  int32_t page_size;             /* tokens of a page: a power of two, 1 .. 1024              */
+  int32_t heads;                 /* 1 .. 1024                                                */
+  int32_t dim;                   /* 64, 128 or 256                                           */
+  int32_t reserved;              /* must be 0                                                */
+  int64_t page_stride, token_stride, head_stride;   /* elements, multiples of 16 bytes, >= 0  */
+  void *k, *v;
+  const float *k_scale, *v_scale;                   /* [heads], E4M3 only                     */
+} w12_kv_cache;
+
+/*
+ * Takes T rows of a QKV product (q_heads query heads, then the cache's heads of K, then of V),
+ * turns Q and K by their positions, stores Q as BF16 and puts K and V into the cache at
+ * slots[t] = page * page_size + token of the page.  Rows whose slot is negative or past the cache
+ * are not put (their Q is stored all the same).  The other slots must differ from one another.
+ * Pair i of the first rot_dim elements of a head is (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ * adjacent != 0; it is turned by positions[axis[i]][t] * inv_freq[i], an angle formed in FP64 (far
+ * positions keep their phase).  Several axes serve images and video (time, height, width); axis
+ * NULL takes axis 0 throughout, a value past the last axis takes the last.  Elements past rot_dim
+ * are copied.  E4M3 caches: value / scale[h] rounded to nearest even, cut off at +-448, NaN kept.
+ * 1 <= T <= 2^20, rot_dim even, 0 <= rot_dim <= dim, 1 <= axes <= 8, 1 <= q_heads <= 4096.
+ */
+typedef struct w12_rope_args {
+  int32_t T, q_heads;
+  int32_t src_dtype;             /* W12_DTYPE_F32 (a w12_gemm result) or W12_DTYPE_BF16      */
+  int32_t rot_dim, axes, adjacent;
+  const void *qkv;               /* [T][ld_qkv]                                              */
+  int64_t ld_qkv;
+  const int32_t *positions;      /* [axes][ld_positions], ld_positions >= T                  */
+  int64_t ld_positions;
+  const int64_t *slots;          /* [T]                                                      */
+  const double *inv_freq;        /* [rot_dim / 2], radians per position                      */
+  const uint8_t *axis;           /* [rot_dim / 2] or NULL                                    */
+  uint16_t *q;                   /* BF16 [T][ldq], q_heads * dim of a row written            */
+  int64_t ldq;
+} w12_rope_args;
+int w12_rope_append(const w12_rope_args *a, const w12_kv_cache *cache, hipStream_t stream);
+
+/*
+ * Attention of drafted tokens.  Request b has the rows (nodes) node_ptr[b] .. node_ptr[b+1] - 1 of
+ * q, its first ctx_len[b] tokens are in the cache, and its node i is the cache's token ctx_len[b] + i
+ * (w12_rope_append put it there).  Token t of a request is in page page_table[b][t / page_size].
+ * Node i attends every token before ctx_len[b], and of the nodes those whose bit is set in its
+ * row of tree_mask (bit j % 64 of word j / 64 for node j; its own bit is not implied; nodes past
+ * the words are not attended), or with tree_mask NULL the nodes 0..i (a chain).  Query head h
+ * reads cache head h / (q_heads / heads).
+ *   out[row][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max),  in FP32.
+ *   lse[row][h] = log sum_t exp(scale * q . k_t), if lse is not NULL.
+ * What a row does not attend never reaches it, NaN and infinity included.  A row that attends
+ * nothing gives zeros and lse -inf.  Tokens past max_pages * page_size, and tokens whose page is
+ * not in 0 .. pages - 1, count as absent.  Rows outside every request are left as they are;
+ * ranges of node_ptr are cut to 0..T and must not decrease; negative lengths count as 0.
+ * node_ptr, ctx_len, page_table and tree_mask are device memory read by the kernels (a captured
+ * graph follows their values).  The result is bitwise the same from run to run.
+ * 1 <= T <= 2^20, 1 <= requests <= 1024, q_heads a multiple of heads (at most 64 times heads),
+ * 1 <= mask_words <= 64, max_pages * page_size < 2^30.
+ * ws: w12_tree_attention_workspace_size bytes, 16-byte aligned, any content; calls that overlap in
+ * time need workspaces of their own.
+ */
+typedef struct w12_attention_args {
+  int32_t T, requests, q_heads, max_pages;
+  int32_t mask_words;            /* words of a tree_mask row (0 with tree_mask NULL)         */
+  float scale;
+  const uint16_t *q;             /* BF16 [T][ldq], head h at h * dim                         */
+  int64_t ldq;
+  const int32_t *node_ptr;       /* [requests + 1]                                           */
+  const int32_t *ctx_len;        /* [requests]                                               */
+  const int32_t *page_table;     /* [requests][ld_table]                                     */
+  int64_t ld_table;
+  const uint64_t *tree_mask;     /* [T][ld_mask] or NULL, 8-byte aligned                     */
+  int64_t ld_mask;
+  uint16_t *out;                 /* BF16 [T][ldo], head h at h * dim                         */
+  int64_t ldo;
+  float *lse;                    /* [T][ld_lse] or NULL, 4-byte aligned                      */
+  int64_t ld_lse;
+} w12_attention_args;
+int w12_tree_attention_workspace_size(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache *cache,
+                                      uint64_t *bytes);
+int w12_tree_attention(const w12_attention_args *a, const w12_kv_cache *cache, void *ws, uint64_t ws_bytes,
+                       hipStream_t stream);
+
+/*
+ * Y[m][n] = sum_k (X[m][k] x_scale[m][k / 128]) (W[n][k] w_scale[n / 128][k / 128]) with E4M3 X and
+ * W, FP32 scales, sums and Y: one scale per row and block of 128 of X (as w12_add_rmsnorm gives
+ * them), one per block of 128 x 128 of W.  Bitwise the same from run to run for the same (M, N, K).
+ * ldx and ldw are multiples of 16 bytes; ldxs, ldws >= ceil(K / 128); Y is 4-byte aligned.
+ * 1 <= M <= 4096, N and K as for w12_gemm.  ws: as for w12_gemm (w12_gemm_e4m3_workspace_size
+ * bytes, initialised once with w12_gemm_workspace_init; every call leaves its counters zero).
+ */
+int w12_gemm_e4m3_workspace_size(int32_t M, int32_t N, int32_t K, uint64_t *bytes);
+int w12_gemm_e4m3(const uint8_t *X, int32_t M, int64_t ldx, const float *x_scale, int64_t ldxs, const uint8_t *W,
+                  int32_t N, int32_t K, int64_t ldw, const float *w_scale, int64_t ldws, float *Y, int64_t ldy,
+                  void *ws, uint64_t ws_bytes, hipStream_t stream);
+
 /* Stored bits per weight: (1.5*N*K + N + 4*(N+1) + 4*E) * 8 / (N*K).  -1 for N < 1, K < 1
  * or E < 0. */
 double w12_bits_per_weight(int32_t N, int32_t K, int64_t E);

@@ -49,6 +49,33 @@ class _PlanInfo(ctypes.Structure):
     ]
 
 
+class _NormArgs(ctypes.Structure):
+    _fields_ = [("M", _c_i32), ("N", _c_i32), ("residual_dtype", _c_i32), ("delta_dtype", _c_i32),
+                ("residual", _c_p), ("ld_residual", _c_i64), ("delta", _c_p), ("ld_delta", _c_i64), ("weight", _c_p),
+                ("residual_out", _c_p), ("ld_residual_out", _c_i64), ("y", _c_p), ("ldy", _c_i64),
+                ("yq", _c_p), ("ldyq", _c_i64), ("yq_scale", _c_p), ("ld_scale", _c_i64),
+                ("eps", ctypes.c_float), ("reserved", _c_i32)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("dtype", _c_i32), ("pages", _c_i32), ("page_size", _c_i32), ("heads", _c_i32), ("dim", _c_i32),
+                ("reserved", _c_i32), ("page_stride", _c_i64), ("token_stride", _c_i64), ("head_stride", _c_i64),
+                ("k", _c_p), ("v", _c_p), ("k_scale", _c_p), ("v_scale", _c_p)]
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("T", _c_i32), ("q_heads", _c_i32), ("src_dtype", _c_i32), ("rot_dim", _c_i32), ("axes", _c_i32),
+                ("adjacent", _c_i32), ("qkv", _c_p), ("ld_qkv", _c_i64), ("positions", _c_p), ("ld_positions", _c_i64),
+                ("slots", _c_p), ("inv_freq", _c_p), ("axis", _c_p), ("q", _c_p), ("ldq", _c_i64)]
+
+
+class _AttentionArgs(ctypes.Structure):
+    _fields_ = [("T", _c_i32), ("requests", _c_i32), ("q_heads", _c_i32), ("max_pages", _c_i32), ("mask_words", _c_i32),
+                ("scale", ctypes.c_float), ("q", _c_p), ("ldq", _c_i64), ("node_ptr", _c_p), ("ctx_len", _c_p),
+                ("page_table", _c_p), ("ld_table", _c_i64), ("tree_mask", _c_p), ("ld_mask", _c_i64),
+                ("out", _c_p), ("ldo", _c_i64), ("lse", _c_p), ("ld_lse", _c_i64)]
+
+
 _SIGNATURES = {
     "w12_layout_bytes": (ctypes.c_int, [_c_i32, _c_i32, ctypes.POINTER(_c_u64), ctypes.POINTER(_c_u64)]),
     "w12_encode_count": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p]),
@@ -70,6 +97,14 @@ _SIGNATURES = {
     "w12_file_load": (ctypes.c_int, [ctypes.c_char_p, _c_i32, ctypes.POINTER(_c_i32), ctypes.POINTER(_Tensor), _c_p,
                                      _c_u64, ctypes.POINTER(_c_p), ctypes.POINTER(_c_i64), _c_p, _c_p]),
     "w12_read_probe": (ctypes.c_int, [_c_p, _c_u64, _c_i32, _c_i32, _c_p, _c_p]),
+    "w12_add_rmsnorm": (ctypes.c_int, [ctypes.POINTER(_NormArgs), _c_p]),
+    "w12_rope_append": (ctypes.c_int, [ctypes.POINTER(_RopeArgs), ctypes.POINTER(_KVCache), _c_p]),
+    "w12_tree_attention_workspace_size": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, ctypes.POINTER(_KVCache),
+                                                         ctypes.POINTER(_c_u64)]),
+    "w12_tree_attention": (ctypes.c_int, [ctypes.POINTER(_AttentionArgs), ctypes.POINTER(_KVCache), _c_p, _c_u64, _c_p]),
+    "w12_gemm_e4m3_workspace_size": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, ctypes.POINTER(_c_u64)]),
+    "w12_gemm_e4m3": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_p, _c_i64, _c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_i64, _c_p,
+                                     _c_i64, _c_p, _c_u64, _c_p]),
     "w12_bits_per_weight": (ctypes.c_double, [_c_i32, _c_i32, _c_i64]),
     "w12_tensor_bytes": (_c_u64, [_c_i32, _c_i32, _c_i64]),
     "w12_status_string": (ctypes.c_char_p, [ctypes.c_int]),

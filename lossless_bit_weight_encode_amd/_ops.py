@@ -1,0 +1,292 @@
+"""Binding of the operators around the products: residual RMS norm, rotary cache write, tree attention
+and the 8-bit block product.  Argument marshalling only, as in ``_lib``: every call checks that its
+tensors are on one GPU and have the shapes and types of the C ABI (include/w12.h), enqueues on the
+current stream (or ``stream``) and returns; pitches and alignment are checked by the library."""
+from __future__ import annotations
+
+import ctypes
+import math
+
+import torch
+
+from ._lib import _AttentionArgs, _KVCache, _NormArgs, _RopeArgs, _c_u64, _check, lib
+
+DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
+QUANT_BLOCK = 128
+
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_FLOATS = {_BF16: DTYPE_BF16, _F32: DTYPE_F32}
+
+
+def _device(*ts) -> torch.device:
+    """The one GPU that every tensor is on; it has to be the current one, whose streams the call uses."""
+    d = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU (libw12 has no CPU path)")
+        i = t.get_device()
+        if d is None:
+            d = i
+        elif d != i:
+            raise ValueError("tensors are on different GPUs")
+    if d != torch.cuda.current_device():
+        raise ValueError("the tensors' GPU is not the current one (use torch.cuda.device)")
+    return d
+
+
+def _raw_stream(stream) -> int:
+    return torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+
+
+def _rows(t: torch.Tensor, what: str, shape: tuple, dtypes, step: int) -> int:
+    """Checks a matrix with contiguous rows; its pitch in elements.  A single row is never stepped
+    by its pitch, and torch may report any stride for it, so it gets its padded width."""
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{what}: expected shape {shape}, got {tuple(t.shape)}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{what}: expected {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: rows must be contiguous")
+    if shape[0] == 1:
+        return -(-shape[1] // step) * step
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, what: str, n: int, dtype) -> None:
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{what}: expected shape {(n,)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: expected {dtype}, got {t.dtype}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{what}: must be contiguous")
+
+
+def _matrix2(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what}: expected a 2-D tensor")
+    return t.shape
+
+
+def add_rmsnorm(residual: torch.Tensor, weight: torch.Tensor, delta: torch.Tensor | None = None, eps: float = 1e-6,
+                residual_out: torch.Tensor | None = None, y: torch.Tensor | None = None, yq: torch.Tensor | None = None,
+                yq_scale: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """r = residual + delta, stored to residual_out (which may be residual itself); y = r's RMS norm times
+    weight.  residual and delta: BF16 or FP32 [M, N], rows of whole 16-byte steps; weight: BF16 [N].
+
+    y (BF16, what gemm() takes) and yq with yq_scale (E4M3 and a scale per row and 128 columns, what
+    gemm_e4m3() takes) are the outputs that are wanted; with none given, y is allocated here, on the
+    stream.  Returns y (None when only yq is wanted)."""
+    m, n = _matrix2(residual, "residual")
+    if y is None and yq is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            y = torch.empty(m, (n + 7) // 8 * 8, dtype=_BF16, device=residual.device)[:, :n]
+    _device(residual, weight, delta, residual_out, y, yq, yq_scale)
+    a = _NormArgs()
+    a.M, a.N, a.eps = m, n, eps
+    shape = (m, n)
+    step = 8 if residual.dtype == _BF16 else 4
+    a.ld_residual = _rows(residual, "residual", shape, _FLOATS, step)
+    a.residual_dtype = _FLOATS[residual.dtype]
+    a.residual = residual.data_ptr()
+    _vector(weight, "weight", n, _BF16)
+    a.weight = weight.data_ptr()
+    if delta is not None:
+        a.ld_delta = _rows(delta, "delta", shape, _FLOATS, 8 if delta.dtype == _BF16 else 4)
+        a.delta_dtype = _FLOATS[delta.dtype]
+        a.delta = delta.data_ptr()
+    if residual_out is not None:
+        a.ld_residual_out = _rows(residual_out, "residual_out", shape, (residual.dtype,), step)
+        a.residual_out = residual_out.data_ptr()
+    if y is not None:
+        a.ldy = _rows(y, "y", shape, (_BF16,), 8)
+        a.y = y.data_ptr()
+    if yq is not None:
+        if yq_scale is None:
+            raise ValueError("yq needs yq_scale")
+        a.ldyq = _rows(yq, "yq", shape, (_E4M3,), 16)
+        a.yq = yq.data_ptr()
+        a.ld_scale = _rows(yq_scale, "yq_scale", (m, -(-n // QUANT_BLOCK)), (_F32,), 1)
+        a.yq_scale = yq_scale.data_ptr()
+    elif yq_scale is not None:
+        raise ValueError("yq_scale without yq")
+    _check("w12_add_rmsnorm", lib().w12_add_rmsnorm(ctypes.byref(a), _raw_stream(stream)))
+    return y
+
+
+class KVCache:
+    """A paged key / value cache: K and V [pages, page_size, heads, dim] (BF16, or E4M3 with a scale per head;
+    views with other orders of the axes are fine as long as dim is contiguous).  The object keeps the
+    tensors and their C descriptor; the cache's contents belong to the caller."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.shape != v.shape:
+            raise ValueError("k and v must have one shape [pages, page_size, heads, dim]")
+        if k.dtype != v.dtype or k.dtype not in (_BF16, _E4M3):
+            raise TypeError("k and v must both be bfloat16 or both float8_e4m3fn")
+        if k.stride() != v.stride() or k.stride(3) != 1:
+            raise ValueError("k and v must have the same strides, with dim contiguous")
+        pages, page, heads, dim = k.shape
+        if (k.dtype == _E4M3) != (k_scale is not None) or (k_scale is None) != (v_scale is None):
+            raise ValueError("an E4M3 cache has k_scale and v_scale, a BF16 cache has none")
+        if k_scale is not None:
+            _vector(k_scale, "k_scale", heads, _F32)
+            _vector(v_scale, "v_scale", heads, _F32)
+        for t in (k, v, k_scale, v_scale):
+            if t is not None and not t.is_cuda:
+                raise ValueError("tensors must live on the GPU (libw12 has no CPU path)")
+            if t is not None and t.device != k.device:
+                raise ValueError("tensors are on different GPUs")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.page_size, self.heads, self.dim = pages, page, heads, dim
+        d = self.desc = _KVCache()
+        d.dtype = DTYPE_BF16 if k.dtype == _BF16 else DTYPE_E4M3
+        d.pages, d.page_size, d.heads, d.dim = pages, page, heads, dim
+        d.page_stride, d.token_stride, d.head_stride = (0 if s == 1 else k.stride(i) for i, s in enumerate(k.shape[:3]))
+        d.k, d.v = k.data_ptr(), v.data_ptr()
+        if k_scale is not None:
+            d.k_scale, d.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
+
+
+def rope_append(qkv: torch.Tensor, cache: KVCache, positions: torch.Tensor, slots: torch.Tensor, inv_freq: torch.Tensor,
+                q_heads: int, axis: torch.Tensor | None = None, adjacent: bool = False, q: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Rows [T, (q_heads + 2 heads) * dim] of a QKV product (FP32 or BF16) -> Q (BF16 [T, q_heads * dim],
+    returned), and K, V put into the cache at slots (int64 [T]: page * page_size + token of the page;
+    a negative slot is not put).  Q and K are turned by positions (int32 [axes, T]) times inv_freq
+    (float64 [rot_dim / 2]); axis (uint8 [rot_dim / 2]) names the axis of every pair."""
+    t, width = _matrix2(qkv, "qkv")
+    dim = cache.dim
+    if width != (q_heads + 2 * cache.heads) * dim:
+        raise ValueError(f"qkv: expected {(q_heads + 2 * cache.heads) * dim} columns, got {width}")
+    if q is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            q = torch.empty(t, q_heads * dim, dtype=_BF16, device=qkv.device)
+    _device(qkv, cache.k, positions, slots, inv_freq, axis, q)
+    a = _RopeArgs()
+    a.T, a.q_heads, a.adjacent = t, q_heads, int(adjacent)
+    a.ld_qkv = _rows(qkv, "qkv", (t, width), _FLOATS, 8)
+    a.src_dtype = _FLOATS[qkv.dtype]
+    a.qkv = qkv.data_ptr()
+    a.axes = _matrix2(positions, "positions")[0]
+    a.ld_positions = _rows(positions, "positions", (a.axes, t), (torch.int32,), 1)
+    a.positions = positions.data_ptr()
+    _vector(slots, "slots", t, torch.int64)
+    a.slots = slots.data_ptr()
+    pairs = inv_freq.numel()
+    _vector(inv_freq, "inv_freq", pairs, torch.float64)
+    a.rot_dim = 2 * pairs
+    a.inv_freq = inv_freq.data_ptr()
+    if axis is not None:
+        _vector(axis, "axis", pairs, torch.uint8)
+        a.axis = axis.data_ptr()
+    a.ldq = _rows(q, "q", (t, q_heads * dim), (_BF16,), 8)
+    a.q = q.data_ptr()
+    _check("w12_rope_append", lib().w12_rope_append(ctypes.byref(a), ctypes.byref(cache.desc), _raw_stream(stream)))
+    return q
+
+
+def tree_attention_workspace_size(rows: int, requests: int, q_heads: int, cache: KVCache) -> int:
+    b = _c_u64()
+    _check("w12_tree_attention_workspace_size",
+           lib().w12_tree_attention_workspace_size(rows, requests, q_heads, ctypes.byref(cache.desc), ctypes.byref(b)))
+    return b.value
+
+
+def tree_attention_workspace(rows: int, requests: int, q_heads: int, cache: KVCache) -> torch.Tensor | None:
+    """A workspace for tree_attention() of at most this many rows and requests over this cache, or None."""
+    need = tree_attention_workspace_size(rows, requests, q_heads, cache)
+    return torch.empty(need, dtype=torch.uint8, device=cache.k.device) if need else None
+
+
+def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ctx_len: torch.Tensor,
+                   node_ptr: torch.Tensor, tree_mask: torch.Tensor | None = None, scale: float | None = None,
+                   out: torch.Tensor | None = None, lse: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over a paged cache (w12_tree_attention): q BF16 [T, q_heads * dim] ->
+    out BF16 [T, q_heads * dim], and lse FP32 [T, q_heads] if given.
+
+    Request b has rows node_ptr[b] .. node_ptr[b + 1] - 1 (int32 [B + 1]) and ctx_len[b] (int32 [B]) tokens in
+    the cache; its node i is token ctx_len[b] + i.  page_table: int32 [B, max_pages].  tree_mask: int64
+    [T, words], bit j % 64 of word j / 64 set where the row's node attends node j of its request; None: a chain.
+    scale: 1 / sqrt(dim) by default.  ws: tree_attention_workspace(); allocated here when omitted."""
+    t, width = _matrix2(q, "q")
+    dim = cache.dim
+    q_heads = width // dim
+    if q_heads * dim != width or q_heads == 0:
+        raise ValueError(f"q: {width} columns are not whole heads of {dim}")
+    if out is None or ws is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            if out is None:
+                out = torch.empty(t, width, dtype=_BF16, device=q.device)
+            if ws is None:
+                ws = tree_attention_workspace(t, ctx_len.numel(), q_heads, cache)
+    _device(q, cache.k, page_table, ctx_len, node_ptr, tree_mask, out, lse, ws)
+    a = _AttentionArgs()
+    requests = ctx_len.numel()
+    a.T, a.requests, a.q_heads = t, requests, q_heads
+    a.scale = 1.0 / math.sqrt(dim) if scale is None else scale
+    a.ldq = _rows(q, "q", (t, width), (_BF16,), 8)
+    a.q = q.data_ptr()
+    _vector(ctx_len, "ctx_len", requests, torch.int32)
+    _vector(node_ptr, "node_ptr", requests + 1, torch.int32)
+    a.ctx_len, a.node_ptr = ctx_len.data_ptr(), node_ptr.data_ptr()
+    a.max_pages = _matrix2(page_table, "page_table")[1]
+    a.ld_table = _rows(page_table, "page_table", (requests, a.max_pages), (torch.int32,), 1)
+    a.page_table = page_table.data_ptr()
+    if tree_mask is not None:
+        a.mask_words = _matrix2(tree_mask, "tree_mask")[1]
+        a.ld_mask = _rows(tree_mask, "tree_mask", (t, a.mask_words), (torch.int64, torch.uint64), 1)
+        a.tree_mask = tree_mask.data_ptr()
+    a.ldo = _rows(out, "out", (t, width), (_BF16,), 8)
+    a.out = out.data_ptr()
+    if lse is not None:
+        a.ld_lse = _rows(lse, "lse", (t, q_heads), (_F32,), 1)
+        a.lse = lse.data_ptr()
+    wsp, wsb = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check("w12_tree_attention", lib().w12_tree_attention(ctypes.byref(a), ctypes.byref(cache.desc), wsp, wsb,
+                                                          _raw_stream(stream)))
+    return out
+
+
+def gemm_e4m3_workspace_size(m: int, n: int, k: int) -> int:
+    b = _c_u64()
+    _check("w12_gemm_e4m3_workspace_size", lib().w12_gemm_e4m3_workspace_size(m, n, k, ctypes.byref(b)))
+    return b.value
+
+
+def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
+    """A ready-to-use (zero-initialised) workspace for gemm_e4m3() with M=m on W[n][k], or None."""
+    need = gemm_e4m3_workspace_size(m, n, k)
+    if not need:
+        return None
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    _check("w12_gemm_workspace_init", lib().w12_gemm_workspace_init(ws.data_ptr(), need, _raw_stream(stream)))
+    return ws
+
+
+def gemm_e4m3(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor,
+              y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Y[M, N] (FP32) = (X x_scale) (W w_scale)^T with E4M3 X [M, K] and W [N, K], x_scale FP32 [M, ceil(K / 128)] and
+    w_scale FP32 [ceil(N / 128), ceil(K / 128)].  ws: gemm_e4m3_workspace(); allocated here when omitted."""
+    m, k = _matrix2(x, "x")
+    n = _matrix2(w, "w")[0]
+    kb = -(-k // QUANT_BLOCK)
+    if y is None or ws is None:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            if y is None:
+                y = torch.empty(m, n, dtype=_F32, device=x.device)
+            if ws is None:
+                ws = gemm_e4m3_workspace(m, n, k, x.device)
+    _device(x, x_scale, w, w_scale, y, ws)
+    wsp, wsb = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    _check("w12_gemm_e4m3", lib().w12_gemm_e4m3(
+        x.data_ptr(), m, _rows(x, "x", (m, k), (_E4M3,), 16),
+        x_scale.data_ptr(), _rows(x_scale, "x_scale", (m, kb), (_F32,), 1),
+        w.data_ptr(), n, k, _rows(w, "w", (n, k), (_E4M3,), 16),
+        w_scale.data_ptr(), _rows(w_scale, "w_scale", (-(-n // QUANT_BLOCK), kb), (_F32,), 1),
+        y.data_ptr(), _rows(y, "y", (m, n), (_F32,), 1), wsp, wsb, _raw_stream(stream)))
+    return y
+

@@ -27,7 +27,8 @@ LIB = os.path.join(PKG, "libw12.so")
 TIMELINE_LIB = os.path.join(PKG, "libw12_timeline.so")
 ARCH = os.environ.get("W12_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["w12_encode.hip", "w12_decode.hip", "w12_gemm.hip", "w12_gemm_wide.hip", "w12_probe.hip", "w12_noalloc.hip", "w12_api.cpp", "w12_file.cpp"]
+SOURCES = ["w12_encode.hip", "w12_decode.hip", "w12_gemm.hip", "w12_gemm_wide.hip", "w12_probe.hip", "w12_noalloc.hip",
+           "w12_norm.hip", "w12_rope.hip", "w12_attention.hip", "w12_gemm_e4m3.hip", "w12_api.cpp", "w12_file.cpp"]
 
 COMMON = [
     f"--offload-arch={ARCH}",

@@ -359,6 +359,206 @@ int w12_read_probe(const void* buf, uint64_t bytes, int32_t loads_per_lane, int3
   return hip_status(w12::launch_read_probe(buf, bytes, loads_per_lane, grid, sink, stream), "read_probe");
 }
 
+// A matrix accessed with 16-byte vectors: aligned base, rows of whole 16-byte steps, and (where rows
+// have to hold cols) a pitch of at least cols.
+static int check_matrix(const void* p, int64_t ld, int64_t rows, int64_t cols, int elem_bytes, const char* what) {
+  if (!p) return fail(W12_ERR_INVALID_ARG, "%s is NULL", what);
+  if (ld < cols) return fail(W12_ERR_INVALID_ARG, "%s pitch %lld < %lld columns", what, (long long)ld, (long long)cols);
+  if (!aligned(p, 16)) return fail(W12_ERR_MISALIGNED, "%s must be 16-byte aligned", what);
+  if (ld % (16 / elem_bytes))
+    return fail(W12_ERR_MISALIGNED, "%s pitch %lld must be a multiple of 16 bytes", what, (long long)ld);
+  if (rows > 1 && ld > (int64_t(1) << 40) / rows)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "%s pitch %lld is too large", what, (long long)ld);
+  return W12_OK;
+}
+
+// An array of 4- or 8-byte values with a pitch of at least cols.
+static int check_table(const void* p, int64_t ld, int64_t rows, int64_t cols, int elem_bytes, const char* what) {
+  if (!p) return fail(W12_ERR_INVALID_ARG, "%s is NULL", what);
+  if (ld < cols) return fail(W12_ERR_INVALID_ARG, "%s pitch %lld < %lld columns", what, (long long)ld, (long long)cols);
+  if (!aligned(p, elem_bytes)) return fail(W12_ERR_MISALIGNED, "%s must be %d-byte aligned", what, elem_bytes);
+  if (rows > 1 && ld > (int64_t(1) << 40) / rows)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "%s pitch %lld is too large", what, (long long)ld);
+  return W12_OK;
+}
+
+static constexpr int32_t kMaxRows = 1 << 20;   // rows of the operators that stream rows
+
+static bool float_dtype(int32_t d) { return d == W12_DTYPE_BF16 || d == W12_DTYPE_F32; }
+
+int w12_add_rmsnorm(const w12_norm_args* a, hipStream_t stream) {
+  if (!a) return fail(W12_ERR_INVALID_ARG, "arguments are NULL");
+  if (a->reserved != 0) return fail(W12_ERR_INVALID_ARG, "reserved field must be 0");
+  if (a->M < 1 || a->M > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "M=%d outside 1..%d", a->M, kMaxRows);
+  if (a->N < 1 || a->N > kMaxK) return fail(W12_ERR_UNSUPPORTED_SHAPE, "N=%d outside 1..65536", a->N);
+  if (!float_dtype(a->residual_dtype) || (a->delta && !float_dtype(a->delta_dtype)))
+    return fail(W12_ERR_INVALID_ARG, "residual and delta are BF16 or FP32");
+  if (!(a->eps >= 0.0f)) return fail(W12_ERR_INVALID_ARG, "eps must not be negative");
+  const int rb = a->residual_dtype == W12_DTYPE_F32 ? 4 : 2;
+  int rc = check_matrix(a->residual, a->ld_residual, a->M, a->N, rb, "residual");
+  if (rc) return rc;
+  if (a->delta && (rc = check_matrix(a->delta, a->ld_delta, a->M, a->N, a->delta_dtype == W12_DTYPE_F32 ? 4 : 2, "delta")))
+    return rc;
+  if (!a->weight) return fail(W12_ERR_INVALID_ARG, "weight is NULL");
+  if (!aligned(a->weight, 16)) return fail(W12_ERR_MISALIGNED, "weight must be 16-byte aligned");
+  if (a->residual_out) {
+    if ((rc = check_matrix(a->residual_out, a->ld_residual_out, a->M, a->N, rb, "residual_out"))) return rc;
+    if (a->residual_out == a->residual && a->ld_residual_out != a->ld_residual)
+      return fail(W12_ERR_INVALID_ARG, "residual_out in place needs the residual's pitch");
+  }
+  if (a->y && (rc = check_matrix(a->y, a->ldy, a->M, a->N, 2, "y"))) return rc;
+  if (a->yq) {
+    if ((rc = check_matrix(a->yq, a->ldyq, a->M, a->N, 1, "yq"))) return rc;
+    if ((rc = check_table(a->yq_scale, a->ld_scale, a->M, w12::ceil_div(a->N, W12_QUANT_BLOCK), 4, "yq_scale"))) return rc;
+  } else if (a->yq_scale) {
+    return fail(W12_ERR_INVALID_ARG, "yq_scale without yq");
+  }
+  if (!a->y && !a->yq && !(a->residual_out && a->delta)) return fail(W12_ERR_INVALID_ARG, "no output is wanted");
+  return hip_status(w12::launch_add_rmsnorm(*a, stream), "add_rmsnorm");
+}
+
+static int check_cache(const w12_kv_cache* c) {
+  if (!c) return fail(W12_ERR_INVALID_ARG, "cache is NULL");
+  if (c->reserved != 0) return fail(W12_ERR_INVALID_ARG, "cache: reserved field must be 0");
+  if (c->dtype != W12_DTYPE_BF16 && c->dtype != W12_DTYPE_E4M3)
+    return fail(W12_ERR_INVALID_ARG, "cache: type %d is neither BF16 nor E4M3", c->dtype);
+  if (c->pages < 1) return fail(W12_ERR_UNSUPPORTED_SHAPE, "cache: %d pages", c->pages);
+  if (c->page_size < 1 || c->page_size > 1024 || (c->page_size & (c->page_size - 1)))
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "cache: page size %d is not a power of two in 1..1024", c->page_size);
+  if (c->heads < 1 || c->heads > 1024) return fail(W12_ERR_UNSUPPORTED_SHAPE, "cache: %d heads outside 1..1024", c->heads);
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "cache: head dimension %d is not 64, 128 or 256", c->dim);
+  if (!c->k || !c->v) return fail(W12_ERR_INVALID_ARG, "cache: k or v is NULL");
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(W12_ERR_MISALIGNED, "cache: k and v must be 16-byte aligned");
+  const int64_t step = c->dtype == W12_DTYPE_BF16 ? 8 : 16;
+  const int64_t strides[3] = {c->page_stride, c->token_stride, c->head_stride};
+  for (int64_t s : strides) {
+    if (s < 0) return fail(W12_ERR_INVALID_ARG, "cache: negative stride");
+    if (s % step) return fail(W12_ERR_MISALIGNED, "cache: stride %lld must be a multiple of 16 bytes", (long long)s);
+  }
+  if (c->page_stride > (int64_t(1) << 42) / c->pages || c->token_stride > (int64_t(1) << 32) / c->page_size ||
+      c->head_stride > (int64_t(1) << 32) / c->heads)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "cache: strides too large");
+  if (c->dtype == W12_DTYPE_E4M3) {
+    if (!c->k_scale || !c->v_scale) return fail(W12_ERR_INVALID_ARG, "cache: an E4M3 cache needs k_scale and v_scale");
+    if (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+      return fail(W12_ERR_MISALIGNED, "cache: scales must be 4-byte aligned");
+  }
+  return W12_OK;
+}
+
+int w12_rope_append(const w12_rope_args* a, const w12_kv_cache* cache, hipStream_t stream) {
+  if (!a) return fail(W12_ERR_INVALID_ARG, "arguments are NULL");
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (a->T < 1 || a->T > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "T=%d outside 1..%d", a->T, kMaxRows);
+  if (a->q_heads < 1 || a->q_heads > 4096) return fail(W12_ERR_UNSUPPORTED_SHAPE, "q_heads=%d outside 1..4096", a->q_heads);
+  if (!float_dtype(a->src_dtype)) return fail(W12_ERR_INVALID_ARG, "qkv is BF16 or FP32");
+  if (a->rot_dim < 0 || a->rot_dim > cache->dim || a->rot_dim % 2)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "rot_dim=%d is not an even number in 0..%d", a->rot_dim, cache->dim);
+  if (a->axes < 1 || a->axes > 8) return fail(W12_ERR_UNSUPPORTED_SHAPE, "axes=%d outside 1..8", a->axes);
+  const int64_t width = (int64_t)(a->q_heads + 2 * cache->heads) * cache->dim;
+  if ((rc = check_matrix(a->qkv, a->ld_qkv, a->T, width, a->src_dtype == W12_DTYPE_F32 ? 4 : 2, "qkv"))) return rc;
+  if ((rc = check_matrix(a->q, a->ldq, a->T, (int64_t)a->q_heads * cache->dim, 2, "q"))) return rc;
+  if (a->rot_dim) {
+    if ((rc = check_table(a->positions, a->ld_positions, a->axes, a->T, 4, "positions"))) return rc;
+    if (!a->inv_freq) return fail(W12_ERR_INVALID_ARG, "inv_freq is NULL");
+    if (!aligned(a->inv_freq, 8)) return fail(W12_ERR_MISALIGNED, "inv_freq must be 8-byte aligned");
+  }
+  if (!a->slots) return fail(W12_ERR_INVALID_ARG, "slots is NULL");
+  if (!aligned(a->slots, 8)) return fail(W12_ERR_MISALIGNED, "slots must be 8-byte aligned");
+  return hip_status(w12::launch_rope_append(*a, *cache, stream), "rope_append");
+}
+
+static int check_attention_shape(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache* cache) {
+  int rc = check_cache(cache);
+  if (rc) return rc;
+  if (T < 1 || T > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "T=%d outside 1..%d", T, kMaxRows);
+  if (requests < 1 || requests > 1024) return fail(W12_ERR_UNSUPPORTED_SHAPE, "requests=%d outside 1..1024", requests);
+  if (q_heads < 1 || q_heads % cache->heads || q_heads / cache->heads > 64)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "q_heads=%d is not 1..64 times the cache's %d heads", q_heads, cache->heads);
+  return W12_OK;
+}
+
+int w12_tree_attention_workspace_size(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache* cache,
+                                      uint64_t* bytes) {
+  int rc = check_attention_shape(T, requests, q_heads, cache);
+  if (rc) return rc;
+  if (!bytes) return fail(W12_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = w12::attention_workspace_bytes(T, requests, q_heads, *cache);
+  return ok();
+}
+
+int w12_tree_attention(const w12_attention_args* a, const w12_kv_cache* cache, void* ws, uint64_t ws_bytes,
+                       hipStream_t stream) {
+  if (!a) return fail(W12_ERR_INVALID_ARG, "arguments are NULL");
+  int rc = check_attention_shape(a->T, a->requests, a->q_heads, cache);
+  if (rc) return rc;
+  const int64_t width = (int64_t)a->q_heads * cache->dim;
+  if ((rc = check_matrix(a->q, a->ldq, a->T, width, 2, "q"))) return rc;
+  if ((rc = check_matrix(a->out, a->ldo, a->T, width, 2, "out"))) return rc;
+  if (a->max_pages < 1 || (int64_t)a->max_pages * cache->page_size >= (int64_t(1) << 30))
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "max_pages=%d: a request holds 1 .. 2^30 - 1 tokens", a->max_pages);
+  if ((rc = check_table(a->page_table, a->ld_table, a->requests, a->max_pages, 4, "page_table"))) return rc;
+  if (!a->node_ptr || !a->ctx_len) return fail(W12_ERR_INVALID_ARG, "node_ptr or ctx_len is NULL");
+  if (!aligned(a->node_ptr, 4) || !aligned(a->ctx_len, 4))
+    return fail(W12_ERR_MISALIGNED, "node_ptr and ctx_len must be 4-byte aligned");
+  if (a->tree_mask) {
+    if (a->mask_words < 1 || a->mask_words > 64)
+      return fail(W12_ERR_UNSUPPORTED_SHAPE, "mask_words=%d outside 1..64", a->mask_words);
+    if ((rc = check_table(a->tree_mask, a->ld_mask, a->T, a->mask_words, 8, "tree_mask"))) return rc;
+  } else if (a->mask_words != 0) {
+    return fail(W12_ERR_INVALID_ARG, "mask_words without tree_mask");
+  }
+  if (a->lse && (rc = check_table(a->lse, a->ld_lse, a->T, a->q_heads, 4, "lse"))) return rc;
+  if (!(a->scale > 0.0f) || a->scale > 1e30f) return fail(W12_ERR_INVALID_ARG, "scale must be positive and finite");
+  const uint64_t need = w12::attention_workspace_bytes(a->T, a->requests, a->q_heads, *cache);
+  if (ws_bytes < need)
+    return fail(W12_ERR_WORKSPACE_TOO_SMALL, "workspace %llu bytes < %llu needed", (unsigned long long)ws_bytes,
+                (unsigned long long)need);
+  if (need && !ws) return fail(W12_ERR_INVALID_ARG, "ws is NULL");
+  if (ws && !aligned(ws, 16)) return fail(W12_ERR_MISALIGNED, "ws must be 16-byte aligned");
+  return hip_status(w12::launch_tree_attention(*a, *cache, ws, stream), "tree_attention");
+}
+
+int w12_gemm_e4m3_workspace_size(int32_t M, int32_t N, int32_t K, uint64_t* bytes) {
+  int rc = check_shape(N, K);
+  if (rc) return rc;
+  if (M < 1 || M > kMaxM) return fail(W12_ERR_UNSUPPORTED_SHAPE, "M=%d outside 1..%d", M, kMaxM);
+  if (!bytes) return fail(W12_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = w12::gemm_e4m3_workspace_bytes(M, N, K);
+  return ok();
+}
+
+int w12_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* x_scale, int64_t ldxs, const uint8_t* W,
+                  int32_t N, int32_t K, int64_t ldw, const float* w_scale, int64_t ldws, float* Y, int64_t ldy,
+                  void* ws, uint64_t ws_bytes, hipStream_t stream) {
+  int rc = check_shape(N, K);
+  if (rc) return rc;
+  if (M < 1 || M > kMaxM) return fail(W12_ERR_UNSUPPORTED_SHAPE, "M=%d outside 1..%d", M, kMaxM);
+  const int64_t kb = w12::ceil_div(K, W12_QUANT_BLOCK);
+  if ((rc = check_matrix(X, ldx, M, K, 1, "X"))) return rc;
+  if ((rc = check_matrix(W, ldw, N, K, 1, "W"))) return rc;
+  if ((rc = check_table(x_scale, ldxs, M, kb, 4, "x_scale"))) return rc;
+  if ((rc = check_table(w_scale, ldws, w12::ceil_div(N, W12_QUANT_BLOCK), kb, 4, "w_scale"))) return rc;
+  if ((rc = check_table(Y, ldy, M, N, 4, "Y"))) return rc;
+  // the kernels address each operand with 32-bit buffer offsets
+  if (((int64_t)M - 1) * ldx + K >= (int64_t(1) << 31))
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "X spans too many bytes for 31-bit buffer offsets");
+  if (((int64_t)N - 1) * ldw + K >= (int64_t(1) << 32) - 16)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "W spans too many bytes for 32-bit buffer offsets");
+  if (((int64_t)M - 1) * ldy + N >= (int64_t(1) << 29))
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "Y spans too many elements for 31-bit buffer offsets");
+  const uint64_t need = w12::gemm_e4m3_workspace_bytes(M, N, K);
+  if (ws_bytes < need)
+    return fail(W12_ERR_WORKSPACE_TOO_SMALL, "workspace %llu bytes < %llu needed", (unsigned long long)ws_bytes,
+                (unsigned long long)need);
+  if (need && !ws) return fail(W12_ERR_INVALID_ARG, "ws is NULL");
+  if (ws && !aligned(ws, 16)) return fail(W12_ERR_MISALIGNED, "ws must be 16-byte aligned");
+  return hip_status(w12::launch_gemm_e4m3(X, M, ldx, x_scale, ldxs, W, N, K, ldw, w_scale, ldws, Y, ldy, ws, stream),
+                    "gemm_e4m3");
+}
+
 double w12_bits_per_weight(int32_t N, int32_t K, int64_t E) {
   if (N < 1 || K < 1 || E < 0) return -1.0;
   const double nk = (double)N * (double)K;

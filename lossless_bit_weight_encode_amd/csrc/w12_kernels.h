@@ -79,6 +79,16 @@ hipError_t timeline_copy(void* host, uint64_t bytes);
 hipError_t launch_read_probe(const void* buf, uint64_t bytes, int32_t loads_per_lane, int64_t grid, uint32_t* sink,
                              hipStream_t stream);
 
+// Operators around the products (w12_norm.hip, w12_rope.hip, w12_attention.hip, w12_gemm_e4m3.hip).
+hipError_t launch_add_rmsnorm(const w12_norm_args& a, hipStream_t stream);
+hipError_t launch_rope_append(const w12_rope_args& a, const w12_kv_cache& c, hipStream_t stream);
+uint64_t attention_workspace_bytes(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache& c);
+hipError_t launch_tree_attention(const w12_attention_args& a, const w12_kv_cache& c, void* ws, hipStream_t stream);
+uint64_t gemm_e4m3_workspace_bytes(int32_t M, int32_t N, int32_t K);
+hipError_t launch_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* xs, int64_t ldxs, const uint8_t* W,
+                            int32_t N, int32_t K, int64_t ldw, const float* wsc, int64_t ldws, float* Y, int64_t ldy,
+                            void* ws, hipStream_t stream);
+
 // Checkpoint files (host side; w12_file.cpp).  Return 0, -1 for an I/O or format error, -2
 // for a HIP error, with a message in err.
 uint64_t file_tensor_bytes(int32_t N, int32_t K, int64_t E);
