@@ -545,6 +545,8 @@ int w12_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* x_scale
   // the kernels address each operand with 32-bit buffer offsets
   if (((int64_t)M - 1) * ldx + K >= (int64_t(1) << 31))
     return fail(W12_ERR_UNSUPPORTED_SHAPE, "X spans too many bytes for 31-bit buffer offsets");
+  if (((int64_t)M - 1) * ldxs + kb >= (int64_t(1) << 29))
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "x_scale spans too many elements for 31-bit buffer offsets");
   if (((int64_t)N - 1) * ldw + K >= (int64_t(1) << 32) - 16)
     return fail(W12_ERR_UNSUPPORTED_SHAPE, "W spans too many bytes for 32-bit buffer offsets");
   if (((int64_t)M - 1) * ldy + N >= (int64_t(1) << 29))

@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
     s.fetch(first);
     s.look_up(first + 1);
     s.put(first, 0);
-    __syncthreads();
+    lds_barrier();
     for (int tile = first; tile < last; ++tile) {
       const int buf = (tile - first) & 1;
       const bool more = tile + 1 < last;
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
         else attend<D, F8, 1>(s, x, tile, buf, half, row, node, scale);
       }
       if (more) s.put(tile + 1, buf ^ 1);
-      __syncthreads();
+      lds_barrier();
     }
 
     {

@@ -64,6 +64,10 @@ __device__ __forceinline__ void wait_lgkm() { asm volatile("s_waitcnt lgkmcnt(0)
 // every buffer-to-LDS load in flight); LDS writes are waited for explicitly before it.
 __device__ __forceinline__ void barrier() { __builtin_amdgcn_s_barrier(); }
 
+// A barrier for what waves put into LDS: this wave's LDS accesses are complete, the loads from
+// memory that it has in flight stay so (__syncthreads would wait for them).
+__device__ __forceinline__ void lds_barrier() { asm volatile("s_waitcnt lgkmcnt(0)\ns_barrier" ::: "memory"); }
+
 __device__ __forceinline__ uint4 lds_read_u128(uint32_t a) {
   uint4 v;
   asm volatile("ds_read_b128 %0, %1\ns_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(a) : "memory");

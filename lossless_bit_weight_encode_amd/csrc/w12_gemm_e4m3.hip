@@ -8,9 +8,10 @@
 // A work-group takes tiles of BN channels x BM rows of X; their steps, end to end, are cut into equal
 // shares, one a work-group (so few tiles of a long k fill the chip).  The work-groups of a tile leave
 // FP32 partial tiles, and the last one to arrive adds them in the order of the work-groups (bitwise the
-// same every time).  Operands go global -> registers (DEPTH steps ahead) -> LDS (double-buffered): W as it is,
-// X widened to BF16 once for all waves; 16-byte pieces are swizzled by row so that the operand
-// reads, 32 rows of one piece, meet every bank equally.
+// same every time).  Operands are loaded into registers DEPTH steps ahead.  Tiles of more than 32 rows pass
+// them through LDS (double-buffered; W as it is, X widened to BF16 once for all waves), their pieces
+// swizzled by row so that the operand reads, 32 rows of one piece, meet every bank equally.  Tiles of up
+// to 32 rows load straight into operand registers: a wave's W is nobody else's, and no wave waits for another.
 #include "w12_device.h"
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
@@ -22,7 +23,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4e __attribute__((ext_vector_type(4)));
 
 constexpr int kStepK = 128;
-constexpr uint32_t kPastEnd = 0xFFFFFFF0u;   // a buffer offset past any operand: reads give 0
 
 // Eight E4M3 bytes to BF16.
 __device__ __forceinline__ uint4 widen8(uint32_t lo, uint32_t hi) {
@@ -49,36 +49,42 @@ struct E4m3Args {
   float* Y;
   uint32_t* counters;
   float* parts;
-  uint32_t ldx, ldw, x_bytes, w_bytes;
-  int64_t ldxs, ldws, ldy;
+  uint32_t ldx, ldw, ldxs, x_bytes, w_bytes, xs_bytes;
+  int64_t ldws, ldy;
   int M, N, K, steps, m_tiles;
   int64_t total, share;    // steps of all tiles, and of a share
   uint32_t part_bytes;
 };
 
-// WN x WM waves of NB x MB blocks of 32 channels x 32 rows.
-template <int WN, int WM, int NB, int MB, int DEPTH, int PER_CU>
+// WN x WM waves of NB x MB blocks of 32 channels x 32 rows; LDS: operands through LDS.
+template <int WN_, int WM_, int NB_, int MB_, int DEPTH, int PER_CU, bool LDS>
 struct E4m3Cfg {
+  static constexpr int WN = WN_, WM = WM_, NB = NB_, MB = MB_, kDepth = DEPTH, kPerCu = PER_CU;
+  static constexpr bool kLds = LDS;
   static constexpr int kWaves = WN * WM, kThreads = kWaves * 64;
   static constexpr int kBN = WN * NB * 32, kBM = WM * MB * 32;
-  static constexpr int kWPieces = kBN * 8 / kThreads, kXPieces = kBM * 8 / kThreads;   // loads of a thread a step
-  static constexpr int kPart = kBN * kBM;                                              // floats of a partial tile
-  static constexpr int kDepth = DEPTH, kPerCu = PER_CU;
-  static_assert(kWPieces >= 1 && kXPieces >= 1, "every thread loads");
+  static constexpr int kWPieces = LDS ? kBN * 8 / kThreads : NB * 4;     // loads of a thread a step
+  static constexpr int kXPieces = LDS ? kBM * 8 / kThreads : MB * 4;
+  static constexpr int kPart = kBN * kBM;                                // floats of a partial tile
   static constexpr int kWavesPerSimd = kWaves * PER_CU / 4;
+  static_assert(kWPieces >= 1 && kXPieces >= 1 && (LDS || DEPTH >= 2), "every thread loads; a slot is free before it is filled");
 };
 
-template <typename C, int WN, int WM, int NB, int MB>
+template <typename C>
 __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m3Args g) {
-  __shared__ uint4 lw[2][C::kBN * 8];
-  __shared__ uint4 lx[2][C::kBM * 16];
+  constexpr int NB = C::NB, MB = C::MB, DEPTH = C::kDepth;
+  __shared__ uint4 lw[C::kLds ? 2 : 1][C::kLds ? C::kBN * 8 : 1];
+  __shared__ uint4 lx[C::kLds ? 2 : 1][C::kLds ? C::kBM * 16 : 1];
   __shared__ uint32_t s_last;
   const int t = threadIdx.x, lane = t & 63, wave = wave_id(), col = lane & 31, hi = lane >> 5;
-  const int wn = wave % WN, wm = wave / WN;
-  const int piece = t & 7, prow = t >> 3;
+  const int wn = wave % C::WN, wm = wave / C::WN;
+  const int piece = t & 7, prow = t >> 3;      // this thread's part of the operands on their way to LDS
   constexpr int kRowsStep = C::kThreads / 8;
   const __amdgpu_buffer_rsrc_t rw = make_rsrc(g.W, g.w_bytes), rx = make_rsrc(g.X, g.x_bytes);
-  const __amdgpu_buffer_rsrc_t rp = make_rsrc(g.parts, g.part_bytes);
+  const __amdgpu_buffer_rsrc_t rp = make_rsrc(g.parts, g.part_bytes), rs = make_rsrc(g.xs, g.xs_bytes);
+  // where this lane's operands are in LDS: its row, the piece that the swizzle gives k = 0
+  const uint32_t wbase = (uint32_t)((wn * NB * 32 + col) * 128 + ((hi ^ (col >> 1 & 7)) * 16));
+  const uint32_t xbase = (uint32_t)((wm * MB * 32 + col) * 256 + (((2 * hi) ^ (col & 15)) * 16));
   const int64_t me = logical_wg(blockIdx.x, gridDim.x);
   const int64_t r0 = me * g.share, r1 = min(r0 + g.share, g.total);
   int64_t at = r0;
@@ -88,44 +94,68 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
     at = c0 + last;
     const int n0 = (int)(tile / g.m_tiles) * C::kBN, m0 = (int)(tile % g.m_tiles) * C::kBM;
 
-    uint32_t woff[C::kWPieces], xoff[C::kXPieces];
+    // Byte offsets of this thread's pieces (rows past the end take the last row, whose results are not
+    // stored), and of the scales of this lane's rows of X.
+    uint32_t woff[C::kLds ? C::kWPieces : NB], xoff[C::kLds ? C::kXPieces : MB], xsoff[MB];
+    if constexpr (C::kLds) {
 #pragma unroll
-    for (int i = 0; i < C::kWPieces; ++i) {
-      const int n = n0 + prow + i * kRowsStep;
-      woff[i] = n < g.N ? (uint32_t)n * g.ldw : kPastEnd;
+      for (int i = 0; i < C::kWPieces; ++i) woff[i] = (uint32_t)min(n0 + prow + i * kRowsStep, g.N - 1) * g.ldw + piece * 16;
+#pragma unroll
+      for (int i = 0; i < C::kXPieces; ++i) xoff[i] = (uint32_t)min(m0 + prow + i * kRowsStep, g.M - 1) * g.ldx + piece * 16;
+    } else {
+#pragma unroll
+      for (int a = 0; a < NB; ++a) woff[a] = (uint32_t)min(n0 + (wn * NB + a) * 32 + col, g.N - 1) * g.ldw + hi * 16;
+#pragma unroll
+      for (int b = 0; b < MB; ++b) xoff[b] = (uint32_t)min(m0 + (wm * MB + b) * 32 + col, g.M - 1) * g.ldx + hi * 16;
     }
 #pragma unroll
-    for (int i = 0; i < C::kXPieces; ++i) {
-      const int m = m0 + prow + i * kRowsStep;
-      xoff[i] = m < g.M ? (uint32_t)m * g.ldx : kPastEnd;
-    }
-    uint4 wreg[C::kDepth][C::kWPieces], xreg[C::kDepth][C::kXPieces];
-    auto fetch = [&](int step, uint4* w, uint4* x) {
-      const int k = step * kStepK + piece * 16;
-      const bool in = step < last && k < g.K;
+    for (int b = 0; b < MB; ++b) xsoff[b] = (uint32_t)min(m0 + (wm * MB + b) * 32 + col, g.M - 1) * g.ldxs;
+    const bool wave_on = m0 + wm * MB * 32 < g.M && n0 + wn * NB * 32 < g.N;
+    const float* wrow = g.wsc + (int64_t)(min(n0 + wn * NB * 32, g.N - 1) / W12_QUANT_BLOCK) * g.ldws;
+
+    // Operands on their way.  Straight to operand registers, piece j of a lane is k = 16 (2 j + hi) .. + 15 of
+    // the step.  Pieces past the end of a row (in the last step) hold what follows it; they are cleared before use.
+    uint4 wreg[DEPTH][C::kWPieces], xreg[DEPTH][C::kXPieces];
+    float sreg[DEPTH][MB + 1];
+    auto fetch = [&](int step, int d) {
+      const int st = min(step, last - 1);
+      const uint32_t k = (uint32_t)(st * kStepK);
 #pragma unroll
-      for (int i = 0; i < C::kWPieces; ++i) w[i] = bload16(rw, in && woff[i] != kPastEnd ? woff[i] + (uint32_t)k : kPastEnd);
+      for (int i = 0; i < C::kWPieces; ++i)
+        wreg[d][i] = C::kLds ? bload16(rw, woff[i] + k) : bload16(rw, woff[i / 4] + k + 32 * (i % 4));
 #pragma unroll
-      for (int i = 0; i < C::kXPieces; ++i) x[i] = bload16(rx, in && xoff[i] != kPastEnd ? xoff[i] + (uint32_t)k : kPastEnd);
+      for (int i = 0; i < C::kXPieces; ++i)
+        xreg[d][i] = C::kLds ? bload16(rx, xoff[i] + k) : bload16(rx, xoff[i / 4] + k + 32 * (i % 4));
     };
-    auto put = [&](int step, int buf, uint4* w, uint4* x) {
-      const int left = g.K - step * kStepK - piece * 16;      // bytes of this piece that belong to the row
-      if ((step + 1) * kStepK > g.K) {
+    // The scales travel ahead as well: loaded when they are needed, they would wait for every load before them.
+    auto fetch_scales = [&](int step, int d) {
+      const int st = min(step, last - 1);
 #pragma unroll
-        for (int i = 0; i < C::kWPieces; ++i) w[i] = first_bytes(w[i], left);
+      for (int b = 0; b < MB; ++b)
+        sreg[d][b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (int)((xsoff[b] + (uint32_t)st) * 4u), 0, 0));
+      sreg[d][MB] = wrow[st];
+    };
+    // What does not belong to the row, in the last step of a k that is no multiple of 128: zeros.
+    auto clear_tail = [&](int d) {
+      const int end = g.K - (g.steps - 1) * kStepK;
 #pragma unroll
-        for (int i = 0; i < C::kXPieces; ++i) x[i] = first_bytes(x[i], left);
-      }
+      for (int i = 0; i < C::kWPieces; ++i)
+        wreg[d][i] = first_bytes(wreg[d][i], end - 16 * (C::kLds ? piece : 2 * (i % 4) + hi));
+#pragma unroll
+      for (int i = 0; i < C::kXPieces; ++i)
+        xreg[d][i] = first_bytes(xreg[d][i], end - 16 * (C::kLds ? piece : 2 * (i % 4) + hi));
+    };
+    auto put = [&](int buf, int d) {
 #pragma unroll
       for (int i = 0; i < C::kWPieces; ++i) {
         const int r = prow + i * kRowsStep;
-        lw[buf][r * 8 + (piece ^ (r & 7))] = w[i];
+        lw[buf][r * 8 + (piece ^ (r >> 1 & 7))] = wreg[d][i];
       }
 #pragma unroll
       for (int i = 0; i < C::kXPieces; ++i) {
         const int r = prow + i * kRowsStep;
-        lx[buf][r * 16 + ((2 * piece) ^ (r & 15))] = widen8(x[i].x, x[i].y);
-        lx[buf][r * 16 + ((2 * piece + 1) ^ (r & 15))] = widen8(x[i].z, x[i].w);
+        lx[buf][r * 16 + ((2 * piece) ^ (r & 15))] = widen8(xreg[d][i].x, xreg[d][i].y);
+        lx[buf][r * 16 + ((2 * piece + 1) ^ (r & 15))] = widen8(xreg[d][i].z, xreg[d][i].w);
       }
     };
 
@@ -136,18 +166,8 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
       for (int b = 0; b < MB; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
-    const bool wave_on = m0 + wm * MB * 32 < g.M && n0 + wn * NB * 32 < g.N;
-    const int nblk = (n0 + wn * NB * 32) / W12_QUANT_BLOCK;
-    const float* xrow[MB];
-#pragma unroll
-    for (int b = 0; b < MB; ++b) xrow[b] = g.xs + (int64_t)min(m0 + (wm * MB + b) * 32 + col, g.M - 1) * g.ldxs;
-    const float* wrow = g.wsc + nblk * g.ldws;
 
-    auto compute = [&](int step, int buf) {
-      float sc[MB];
-      const float ws = wrow[step];
-#pragma unroll
-      for (int b = 0; b < MB; ++b) sc[b] = xrow[b][step] * ws;
+    auto compute = [&](int buf, int d) {
       f32x16 part[NB][MB];
 #pragma unroll
       for (int a = 0; a < NB; ++a)
@@ -155,30 +175,43 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
         for (int b = 0; b < MB; ++b)
 #pragma unroll
           for (int i = 0; i < 16; ++i) part[a][b][i] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        // this lane's k: 16 from 16 (2 j + hi), in two instructions of 8
-        uint4 w[NB];
-#pragma unroll
-        for (int a = 0; a < NB; ++a) {
-          const int r = (wn * NB + a) * 32 + col;
-          w[a] = lw[buf][r * 8 + ((2 * j + hi) ^ (r & 7))];
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint4 x[MB];
-#pragma unroll
-          for (int b = 0; b < MB; ++b) {
-            const int r = (wm * MB + b) * 32 + col;
-            x[b] = lx[buf][r * 16 + ((2 * (2 * j + hi) + e) ^ (r & 15))];
-          }
+      // Eight instructions of 16 k a block; instruction 2 j + e takes half e of piece j.  Operands are read from
+      // LDS kAhead of them before their use (left to itself the compiler reads them right before it).
+      constexpr int kAhead = C::kLds ? (NB * MB >= 4 ? 1 : 2) : 0;
+      uint4 w[2][NB], x[kAhead + 1][MB];
+      auto operands = [&](int i) {
+        const int j = i / 2, e = i % 2;
+        if (e == 0) {
 #pragma unroll
           for (int a = 0; a < NB; ++a) {
-            const bf16x8 wb = __builtin_bit_cast(bf16x8, e ? widen8(w[a].z, w[a].w) : widen8(w[a].x, w[a].y));
-#pragma unroll
-            for (int b = 0; b < MB; ++b)
-              part[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb, __builtin_bit_cast(bf16x8, x[b]), part[a][b], 0, 0, 0);
+            if constexpr (C::kLds)
+              w[j % 2][a] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(lw[buf]) + (wbase ^ (32u * j)) + a * 32 * 128);
+            else
+              w[j % 2][a] = wreg[d][a * 4 + j];
           }
+        }
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          if constexpr (C::kLds)
+            x[i % (kAhead + 1)][b] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(lx[buf]) +
+                                                                      (xbase ^ (64u * j + 16u * e)) + b * 32 * 256);
+          else
+            x[0][b] = e ? widen8(xreg[d][b * 4 + j].z, xreg[d][b * 4 + j].w) : widen8(xreg[d][b * 4 + j].x, xreg[d][b * 4 + j].y);
+        }
+      };
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) operands(i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i + kAhead < 8) operands(i + kAhead);
+        if constexpr (C::kLds) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int a = 0; a < NB; ++a) {
+          const uint4 u = w[i / 2 % 2][a];
+          const bf16x8 wb = __builtin_bit_cast(bf16x8, i % 2 ? widen8(u.z, u.w) : widen8(u.x, u.y));
+#pragma unroll
+          for (int b = 0; b < MB; ++b)
+            part[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb, __builtin_bit_cast(bf16x8, x[i % (kAhead + 1)][b]), part[a][b], 0, 0, 0);
         }
       }
 #pragma unroll
@@ -186,106 +219,165 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
 #pragma unroll
         for (int b = 0; b < MB; ++b)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) acc[a][b][i] += part[a][b][i] * sc[b];
+          for (int i = 0; i < 16; ++i) acc[a][b][i] += part[a][b][i] * (sreg[d][b] * sreg[d][MB]);
     };
 
-    constexpr int DEPTH = C::kDepth;
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) fetch(first + d, wreg[d], xreg[d]);
-    put(first, 0, wreg[0], xreg[0]);
-    fetch(first + DEPTH, wreg[0], xreg[0]);
-    __syncthreads();
-    // step s is computed from buffer (s - first) % 2 while step s + 1 goes from its registers into the other
-    for (int s0 = first; s0 < last; s0 += 2 * DEPTH) {
+    for (int d = 0; d < DEPTH; ++d) {
+      fetch(first + d, d);
+      fetch_scales(first + d, d);
+    }
+    if constexpr (C::kLds) {
+      put(0, 0);
+      fetch(first + DEPTH, 0);
+      lds_barrier();
+    }
+    // Step s goes through the registers of slot (s - first) % DEPTH and, with LDS, buffer (s - first) % 2, into
+    // which it is put while step s - 1 is computed.  Only the computing is skipped past the last whole step, and
+    // a step that k ends in is taken by itself below: where paths meet that a fetch or its use was on one of,
+    // the compiler waits for more than is needed.
+    constexpr int kTurn = DEPTH % 2 ? 2 * DEPTH : DEPTH;
+    const bool tail = last * kStepK > g.K;
+    const int whole = last - tail;
+    for (int s0 = first; s0 < whole; s0 += kTurn) {
 #pragma unroll
-      for (int d = 0; d < 2 * DEPTH; ++d) {
-        const int step = s0 + d;
-        if (step < last) {
-          if (wave_on) compute(step, d & 1);
-          if (step + 1 < last) {
-            put(step + 1, (d + 1) & 1, wreg[(d + 1) % DEPTH], xreg[(d + 1) % DEPTH]);
-            fetch(step + 1 + DEPTH, wreg[(d + 1) % DEPTH], xreg[(d + 1) % DEPTH]);
-          }
-          __syncthreads();
+      for (int i = 0; i < kTurn; ++i) {
+        const int d = i % DEPTH, next = (i + 1) % DEPTH, step = s0 + i;
+        if (wave_on && step < whole) compute(i & 1, d);
+        if constexpr (C::kLds) {
+          put((i + 1) & 1, next);
+          fetch(step + 1 + DEPTH, next);
+          fetch_scales(step + DEPTH, d);
+          lds_barrier();
+        } else {
+          fetch(step + DEPTH, d);
+          fetch_scales(step + DEPTH, d);
         }
       }
     }
+    if (tail) {
+      fetch(whole, 0);
+      fetch_scales(whole, 0);
+      clear_tail(0);
+      if constexpr (C::kLds) {
+        put(0, 0);
+        lds_barrier();
+      }
+      if (wave_on) compute(0, 0);
+      if constexpr (C::kLds) lds_barrier();      // the next tile goes to the same buffers
+    }
 
-    const bool whole = first == 0 && last == g.steps;
-    bool store = whole;
-    if (!whole) {
-      // partial tile [float4][lane] of each wave; device-coherent (sc1), as its reader may be on another XCD
-      const uint32_t wbase = (uint32_t)wave * NB * MB * 4 * 64 * 16 + (uint32_t)lane * 16;
+    const int rows = min(g.M - m0, C::kBM), cols = min(g.N - n0, C::kBN);
+    const bool vec = (g.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(g.Y) & 15) == 0;
+    auto store_y = [&](int m, int n, const float v[4]) {      // four channels of a row of the tile
+      float* y = g.Y + (m0 + m) * g.ldy + n0 + n;
+      if (vec && n + 4 <= cols) {
+        *reinterpret_cast<float4*>(y) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (n + i < cols) y[i] = v[i];
+      }
+    };
+    if (first == 0 && last == g.steps) {
       if (wave_on) {
-        const uint32_t base = (uint32_t)((2 * me + (c0 > r0)) * (C::kPart * 4)) + wbase;
-#pragma unroll
-        for (int a = 0; a < NB; ++a)
-#pragma unroll
-          for (int b = 0; b < MB; ++b)
-            if (m0 + (wm * MB + b) * 32 + col < g.M) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const u32x4e v = {__float_as_uint(acc[a][b][4 * q]), __float_as_uint(acc[a][b][4 * q + 1]),
-                                  __float_as_uint(acc[a][b][4 * q + 2]), __float_as_uint(acc[a][b][4 * q + 3])};
-                __builtin_amdgcn_raw_buffer_store_b128(v, rp, (int)(base + (uint32_t)((a * MB + b) * 4 + q) * 1024u), 0,
-                                                       kCachePolicySc1);
-              }
-            }
-      }
-      wait_vm_all();      // the stores of this wave are complete
-      __syncthreads();
-      const int64_t g0 = c0 / g.share, g1 = (c0 + g.steps - 1) / g.share;
-      if (t == 0) {
-        const uint32_t prev = __hip_atomic_fetch_add(g.counters + g0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = prev == (uint32_t)(g1 - g0);
-        if (s_last) __hip_atomic_store(g.counters + g0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      __syncthreads();
-      store = s_last != 0;
-      __syncthreads();    // s_last may be written again
-      if (store && wave_on) {
 #pragma unroll
         for (int a = 0; a < NB; ++a)
 #pragma unroll
           for (int b = 0; b < MB; ++b) {
-            if (m0 + (wm * MB + b) * 32 + col >= g.M) continue;
+            const int m = (wm * MB + b) * 32 + col;
+            if (m >= rows) continue;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
-            for (int64_t p = g0; p <= g1; ++p) {
-              const uint32_t base = (uint32_t)((2 * p + (c0 > p * g.share)) * (C::kPart * 4)) + wbase;
-              f32x4 v[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                v[q] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     rp, (int)(base + (uint32_t)((a * MB + b) * 4 + q) * 1024u), 0, kCachePolicySc1));
-#pragma unroll
-              for (int i = 0; i < 16; ++i) acc[a][b][i] += v[i >> 2][i & 3];
+            for (int q = 0; q < 4; ++q) {
+              const float v[4] = {acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+              store_y(m, (wn * NB + a) * 32 + 8 * q + 4 * hi, v);
             }
           }
       }
+      continue;
     }
-    if (store && wave_on) {
-      const bool vec = (g.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(g.Y) & 15) == 0;
+    // A partial tile, device-coherent (sc1), as its reader may be on another XCD.  Tiles of up to 32 rows
+    // are laid out [row of X][channel], so that every thread adds (one row has few places, and many parts);
+    // the others [wave][float4][lane], whole lines a store, and a lane adds what it holds.
+    const uint32_t lane_part = (uint32_t)(wave * NB * MB * 4 * 64 + lane) * 16u;
+    if (wave_on) {
+      const uint32_t base = (uint32_t)((2 * me + (c0 > r0)) * (C::kPart * 4));
 #pragma unroll
       for (int a = 0; a < NB; ++a)
 #pragma unroll
         for (int b = 0; b < MB; ++b) {
-          const int m = m0 + (wm * MB + b) * 32 + col;
-          if (m >= g.M) continue;
-          float* y = g.Y + m * g.ldy;
+          const int m = (wm * MB + b) * 32 + col;
+          if (m >= rows) continue;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const int n = n0 + (wn * NB + a) * 32 + 8 * q + 4 * hi;
-            if (vec && n + 4 <= g.N) {
-              *reinterpret_cast<float4*>(y + n) =
-                  make_float4(acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (n + i < g.N) y[n + i] = acc[a][b][4 * q + i];
-            }
+            const u32x4e v = {__float_as_uint(acc[a][b][4 * q]), __float_as_uint(acc[a][b][4 * q + 1]),
+                              __float_as_uint(acc[a][b][4 * q + 2]), __float_as_uint(acc[a][b][4 * q + 3])};
+            const uint32_t off = C::kLds ? lane_part + (uint32_t)((a * MB + b) * 4 + q) * 1024u
+                                         : (uint32_t)(m * C::kBN + (wn * NB + a) * 32 + 8 * q + 4 * hi) * 4u;
+            __builtin_amdgcn_raw_buffer_store_b128(v, rp, (int)(base + off), 0, kCachePolicySc1);
           }
         }
+    }
+    wait_vm_all();      // the stores of this wave are complete
+    __syncthreads();
+    const int64_t g0 = c0 / g.share, g1 = (c0 + g.steps - 1) / g.share;
+    if (t == 0) {
+      // the tile's counter is its first work-group's
+      const uint32_t prev = __hip_atomic_fetch_add(g.counters + g0, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      s_last = prev == (uint32_t)(g1 - g0);
+      if (s_last) __hip_atomic_store(g.counters + g0, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    const bool mine = s_last != 0;
+    __syncthreads();    // s_last may be written again
+    if (!mine) continue;
+    const int parts = (int)(g1 - g0) + 1;
+    const uint32_t base0 = (uint32_t)((2 * g0 + (c0 > g0 * g.share)) * (C::kPart * 4));
+    auto load_part = [&](int p, uint32_t off) {      // the tile is the first that the later work-groups hold
+      const uint32_t base = p == 0 ? base0 : (uint32_t)(2 * (g0 + p) * (C::kPart * 4));
+      return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rp, (int)(base + off), 0, kCachePolicySc1));
+    };
+    if constexpr (C::kLds) {
+      if (!wave_on) continue;
+#pragma unroll
+      for (int a = 0; a < NB; ++a)
+#pragma unroll
+        for (int b = 0; b < MB; ++b) {
+          const int m = (wm * MB + b) * 32 + col;
+          if (m >= rows) continue;
+          f32x4 sum[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) sum[q] = load_part(0, lane_part + (uint32_t)((a * MB + b) * 4 + q) * 1024u);
+          for (int p = 1; p < parts; ++p) {
+            f32x4 v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = load_part(p, lane_part + (uint32_t)((a * MB + b) * 4 + q) * 1024u);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) sum[q] += v[q];
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float v[4] = {sum[q][0], sum[q][1], sum[q][2], sum[q][3]};
+            store_y(m, (wn * NB + a) * 32 + 8 * q + 4 * hi, v);
+          }
+        }
+    } else {
+      const int quads = (cols + 3) / 4;
+      for (int i = t; i < quads * rows; i += C::kThreads) {
+        const int m = i / quads, n = i % quads * 4;
+        const uint32_t off = (uint32_t)(m * C::kBN + n) * 4u;
+        f32x4 sum = {0, 0, 0, 0};
+        for (int p = 0; p < parts; p += 8) {      // eight parts in flight
+          f32x4 v[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) v[u] = load_part(min(p + u, parts - 1), off);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (p + u < parts) sum += v[u];
+        }
+        const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+        store_y(m, n, v);
+      }
     }
   }
 }
@@ -296,9 +388,9 @@ struct E4m3Plan {
   uint64_t part_bytes;
 };
 
-using E4m3Rows32 = E4m3Cfg<4, 1, 1, 1, 3, 3>;
-using E4m3Rows64 = E4m3Cfg<4, 1, 1, 2, 2, 2>;
-using E4m3Rows128 = E4m3Cfg<4, 2, 2, 2, 1, 1>;
+using E4m3Rows32 = E4m3Cfg<4, 1, 2, 1, 2, 2, false>;
+using E4m3Rows64 = E4m3Cfg<8, 1, 1, 2, 2, 1, true>;
+using E4m3Rows128 = E4m3Cfg<4, 2, 2, 2, 1, 1, true>;
 
 template <typename C>
 static void plan_with(E4m3Plan& p, int M, int N) {
@@ -308,7 +400,6 @@ static void plan_with(E4m3Plan& p, int M, int N) {
   const int64_t slots = (int64_t)device_cus() * C::kPerCu;
   p.share = ceil_div(p.total, slots);
   if (p.share < 4) p.share = 4 < p.steps ? 4 : p.steps;
-  if (C::kBM < 128 && 2 * p.share > p.steps) p.share = ceil_div(p.share, p.steps) * p.steps;
   p.groups = ceil_div(p.total, p.share);
   p.part_bytes = p.share % p.steps ? (uint64_t)(2 * p.groups) * C::kPart * 4 : 0;
 }
@@ -344,7 +435,8 @@ hipError_t launch_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const floa
   g.ldw = (uint32_t)ldw;
   g.x_bytes = (uint32_t)(ceil_div((M - 1) * ldx + K, 16) * 16);
   g.w_bytes = (uint32_t)(ceil_div((N - 1) * ldw + K, 16) * 16);
-  g.ldxs = ldxs;
+  g.ldxs = (uint32_t)ldxs;
+  g.xs_bytes = (uint32_t)(((M - 1) * ldxs + ceil_div(K, W12_QUANT_BLOCK)) * 4);
   g.ldws = ldws;
   g.ldy = ldy;
   g.M = M;
@@ -356,9 +448,9 @@ hipError_t launch_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const floa
   g.share = p.share;
   g.part_bytes = (uint32_t)p.part_bytes;
   const dim3 grid((unsigned)p.groups);
-  if (p.path == 32) hipLaunchKernelGGL((k_gemm_e4m3<E4m3Rows32, 4, 1, 1, 1>), grid, dim3(E4m3Rows32::kThreads), 0, stream, g);
-  else if (p.path == 64) hipLaunchKernelGGL((k_gemm_e4m3<E4m3Rows64, 4, 1, 1, 2>), grid, dim3(E4m3Rows64::kThreads), 0, stream, g);
-  else hipLaunchKernelGGL((k_gemm_e4m3<E4m3Rows128, 4, 2, 2, 2>), grid, dim3(E4m3Rows128::kThreads), 0, stream, g);
+  if (p.path == 32) hipLaunchKernelGGL(k_gemm_e4m3<E4m3Rows32>, grid, dim3(E4m3Rows32::kThreads), 0, stream, g);
+  else if (p.path == 64) hipLaunchKernelGGL(k_gemm_e4m3<E4m3Rows64>, grid, dim3(E4m3Rows64::kThreads), 0, stream, g);
+  else hipLaunchKernelGGL(k_gemm_e4m3<E4m3Rows128>, grid, dim3(E4m3Rows128::kThreads), 0, stream, g);
   return hipGetLastError();
 }
 
