@@ -644,3 +644,11 @@ def test_operators_in_a_graph():
         torch.cuda.synchronize()
         assert torch.equal(got, out) and torch.equal(gq, qkv), f"replay {i} differs from the eager step"
         assert got.isfinite().all() and got.abs().max() > 0
+
+
+@pytest.mark.parametrize("ctx,n,hq,d,f8", [(0, 64, 5, 128, False), (100, 63, 5, 128, False), (40, 50, 1, 64, True), (7, 33, 3, 256, False)])
+def test_attention_rows_that_attend_one_drafted_token(ctx, n, hq, d, f8):
+    """Every place of a tile is some row's only drafted token (and with ctx 0 its only token)."""
+    p = Problem([ctx], [n], hq, 1, d, page=64, f8=f8, seed=60 + n)
+    p.mask = mask_tensor([1 << ((7 * i + 3) % n) for i in range(n)], 1)
+    p.check(*p.run())
