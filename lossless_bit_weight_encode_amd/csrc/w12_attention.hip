@@ -29,7 +29,9 @@
 namespace w12 {
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4a __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kAttnThreads = 256;
@@ -180,7 +182,7 @@ struct Tile {
 // LDS: K and V of two tiles, and per tile and token whether it is there.
 template <int D>
 struct Lds {
-  uint4 kv[2][2][kTile * D / 8];
+  u32x4a kv[2][2][kTile * D / 8];
   uint8_t there[2][kTile];
   uint32_t bad;        // drafted tokens of this segment had values that are infinite or NaN
   int64_t before[kMaxRequests + 1];
@@ -189,25 +191,19 @@ struct Lds {
 
 // Whether one of a piece's values is infinite or NaN: an exponent of ones (BF16), all bits but the sign (E4M3).
 // Such a field is the only one that a carry leaves when 1 is added at its foot.
-__device__ __forceinline__ uint32_t carries_bf16(uint32_t w) { return ((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u; }
-__device__ __forceinline__ uint32_t carries_e4m3(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 template <bool F8>
-__device__ __forceinline__ bool not_finite(uint4 u) {
-  if constexpr (F8) return (carries_e4m3(u.x) | carries_e4m3(u.y) | carries_e4m3(u.z) | carries_e4m3(u.w)) != 0;
-  else return (carries_bf16(u.x) | carries_bf16(u.y) | carries_bf16(u.z) | carries_bf16(u.w)) != 0;
+__device__ __forceinline__ bool not_finite(u32x4a u) {
+  constexpr uint32_t field = F8 ? 0x7F7F7F7Fu : 0x7F807F80u, foot = F8 ? 0x01010101u : 0x00800080u, top = F8 ? 0x80808080u : 0x80008000u;
+  const u32x4a c = ((u & field) + foot) & top;
+  return (c[0] | c[1] | c[2] | c[3]) != 0;
 }
 
-// E4M3 to BF16: 16 bytes become two pieces.
-__device__ __forceinline__ void widen(uint4 u, uint4 out[2]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-  uint32_t r[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r[2 * i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, false));
-    r[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[i], 1.0f, true));
-  }
-  out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-  out[1] = make_uint4(r[4], r[5], r[6], r[7]);
+// E4M3 to BF16: 8 bytes.
+__device__ __forceinline__ u32x4a widen(uint32_t lo, uint32_t hi) {
+  return u32x4a{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false)),
+                __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true))};
 }
 
 // The tiles of a segment on their way from the cache to LDS.  WHOLE: a tile lies in one page (pages of 64
@@ -224,7 +220,7 @@ struct Stream {
   int page_bits, ctx, len;
   int64_t head_bytes;
   uint32_t off[WHOLE ? T::kPass : 1];
-  uint4 k[T::kPass], v[T::kPass];
+  u32x4a k[T::kPass], v[T::kPass];
   int page[WHOLE ? 1 : T::kPass];      // of the tile that is fetched next
   uint32_t there;                      // bit i: the token of pass i of the fetched tile is there
 
@@ -264,8 +260,8 @@ struct Stream {
       there = 0;
 #pragma unroll
       for (int i = 0; i < T::kPass; ++i) {
-        k[i] = *reinterpret_cast<const uint4*>(kp + off[i]);
-        v[i] = *reinterpret_cast<const uint4*>(vp + off[i]);
+        k[i] = *reinterpret_cast<const u32x4a*>(kp + off[i]);
+        v[i] = *reinterpret_cast<const u32x4a*>(vp + off[i]);
         there |= (in && tile * kTile + i * T::kRows + row() < len ? 1u : 0u) << i;
       }
     } else {
@@ -276,8 +272,8 @@ struct Stream {
         const bool in = (uint32_t)page[i] < (uint32_t)c.pages;
         const int64_t e = (int64_t)(in ? page[i] : 0) * c.page_stride + (int64_t)(token & (c.page_size - 1)) * c.token_stride;
         const int64_t at = e * (F8 ? 1 : 2) + head_bytes + piece() * 16;
-        k[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.k) + at);
-        v[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(c.v) + at);
+        k[i] = *reinterpret_cast<const u32x4a*>(static_cast<const char*>(c.k) + at);
+        v[i] = *reinterpret_cast<const u32x4a*>(static_cast<const char*>(c.v) + at);
         there |= (in && token < len ? 1u : 0u) << i;
       }
     }
@@ -287,35 +283,36 @@ struct Stream {
   // that are infinite or NaN, are taken out (a row that does not attend the token would meet them as
   // 0 * inf); the latter are marked, and added by add_bad_tokens to the rows that attend them.
   __device__ __forceinline__ void put(int tile, int buf) {
+    if ((tile + 1) * kTile > ctx) put_values<true>(tile, buf);
+    else put_values<false>(tile, buf);
+  }
+
+  template <bool DRAFTED>
+  __device__ __forceinline__ void put_values(int tile, int buf) {
 #pragma unroll
     for (int i = 0; i < T::kPass; ++i) {
       const int r = i * T::kRows + row();
       const bool in = there >> i & 1;
       if (piece() == 0) lds.there[buf][r] = in;
-      const uint32_t keep = in ? ~0u : 0u;
-      v[i] = make_uint4(v[i].x & keep, v[i].y & keep, v[i].z & keep, v[i].w & keep);
-      if ((tile + 1) * kTile > ctx) {
-        const bool bad = tile * kTile + r >= ctx && not_finite<F8>(v[i]);
+      uint32_t keep = in ? ~0u : 0u;
+      if constexpr (DRAFTED) {
+        const bool bad = in && tile * kTile + r >= ctx && not_finite<F8>(v[i]);
         const uint64_t mine = ((1ull << T::kSrc) - 1) << ((threadIdx.x & 63) / T::kSrc * T::kSrc);
-        if (__ballot(bad) & mine) {
-          v[i] = make_uint4(0, 0, 0, 0);
-          lds.bad = 1;
-        }
+        const uint64_t any = __ballot(bad);
+        if (any) lds.bad = 1;
+        keep = any & mine ? 0u : keep;
       }
-      uint4* const kd = lds.kv[buf][0] + r * T::kPieces;
-      uint4* const vd = lds.kv[buf][1] + r * T::kPieces;
+      const u32x4a kept = v[i] & keep;
+      u32x4a* const kd = lds.kv[buf][0] + r * T::kPieces;
+      u32x4a* const vd = lds.kv[buf][1] + r * T::kPieces;
       if constexpr (F8) {
-        uint4 k2[2], v2[2];
-        widen(k[i], k2);
-        widen(v[i], v2);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          kd[(2 * piece() + j) ^ T::k_swizzle(r)] = k2[j];
-          vd[(2 * piece() + j) ^ T::v_swizzle(r)] = v2[j];
-        }
+        kd[(2 * piece()) ^ T::k_swizzle(r)] = widen(k[i][0], k[i][1]);
+        kd[(2 * piece() + 1) ^ T::k_swizzle(r)] = widen(k[i][2], k[i][3]);
+        vd[(2 * piece()) ^ T::v_swizzle(r)] = widen(kept[0], kept[1]);
+        vd[(2 * piece() + 1) ^ T::v_swizzle(r)] = widen(kept[2], kept[3]);
       } else {
         kd[piece() ^ T::k_swizzle(r)] = k[i];
-        vd[piece() ^ T::v_swizzle(r)] = v[i];
+        vd[piece() ^ T::v_swizzle(r)] = kept;
       }
     }
   }
@@ -362,7 +359,7 @@ __device__ __forceinline__ void attend(const w12_attention_args& a, const Lds<D>
   for (int n = 0; n < NS; ++n)
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      const uint4 k = *reinterpret_cast<const uint4*>(kbase + n * 32 * T::kRowBytes + (kpiece ^ (ks * 32u)));
+      const u32x4a k = *reinterpret_cast<const u32x4a*>(kbase + n * 32 * T::kRowBytes + (kpiece ^ (ks * 32u)));
       if (ks == 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) sc[n][i] = 0.0f;
@@ -409,24 +406,22 @@ __device__ __forceinline__ void attend(const w12_attention_args& a, const Lds<D>
   for (int n = 0; n < NS; ++n) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
-      uint32_t p[4];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         sc[n][8 * ks + i] = __builtin_amdgcn_exp2f(sc[n][8 * ks + i] * scale - base);
         x.l += sc[n][8 * ks + i];
       }
+      u32x4a p;
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = bf16_pair(sc[n][8 * ks + 2 * i], sc[n][8 * ks + 2 * i + 1]);
-      const bf16x8 pb = __builtin_bit_cast(bf16x8, make_uint4(p[0], p[1], p[2], p[3]));
+      const bf16x8 pb = __builtin_bit_cast(bf16x8, p);
 #pragma unroll
       for (int db = 0; db < D / 32; ++db) {
-        uint2 v[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          v[j] = __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                                               (lds_s16x4*)(vbase + (n * 32 + 16 * ks + 8 * j) * T::kRowBytes + (vpiece ^ (db * 64u)))));
-        x.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-            __builtin_bit_cast(bf16x8, make_uint4(v[0].x, v[0].y, v[1].x, v[1].y)), pb, x.o[db], 0, 0, 0);
+        const uint8_t* at = vbase + (n * 32 + 16 * ks) * T::kRowBytes + (vpiece ^ (db * 64u));
+        const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+        const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * T::kRowBytes));
+        const s16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+        x.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), pb, x.o[db], 0, 0, 0);
       }
     }
   }
@@ -509,8 +504,8 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
   Rows<D> x;
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
-    uint4 q = make_uint4(0, 0, 0, 0);
-    if (mine) q = *reinterpret_cast<const uint4*>(a.q + row * a.ldq + head * D + ks * 16 + hi * 8);
+    u32x4a q = {0, 0, 0, 0};
+    if (mine) q = *reinterpret_cast<const u32x4a*>(a.q + row * a.ldq + head * D + ks * 16 + hi * 8);
     x.q[ks] = __builtin_bit_cast(bf16x8, q);
   }
   s.fetch(first);
