@@ -597,12 +597,16 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
   }
 }
 
-// Joins the partial results of blocks of several chunks: a wave takes 32 rows and 8 elements, and adds the
-// parts in the order of the chunks (bitwise the same every time), eight in flight.
-template <int D, bool F8>
+// Joins the partial results of blocks of several chunks: 32 rows and 8 elements at a time, the parts in the order of
+// the chunks, eight in flight.  With few rows (SPLIT) each wave of a work-group takes a quarter of the parts and
+// the first adds the quarters in their order; with many each wave has elements of its own.  Either way
+// the order is the same every time, and with it every bit.
+template <int D, bool F8, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12_kv_cache c, const float* ws,
                                                        int row_groups, int target) {
-  __shared__ int64_t before[kMaxRequests + 1], rows_before[kMaxRequests + 1], sums[kAttnThreads / 64];
+  constexpr int kWaves = kAttnThreads / 64;
+  __shared__ int64_t before[kMaxRequests + 1], rows_before[kMaxRequests + 1], sums[kWaves];
+  __shared__ float quarter[SPLIT ? kWaves : 1][6][64];
   const int group = a.q_heads / c.heads;
   const Plan plan = plan_items(a, c, group, target, before, sums);
   const int64_t x = blockIdx.x;
@@ -619,42 +623,59 @@ __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12
   const int chunks = (bl.tiles + plan.chunk - 1) / plan.chunk;
   const int rgx = (int)(x - (a.requests > 1 ? uniform(rows_before[b]) : 0)), rb = rgx / 4, rg = rgx % 4;
   if (chunks <= 1 || rgx * 32 >= rq.nodes * group) return;      // written whole, or no rows
-  const int h = blockIdx.y, quad = blockIdx.z * (kAttnThreads / 64) + wave_id();
+  const int h = blockIdx.y, wave = wave_id();
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
   // the block's items: one a chunk, count() apart
   const int64_t item0 = (a.requests > 1 ? uniform(before[b]) : 0) + (int64_t)h * chunks * bl.count() + rb;
   const int64_t slot = slot_floats(D, row_groups) * 4, step = slot * bl.count();
   const char* part = reinterpret_cast<const char*>(ws) + item0 * slot;
-  const uint32_t o_off = (uint32_t)((rg * (D / 8) + quad) * 64 + lane) * 16u;
   const uint32_t ml_off = (uint32_t)(row_groups * 32 * D * 4 + (rg * 32 + col) * 8);
+  const int r = rgx * 32 + col;
+  const int64_t row = rq.start + r / group;
+  const int head = h * group + r % group;
+  const int quad = SPLIT ? blockIdx.z : blockIdx.z * kWaves + wave;
+  const uint32_t o_off = (uint32_t)((rg * (D / 8) + quad) * 64 + lane) * 16u;
   float m = -INFINITY, l = 0.0f;
   float4 o = make_float4(0, 0, 0, 0);
-  for (int i0 = 0; i0 < chunks; i0 += 8) {
+  auto add = [&](float m2, float l2, float4 o2) {
+    const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.0f : mn;
+    const float f1 = exp2f(m - base), f2 = exp2f(m2 - base);
+    m = mn;
+    l = l * f1 + l2 * f2;
+    o.x = o.x * f1 + o2.x * f2;
+    o.y = o.y * f1 + o2.y * f2;
+    o.z = o.z * f1 + o2.z * f2;
+    o.w = o.w * f1 + o2.w * f2;
+  };
+  const int begin = SPLIT ? chunks * wave / kWaves : 0, end = SPLIT ? chunks * (wave + 1) / kWaves : chunks;
+  for (int i0 = begin; i0 < end; i0 += 8) {
     float4 p[8];
     float2 ml[8];
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const char* at = part + min(i0 + u, chunks - 1) * step;
+      const char* at = part + min(i0 + u, end - 1) * step;
       ml[u] = *reinterpret_cast<const float2*>(at + ml_off);
       p[u] = *reinterpret_cast<const float4*>(at + o_off);
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      if (i0 + u >= chunks) break;
-      const float mn = fmaxf(m, ml[u].x), base = mn == -INFINITY ? 0.0f : mn;
-      const float f1 = exp2f(m - base), f2 = exp2f(ml[u].x - base);
-      m = mn;
-      l = l * f1 + ml[u].y * f2;
-      o.x = o.x * f1 + p[u].x * f2;
-      o.y = o.y * f1 + p[u].y * f2;
-      o.z = o.z * f1 + p[u].z * f2;
-      o.w = o.w * f1 + p[u].w * f2;
+    for (int u = 0; u < 8; ++u)
+      if (i0 + u < end) add(ml[u].x, ml[u].y, p[u]);
+  }
+  if constexpr (SPLIT) {
+    if (wave) {
+      const float v[6] = {m, l, o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int i = 0; i < 6; ++i) quarter[wave][i][lane] = v[i];
+    }
+    __syncthreads();
+    if (wave) return;
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) {
+      const float* q = &quarter[i][0][lane];
+      add(q[0], q[64], make_float4(q[128], q[192], q[256], q[320]));
     }
   }
-  const int r = rgx * 32 + col;
   if (r >= rq.nodes * group) return;
-  const int64_t row = rq.start + r / group;
-  const int head = h * group + r % group;
   const float inv = l == 0.0f ? 0.0f : (F8 ? c.v_scale[h] : 1.0f) / l;
   uint2 v = make_uint2(0, 0);
   if (l != 0.0f) {
@@ -667,7 +688,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12
 
 // Items of four waves that a call aims at: two rounds of the work-groups that the chip holds at once (two a
 // compute unit, one where a head of 256 takes its LDS).
-static int attention_target(int D) { return device_cus() * (D == 256 ? 1 : 2); }
+static int attention_target(int D) { return 2 * device_cus() * (D == 256 ? 1 : 2); }
 // Groups of 32 rows that a block can hold.
 static int attention_row_groups(int32_t T, int32_t q_heads, const w12_kv_cache& c) {
   const int64_t rows = (int64_t)T * (q_heads / c.heads);
@@ -697,8 +718,13 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t row_blocks = ceil_div((int64_t)a.T * (a.q_heads / c.heads), 32) + a.requests;
-  const dim3 grid((unsigned)row_blocks, (unsigned)c.heads, D / 8 / (kAttnThreads / 64));
-  hipLaunchKernelGGL((k_join<D, F8>), grid, dim3(kAttnThreads), 0, stream, a, c, (const float*)ws, rg, target);
+  // few rows: waves share the parts (63 nodes over 8191 tokens 11.4 -> 7.7 us); many: they share the work of finding
+  // the request, and a wave's parts are few (16 requests of 24 nodes 29 -> 13 us)
+  const unsigned x = (unsigned)row_blocks, y = (unsigned)c.heads;
+  if (row_blocks * c.heads < device_cus())
+    hipLaunchKernelGGL((k_join<D, F8, true>), dim3(x, y, D / 8), t, 0, stream, a, c, (const float*)ws, rg, target);
+  else
+    hipLaunchKernelGGL((k_join<D, F8, false>), dim3(x, y, D / 32), t, 0, stream, a, c, (const float*)ws, rg, target);
   return hipGetLastError();
 }
 
