@@ -318,6 +318,81 @@ struct Stream {
   }
 };
 
+// A tile in one page of a BF16 cache goes from memory to LDS without passing through registers: a lane names the
+// 16 bytes that belong in its place of a row (the swizzle is in the addresses).  The page table is read through the
+// scalar cache, so nothing in the loop waits for a load but the barrier that ends it.  Tiles that have drafted or
+// missing tokens (few) are gone over in LDS before they are used.
+template <int D>
+struct Direct {
+  using T = Tile<D, false>;
+  typedef __attribute__((address_space(4))) const int32_t scalar_i32;
+  const w12_attention_args& a;
+  const w12_kv_cache& c;
+  Lds<D>& lds;
+  scalar_i32* table;
+  int page_bits, ctx, len;
+  int64_t head_bytes;
+  uint32_t koff[T::kPass], voff[T::kPass];
+
+  __device__ __forceinline__ int row() const { return threadIdx.x / T::kSrc; }
+  __device__ __forceinline__ int place() const { return threadIdx.x % T::kSrc; }
+
+  __device__ __forceinline__ void begin(int b, int h, const Request& rq) {
+    table = (scalar_i32*)(uintptr_t)(a.page_table + b * a.ld_table);
+    ctx = rq.ctx;
+    len = rq.len;
+    head_bytes = (int64_t)h * c.head_stride * 2;
+#pragma unroll
+    for (int i = 0; i < T::kPass; ++i) {
+      const int r = i * T::kRows + row();
+      koff[i] = (uint32_t)r * (uint32_t)(c.token_stride * 2) + (place() ^ T::k_swizzle(r)) * 16;
+      voff[i] = (uint32_t)r * (uint32_t)(c.token_stride * 2) + (place() ^ T::v_swizzle(r)) * 16;
+    }
+  }
+
+  __device__ __forceinline__ int page_of(int tile) const { return table[uniform(tile * kTile >> page_bits)]; }
+  __device__ __forceinline__ bool is_page(int p) const { return (uint32_t)p < (uint32_t)c.pages; }
+  // Whether a tile has tokens to look at one by one.
+  __device__ __forceinline__ bool special(int tile) const { return (tile + 1) * kTile > ctx || !is_page(page_of(tile)); }
+
+  // Starts a tile's way into a buffer; wait_vm_all ends it.
+  __device__ __forceinline__ void fetch(int tile, int buf) {
+    const int p = page_of(tile);
+    const int64_t base = ((int64_t)(is_page(p) ? p : 0) * c.page_stride + (int64_t)(tile * kTile & (c.page_size - 1)) * c.token_stride) * 2 +
+                         head_bytes;
+    const uint64_t kp = (uint64_t)(uintptr_t)c.k + base, vp = (uint64_t)(uintptr_t)c.v + base;
+    const uint32_t wave_at = (uint32_t)wave_id() * 1024u;
+#pragma unroll
+    for (int i = 0; i < T::kPass; ++i) {
+      to_lds(kp, koff[i], lds_off(lds.kv[buf][0]) + i * (kAttnThreads * 16) + wave_at);
+      to_lds(vp, voff[i], lds_off(lds.kv[buf][1]) + i * (kAttnThreads * 16) + wave_at);
+    }
+  }
+  // 16 bytes a lane from base + off to the wave's 1 KB of LDS at `at`.  Not through the builtin: the compiler would
+  // wait for it before every read of LDS.
+  __device__ __forceinline__ static void to_lds(uint64_t base, uint32_t off, uint32_t at) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" : : "s"(uniform((int)at)), "v"(off), "s"(base) : "memory", "m0");
+  }
+
+  // What put() does in Stream, in place.
+  __device__ __forceinline__ void look_over(int tile, int buf) {
+    const bool in_page = is_page(page_of(tile));
+#pragma unroll
+    for (int i = 0; i < T::kPass; ++i) {
+      const int r = i * T::kRows + row();
+      const bool in = in_page && tile * kTile + r < len;
+      if (place() == 0) lds.there[buf][r] = in;
+      u32x4a* const v = lds.kv[buf][1] + r * T::kPieces + place();
+      const u32x4a was = *v;
+      const bool bad = in && tile * kTile + r >= ctx && not_finite<false>(was);
+      const uint64_t mine = ((1ull << T::kSrc) - 1) << ((threadIdx.x & 63) / T::kSrc * T::kSrc);
+      const uint64_t any = __ballot(bad);
+      if (any) lds.bad = 1;
+      if (!in || (any & mine)) *v = u32x4a{0, 0, 0, 0};
+    }
+  }
+};
+
 // A wave's 32 rows (a lane: its row's elements of the query and result, shared with the lane 32 away).
 template <int D>
 struct Rows {
@@ -346,36 +421,61 @@ __device__ __forceinline__ uint32_t attended(const w12_attention_args& a, int ct
   return valid & (cached | sees);
 }
 
-// NS blocks of 32 tokens (from block `sub` of the tile in `buf`) for the wave's rows.
+// NS blocks of 32 tokens (from block `sub` of the tile in `buf`) for the wave's rows.  special: tokens may be missing
+// or drafted.
 template <int D, int NS, typename T>
 __device__ __forceinline__ void attend(const w12_attention_args& a, const Lds<D>& lds, Rows<D>& x, int ctx, int tile, int buf,
-                                       int sub, int row, int node, float scale) {
+                                       int sub, int row, int node, float scale, bool special) {
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
+  constexpr int KS = D / 16, DB = D / 32;
   f32x16 sc[NS];
   // a lane's K operand: its token's row; the piece 2 ks + hi is the one for ks = 0 with bits of ks flipped
   const uint8_t* kbase = reinterpret_cast<const uint8_t*>(lds.kv[buf][0]) + (sub * 32 + col) * T::kRowBytes;
   const uint32_t kpiece = (uint32_t)(hi ^ T::k_swizzle(col)) * 16;
+  // operands are read kAhead instructions before their use (left to itself the compiler reads them right before it)
+  constexpr int kAhead = 4;
+  u32x4a kf[kAhead];
+  auto read_k = [&](int i) {
+    kf[i % kAhead] = *reinterpret_cast<const u32x4a*>(kbase + i / KS * 32 * T::kRowBytes + (kpiece ^ (i % KS * 32u)));
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) read_k(i);
 #pragma unroll
   for (int n = 0; n < NS; ++n)
 #pragma unroll
-    for (int ks = 0; ks < D / 16; ++ks) {
-      const u32x4a k = *reinterpret_cast<const u32x4a*>(kbase + n * 32 * T::kRowBytes + (kpiece ^ (ks * 32u)));
-      if (ks == 0) {
+    for (int i = 0; i < 16; ++i) sc[n][i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) sc[n][i] = 0.0f;
+  for (int i = 0; i < NS * KS; ++i) {
+    __builtin_amdgcn_sched_barrier(0);
+    sc[i / KS] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, kf[i % kAhead]), x.q[i % KS], sc[i / KS], 0, 0, 0);
+    if (i + kAhead < NS * KS) read_k(i + kAhead);
+  }
+  // a lane's V operand: 4 elements of one token, which the transposing read exchanges among 16 lanes
+  const int g = lane >> 4, t4 = (lane & 15) >> 2;
+  const int vtoken = 4 * (g >> 1) + t4;
+  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(lds.kv[buf][1]) + (sub * 32 + vtoken) * T::kRowBytes + (lane & 1) * 8;
+  const uint32_t vpiece = (uint32_t)((2 * (g & 1) + ((lane & 3) >> 1)) ^ T::v_swizzle(vtoken)) * 16;
+  constexpr int kVAhead = 4;
+  s16x8 vf[kVAhead];
+  auto read_v = [&](int i) {      // of 16 tokens i / DB, elements 32 (i % DB) .. + 31
+    const uint8_t* at = vbase + i / DB * 16 * T::kRowBytes + (vpiece ^ (i % DB * 64u));
+    const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+    const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * T::kRowBytes));
+    vf[i % kVAhead] = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+#pragma unroll
+  for (int i = 0; i < kVAhead; ++i) read_v(i);
+  if (special) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const int tok0 = tile * kTile + (sub + n) * 32;
+      const uint32_t valid = (uint32_t)__ballot(lds.there[buf][(sub + n) * 32 + col] != 0);
+      if (valid != ~0u || tok0 + 32 > ctx) {
+        const uint32_t mine = attended(a, ctx, row, node, tok0, valid) >> (4 * hi);
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (!(mine >> (8 * (r >> 2) + (r & 3)) & 1)) sc[n][r] = -INFINITY;
       }
-      sc[n] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, k), x.q[ks], sc[n], 0, 0, 0);
-    }
-  // masks: needed where a token is missing or a drafted one is among them
-#pragma unroll
-  for (int n = 0; n < NS; ++n) {
-    const int tok0 = tile * kTile + (sub + n) * 32;
-    const uint32_t valid = (uint32_t)__ballot(lds.there[buf][(sub + n) * 32 + col] != 0);
-    if (valid != ~0u || tok0 + 32 > ctx) {
-      const uint32_t mine = attended(a, ctx, row, node, tok0, valid) >> (4 * hi);
-#pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (!(mine >> (8 * (r >> 2) + (r & 3)) & 1)) sc[n][r] = -INFINITY;
     }
   }
   float top = -INFINITY;
@@ -397,32 +497,23 @@ __device__ __forceinline__ void attend(const w12_attention_args& a, const Lds<D>
       for (int r = 0; r < 16; ++r) x.o[db][r] *= corr;
   }
   const float base = x.m == -INFINITY ? 0.0f : x.m * scale;
-  // a lane's V operand: 4 elements of one token, which the transposing read exchanges among 16 lanes
-  const int g = lane >> 4, t4 = (lane & 15) >> 2;
-  const int vtoken = 4 * (g >> 1) + t4;
-  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(lds.kv[buf][1]) + (sub * 32 + vtoken) * T::kRowBytes + (lane & 1) * 8;
-  const uint32_t vpiece = (uint32_t)((2 * (g & 1) + ((lane & 3) >> 1)) ^ T::v_swizzle(vtoken)) * 16;
 #pragma unroll
-  for (int n = 0; n < NS; ++n) {
+  for (int u = 0; u < 2 * NS; ++u) {      // 16 tokens
+    const int n = u / 2, ks = u % 2;
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
+    for (int i = 0; i < 8; ++i) {
+      sc[n][8 * ks + i] = __builtin_amdgcn_exp2f(sc[n][8 * ks + i] * scale - base);
+      x.l += sc[n][8 * ks + i];
+    }
+    u32x4a p;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sc[n][8 * ks + i] = __builtin_amdgcn_exp2f(sc[n][8 * ks + i] * scale - base);
-        x.l += sc[n][8 * ks + i];
-      }
-      u32x4a p;
+    for (int i = 0; i < 4; ++i) p[i] = bf16_pair(sc[n][8 * ks + 2 * i], sc[n][8 * ks + 2 * i + 1]);
+    const bf16x8 pb = __builtin_bit_cast(bf16x8, p);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = bf16_pair(sc[n][8 * ks + 2 * i], sc[n][8 * ks + 2 * i + 1]);
-      const bf16x8 pb = __builtin_bit_cast(bf16x8, p);
-#pragma unroll
-      for (int db = 0; db < D / 32; ++db) {
-        const uint8_t* at = vbase + (n * 32 + 16 * ks) * T::kRowBytes + (vpiece ^ (db * 64u));
-        const s16x4 v0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
-        const s16x4 v1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * T::kRowBytes));
-        const s16x8 v = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
-        x.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), pb, x.o[db], 0, 0, 0);
-      }
+    for (int db = 0; db < DB; ++db) {
+      const int i = u * DB + db;
+      x.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[i % kVAhead]), pb, x.o[db], 0, 0, 0);
+      if (i + kVAhead < 2 * NS * DB) read_v(i + kVAhead);
     }
   }
 }
@@ -486,7 +577,8 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
   const int rb = in % bl.count(), chunk = in / bl.count() % chunks, h = in / bl.count() / chunks;
   const int w = rb < bl.full ? 4 : bl.rest;
   const int first = chunk * plan.chunk, last = min(first + plan.chunk, bl.tiles);
-  Stream<D, F8, WHOLE> s{a, c, lds};
+  constexpr bool kDirect = WHOLE && !F8;
+  std::conditional_t<kDirect, Direct<D>, Stream<D, F8, WHOLE>> s{a, c, lds};
   s.page_bits = 31 - __builtin_clz(c.page_size);
   // this wave's rows: in a block of 4 every wave has 32 rows and all tokens, in one of 2 the waves
   // are two groups of rows by two halves of each tile
@@ -500,7 +592,8 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
   const int row = rq.start + node;
   const float scale = a.scale * kLog2e * (F8 ? c.k_scale[h] : 1.0f);
   s.begin(b, h, rq);
-  s.look_up(first);
+  if constexpr (kDirect) s.fetch(first, 0);
+  else s.look_up(first);
   Rows<D> x;
 #pragma unroll
   for (int ks = 0; ks < D / 16; ++ks) {
@@ -508,8 +601,10 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
     if (mine) q = *reinterpret_cast<const u32x4a*>(a.q + row * a.ldq + head * D + ks * 16 + hi * 8);
     x.q[ks] = __builtin_bit_cast(bf16x8, q);
   }
-  s.fetch(first);
-  s.look_up(min(first + 1, last - 1));
+  if constexpr (!kDirect) {
+    s.fetch(first);
+    s.look_up(min(first + 1, last - 1));
+  }
 #pragma unroll
   for (int db = 0; db < D / 32; ++db)
 #pragma unroll
@@ -517,17 +612,33 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
   x.m = -INFINITY;
   x.l = 0.0f;
   if (threadIdx.x == 0) lds.bad = 0;
-  lds_barrier();
-  s.put(first, 0);
-  lds_barrier();
+  if constexpr (kDirect) {
+    wait_vm_all();
+    lds_barrier();
+  } else {
+    lds_barrier();
+    s.put(first, 0);
+    lds_barrier();
+  }
   // one loop for each kind of wave: paths that meet inside a loop cost copies of the result's registers
   auto run = [&](auto blocks, int sub) {
     for (int tile = first; tile < last; ++tile) {
       const int buf = (tile - first) & 1, next = min(tile + 1, last - 1);      // past the end: what the caches hold
-      s.fetch(next);
-      s.look_up(min(tile + 2, last - 1));
-      if constexpr (blocks.value > 0) attend<D, blocks.value, T>(a, lds, x, rq.ctx, tile, buf, sub, row, node, scale);
-      s.put(next, buf ^ 1);
+      bool special = true;
+      if constexpr (kDirect) {
+        special = s.special(tile);
+        if (special) {
+          s.look_over(tile, buf);
+          lds_barrier();
+        }
+        s.fetch(next, buf ^ 1);
+      } else {
+        s.fetch(next);
+        s.look_up(min(tile + 2, last - 1));
+      }
+      if constexpr (blocks.value > 0) attend<D, blocks.value, T>(a, lds, x, rq.ctx, tile, buf, sub, row, node, scale, special);
+      if constexpr (kDirect) wait_vm_all();
+      else s.put(next, buf ^ 1);
       lds_barrier();
     }
   };
