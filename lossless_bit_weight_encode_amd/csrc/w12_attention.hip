@@ -497,25 +497,34 @@ __device__ __forceinline__ void attend(const w12_attention_args& a, const Lds<D>
       for (int r = 0; r < 16; ++r) x.o[db][r] *= corr;
   }
   const float base = x.m == -INFINITY ? 0.0f : x.m * scale;
+  // 16 tokens (u) at a time, and beside each of their matrix instructions a part of the next 16 tokens' exponentials: a
+  // wave issues in order, so what is to run under a matrix instruction has to stand right behind it
+  constexpr int kEach = 8 / DB > 0 ? 8 / DB : 1;
+  u32x4a p[2];
+  auto weigh = [&](int u, int i) {      // score i of 8
+    float& l = x.l;
+    const float e = __builtin_amdgcn_exp2f(sc[u / 2][8 * (u % 2) + i] * scale - base);
+    l += e;
+    sc[u / 2][8 * (u % 2) + i] = e;
+    if (i % 2) p[u % 2][i / 2] = bf16_pair(sc[u / 2][8 * (u % 2) + i - 1], e);
+  };
 #pragma unroll
-  for (int u = 0; u < 2 * NS; ++u) {      // 16 tokens
-    const int n = u / 2, ks = u % 2;
+  for (int i = 0; i < 8; ++i) weigh(0, i);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sc[n][8 * ks + i] = __builtin_amdgcn_exp2f(sc[n][8 * ks + i] * scale - base);
-      x.l += sc[n][8 * ks + i];
-    }
-    u32x4a p;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = bf16_pair(sc[n][8 * ks + 2 * i], sc[n][8 * ks + 2 * i + 1]);
-    const bf16x8 pb = __builtin_bit_cast(bf16x8, p);
+  for (int u = 0; u < 2 * NS; ++u)
 #pragma unroll
     for (int db = 0; db < DB; ++db) {
       const int i = u * DB + db;
-      x.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[i % kVAhead]), pb, x.o[db], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      x.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, vf[i % kVAhead]),
+                                                        __builtin_bit_cast(bf16x8, p[u % 2]), x.o[db], 0, 0, 0);
       if (i + kVAhead < 2 * NS * DB) read_v(i + kVAhead);
+      if (u + 1 < 2 * NS) {
+#pragma unroll
+        for (int j = 0; j < kEach; ++j)
+          if (db * kEach + j < 8) weigh(u + 1, db * kEach + j);
+      }
     }
-  }
 }
 
 // Drafted tokens of tiles [first, last) whose values were taken out (infinities, NaN): added one by one, element by
