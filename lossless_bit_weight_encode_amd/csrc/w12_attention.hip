@@ -629,6 +629,9 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
     s.put(first, 0);
     lds_barrier();
   }
+  // The query is here before the loop: a load that is first used inside it would be waited for there, every time.
+#pragma unroll
+  for (int ks = 0; ks < D / 16; ++ks) asm volatile("" : "+v"(x.q[ks]));
   // one loop for each kind of wave: paths that meet inside a loop cost copies of the result's registers
   auto run = [&](auto blocks, int sub) {
     for (int tile = first; tile < last; ++tile) {
