@@ -121,9 +121,10 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
     // the step.  Pieces past the end of a row (in the last step) hold what follows it; they are cleared before use.
     uint4 wreg[DEPTH][C::kWPieces], xreg[DEPTH][C::kXPieces];
     float sreg[DEPTH][MB + 1];
+    const bool tail = last * kStepK > g.K;
+    const int whole = last - tail;
     auto fetch = [&](int step, int d) {
-      const int st = min(step, last - 1);
-      const uint32_t k = (uint32_t)(st * kStepK);
+      const uint32_t k = (uint32_t)(step * kStepK);
 #pragma unroll
       for (int i = 0; i < C::kWPieces; ++i)
         wreg[d][i] = C::kLds ? bload16(rw, woff[i] + k) : bload16(rw, woff[i / 4] + k + 32 * (i % 4));
@@ -133,8 +134,7 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
     };
     // Scales.  A lane's are those of its rows of X, each in a line of memory of its own: with LDS they are brought there
     // for 32 steps at once (512 rows through 34816 x 5120: 20 us less than step by step); else they travel with the operands.
-    auto fetch_scales = [&](int step, int d) {
-      const int st = min(step, last - 1);
+    auto fetch_scales = [&](int st, int d) {
 #pragma unroll
       for (int b = 0; b < MB; ++b)
         sreg[d][b] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, (int)((xsoff[b] + (uint32_t)st) * 4u), 0, 0));
@@ -162,18 +162,22 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
       for (int i = 0; i < C::kXPieces; ++i)
         xreg[d][i] = first_bytes(xreg[d][i], end - 16 * (C::kLds ? piece : 2 * (i % 4) + hi));
     };
+    // Part i of the kParts in which a step is put into its buffer.
+    constexpr int kParts = C::kWPieces + C::kXPieces;
+    auto put_part = [&](int i, int buf, int d) {
+      if (i < C::kWPieces) {
+        const int r = prow + i * kRowsStep;
+        lw[buf][r * 8 + (piece ^ (r >> 1 & 7))] = wreg[d][i < C::kWPieces ? i : 0];
+      } else {
+        const int j = i - C::kWPieces, r = prow + j * kRowsStep;
+        const uint4 x = xreg[d][j < 0 ? 0 : j];
+        lx[buf][r * 16 + ((2 * piece) ^ (r & 15))] = widen8(x.x, x.y);
+        lx[buf][r * 16 + ((2 * piece + 1) ^ (r & 15))] = widen8(x.z, x.w);
+      }
+    };
     auto put = [&](int buf, int d) {
 #pragma unroll
-      for (int i = 0; i < C::kWPieces; ++i) {
-        const int r = prow + i * kRowsStep;
-        lw[buf][r * 8 + (piece ^ (r >> 1 & 7))] = wreg[d][i];
-      }
-#pragma unroll
-      for (int i = 0; i < C::kXPieces; ++i) {
-        const int r = prow + i * kRowsStep;
-        lx[buf][r * 16 + ((2 * piece) ^ (r & 15))] = widen8(xreg[d][i].x, xreg[d][i].y);
-        lx[buf][r * 16 + ((2 * piece + 1) ^ (r & 15))] = widen8(xreg[d][i].z, xreg[d][i].w);
-      }
+      for (int i = 0; i < kParts; ++i) put_part(i, buf, d);
     };
 
     f32x16 acc[NB][MB];
@@ -184,7 +188,10 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.0f;
 
-    auto compute = [&](int buf, int d, int scales) {
+    // `beside(i)` stands behind the matrix instructions of the i-th of 8 parts: what is to run under them has to.  A step
+    // past the last whole one counts nothing (its operands are that step's, so 0 times its sum is 0, or NaN where
+    // the sum is NaN already).
+    auto compute = [&](int buf, int d, int scales, bool counts, auto beside) {
       float sc[MB];
       if constexpr (C::kLds) {
         const float ws = lws[scales][wn * NB * 32 / W12_QUANT_BLOCK];
@@ -194,6 +201,8 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
 #pragma unroll
         for (int b = 0; b < MB; ++b) sc[b] = sreg[d][b] * sreg[d][MB];
       }
+#pragma unroll
+      for (int b = 0; b < MB; ++b) sc[b] = counts ? sc[b] : 0.0f;
       f32x16 part[NB][MB];
 #pragma unroll
       for (int a = 0; a < NB; ++a)
@@ -239,6 +248,7 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
           for (int b = 0; b < MB; ++b)
             part[a][b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(wb, __builtin_bit_cast(bf16x8, x[i % (kAhead + 1)][b]), part[a][b], 0, 0, 0);
         }
+        beside(i);
       }
 #pragma unroll
       for (int a = 0; a < NB; ++a)
@@ -248,23 +258,21 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
           for (int i = 0; i < 16; ++i) acc[a][b][i] += part[a][b][i] * sc[b];
     };
 
+    auto within = [&](int step) { return max(min(step, whole - 1), first); };
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      fetch(first + d, d);
-      if constexpr (!C::kLds) fetch_scales(first + d, d);
+      fetch(within(first + d), d);
+      if constexpr (!C::kLds) fetch_scales(within(first + d), d);
     }
     if constexpr (C::kLds) {
       put(0, 0);
-      fetch(first + DEPTH, 0);
+      fetch(within(first + DEPTH), 0);
       lds_barrier();
     }
     // Step s goes through the registers of slot (s - first) % DEPTH and, with LDS, buffer (s - first) % 2, into
-    // which it is put while step s - 1 is computed.  Only the computing is skipped past the last whole step, and
-    // a step that k ends in is taken by itself below: where paths meet that a fetch or its use was on one of,
-    // the compiler waits for more than is needed.
+    // which it is put while step s - 1 is computed.  There is no branch in a turn: where paths meet that a fetch
+    // or its use was on one of, the compiler waits for more than is needed.  A step that k ends in is taken by itself below.
     constexpr int kTurn = DEPTH % 2 ? 2 * DEPTH : DEPTH;
-    const bool tail = last * kStepK > g.K;
-    const int whole = last - tail;
     static_assert(kScaleSteps % kTurn == 0, "scales are renewed between turns");
     for (int s0 = first; s0 < whole; s0 += kTurn) {
       if constexpr (C::kLds) {
@@ -273,14 +281,18 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
 #pragma unroll
       for (int i = 0; i < kTurn; ++i) {
         const int d = i % DEPTH, next = (i + 1) % DEPTH, step = s0 + i;
-        if (wave_on && step < whole) compute(i & 1, d, (s0 - first) % kScaleSteps + i);
+        compute(i & 1, d, (s0 - first) % kScaleSteps + i, step < whole, [&](int part) {
+          if constexpr (C::kLds) {
+#pragma unroll
+            for (int q = part * kParts / 8; q < (part + 1) * kParts / 8; ++q) put_part(q, (i + 1) & 1, next);
+          }
+        });
         if constexpr (C::kLds) {
-          put((i + 1) & 1, next);
-          fetch(step + 1 + DEPTH, next);
+          fetch(within(step + 1 + DEPTH), next);
           lds_barrier();
         } else {
-          fetch(step + DEPTH, d);
-          fetch_scales(step + DEPTH, d);
+          fetch(within(step + DEPTH), d);
+          fetch_scales(within(step + DEPTH), d);
         }
       }
     }
@@ -292,7 +304,7 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
         put(0, 0);
         put_scales(whole);
       }
-      if (wave_on) compute(0, 0, 0);
+      compute(0, 0, 0, true, [](int) {});
       if constexpr (C::kLds) lds_barrier();      // the next tile goes to the same buffers
     }
 
