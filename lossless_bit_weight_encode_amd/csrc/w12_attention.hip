@@ -41,7 +41,7 @@ constexpr int kMaxRequests = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;       // log2 of the largest p that a stale maximum may give
 constexpr int kMinChunk = 2;         // least tiles of a chunk where all rows are up to 64,
-constexpr int kMinChunkLarge = 6;    // and elsewhere: a partial result is as large as 2 tiles
+constexpr int kMinChunkLarge = 4;    // and elsewhere: a partial result is as large as 2 tiles
 
 // One request: its rows and lengths, cut to what is there.
 struct Request {
@@ -127,11 +127,23 @@ __device__ __forceinline__ float other_half(float v) {
   return __builtin_bit_cast(float, (threadIdx.x & 32) ? sw[0] : sw[1]);
 }
 
-// Tiles of a chunk: the cost of all tiles over `target` items of four waves, at least kMinChunk (one request of
-// up to 64 rows: its partial results are small) or 8.
+// Tiles of a chunk where requests share the chip: the cost of all tiles over `target` items of four waves.
 __device__ __forceinline__ int chunk_of(int64_t cost, int target, int rows) {
   const int64_t even = (cost + 4 * (int64_t)target - 1) / (4 * (int64_t)target);
   return (int)max(even, (int64_t)(rows <= kBlockRows / 2 ? kMinChunk : kMinChunkLarge));
+}
+
+// Tiles of a chunk of one request, whose items (per = heads x blocks, for each chunk) are about equally long: they
+// go in whole rounds of the `slots` work-groups that the chip holds, the fewest that leave at most a quarter of the
+// slots empty; a few items over a round would cost another one.
+__device__ __forceinline__ int one_request_chunk(const Blocks& k, int slots, int per, int rows) {
+  int chunks = 1;
+  for (int rounds = 1; rounds <= 4; ++rounds) {
+    chunks = max(rounds * slots / max(per, 1), 1);
+    if (4 * chunks * per >= 3 * rounds * slots) break;
+  }
+  const int least = rows <= kBlockRows / 2 ? min(max((k.tiles + 31) / 32, kMinChunk), 2 * kMinChunk) : kMinChunkLarge;
+  return max((k.tiles + chunks - 1) / chunks, least);
 }
 
 // The items of a call.  `before` (LDS) holds the number of items before each request; one request needs none.
@@ -149,7 +161,7 @@ __device__ __forceinline__ Plan plan_items(const w12_attention_args& a, const w1
   Plan p;
   if (a.requests == 1) {
     const Blocks k = blocks_of(request_of(a, c.page_size, 0), group);
-    p.chunk = chunk_of(k.cost() * c.heads, target, a.T * group);
+    p.chunk = one_request_chunk(k, target / 2, c.heads * k.count(), a.T * group);
     p.items = items_of(k, c.heads, p.chunk);
   } else {
     const int64_t cost = uniform(prefix_requests(a.requests, before, sums, [&](int b) {
