@@ -8,10 +8,15 @@
 // A work-group takes tiles of BN channels x BM rows of X; their steps, end to end, are cut into equal
 // shares, one a work-group (so few tiles of a long k fill the chip).  The work-groups of a tile leave
 // FP32 partial tiles, and the last one to arrive adds them in the order of the work-groups (bitwise the
-// same every time).  Operands are loaded into registers DEPTH steps ahead.  Tiles of more than 32 rows pass
-// them through LDS (double-buffered; W as it is, X widened to BF16 once for all waves), their pieces
-// swizzled by row so that the operand reads, 32 rows of one piece, meet every bank equally.  Tiles of up
-// to 32 rows load straight into operand registers: a wave's W is nobody else's, and no wave waits for another.
+// same every time).  Operands are loaded into registers DEPTH steps ahead.  They pass
+// through LDS (double-buffered; W as it is, X widened to BF16 once for all waves), their pieces
+// swizzled by row so that the operand reads, 32 rows of one piece, meet every bank equally; the next step's
+// pieces are put there beside the matrix instructions.  For a few rows over a short W they load
+// straight into operand registers: a wave's W is nobody else's, and no wave waits for another.
+//
+// Bound: few rows by the read of W (63 rows of 34816 x 5120, 178 MB: 57 us, 3.3 TB/s; a bare read of W in this order
+// takes 38), many by the matrix instructions and what feeds them (512 rows: 222 us, 820 TFLOP/s; the
+// instructions alone 120).
 #include "w12_device.h"
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
@@ -337,7 +342,7 @@ __global__ __launch_bounds__(C::kThreads, C::kWavesPerSimd) void k_gemm_e4m3(E4m
       }
       continue;
     }
-    // A partial tile, device-coherent (sc1), as its reader may be on another XCD.  Tiles of up to 32 rows
+    // A partial tile, device-coherent (sc1), as its reader may be on another XCD.  Tiles in registers
     // are laid out [row of X][channel], so that every thread adds (one row has few places, and many parts);
     // the others [wave][float4][lane], whole lines a store, and a lane adds what it holds.
     const uint32_t lane_part = (uint32_t)(wave * NB * MB * 4 * 64 + lane) * 16u;
@@ -429,8 +434,12 @@ struct E4m3Plan {
   uint64_t part_bytes;
 };
 
-// Tiles of up to 32 rows: 128 channels, so that a thread's registers leave room for three work-groups a compute unit
-// (5120 channels of 17408, one row: 26.4 us; 256 channels and two work-groups 28.4).
+// Which tile (us, both sides): up to 64 rows Rows64, 256 channels on 8 waves, where Rows128 pads (34816 channels of 5120:
+// 16 rows 46 / 56, 64 rows 57 / 64; 96 rows 71 / 71).  Up to 4 rows, a W of long rows and up to 128 MB is faster
+// straight into registers, with three small work-groups a compute unit and partial tiles of the real rows only (Rows32
+// / Rows64: 5120 of 17408 with 1 row 26.5 / 31.2, 4 rows 29.0 / 31.6, 8 rows 32.7 / 29.5; 5120 of 5120 with 1 row
+// 13.9 / 14.8, but 5120 of 34816 51.9 / 48.2, 10240 of 8192 27.4 / 26.0, 34816 of 5120 57 / 43).  Tiles of 128
+// channels: with 256 and two work-groups a unit 5120 of 17408 takes 28.5.
 using E4m3Rows32 = E4m3Cfg<4, 1, 1, 1, 2, 3, false>;
 using E4m3Rows64 = E4m3Cfg<8, 1, 1, 2, 2, 1, true>;
 using E4m3Rows128 = E4m3Cfg<4, 2, 2, 2, 1, 1, true>;
@@ -450,7 +459,7 @@ static void plan_with(E4m3Plan& p, int M, int N) {
 static E4m3Plan plan_e4m3(int M, int N, int K) {
   E4m3Plan p;
   p.steps = ceil_div(K, kStepK);
-  p.path = M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  p.path = M <= 4 && K >= N && (int64_t)N * K <= (int64_t(1) << 27) ? 32 : M <= 64 ? 64 : 128;
   if (p.path == 32) plan_with<E4m3Rows32>(p, M, N);
   else if (p.path == 64) plan_with<E4m3Rows64>(p, M, N);
   else plan_with<E4m3Rows128>(p, M, N);
