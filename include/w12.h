@@ -299,8 +299,9 @@ int w12_read_probe(const void *buf, uint64_t bytes, int32_t loads_per_lane, int3
  * of drafted tokens over that cache, and an 8-bit product for layers that are kept in 8 bits (a
  * drafter's; the target's weights are W12).  All conventions above apply.  Matrices here are
  * accessed with 16-byte vectors: base pointers are 16-byte aligned and pitches are multiples of
- * 16 bytes unless an argument says otherwise; no byte past the last element of a row is read or
- * written.  E4M3 is the 8-bit OCP format with 3 mantissa bits (largest value 448).
+ * 16 bytes unless an argument says otherwise.  Nothing past the last element of a row is written;
+ * what lies between rows, or in the 16-byte step that holds an operand's last element, may be read
+ * and never counts.  E4M3 is the 8-bit OCP format with 3 mantissa bits (largest value 448).
  */
 #define W12_DTYPE_BF16 0
 #define W12_DTYPE_F32 1
@@ -398,7 +399,7 @@ int w12_rope_append(const w12_rope_args *a, const w12_kv_cache *cache, hipStream
  *   out[row][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max),  in FP32.
  *   lse[row][h] = log sum_t exp(scale * q . k_t), if lse is not NULL.
  * What a row does not attend never reaches it, NaN and infinity included.  A row that attends
- * nothing gives zeros and lse -inf.  Tokens past max_pages * page_size, and tokens whose page is
+ * nothing, or whose scores are all -inf, gives zeros and lse -inf.  Tokens past max_pages * page_size, and tokens whose page is
  * not in 0 .. pages - 1, count as absent.  Rows outside every request are left as they are;
  * ranges of node_ptr are cut to 0..T and must not decrease; negative lengths count as 0.
  * node_ptr, ctx_len, page_table and tree_mask are device memory read by the kernels (a captured
@@ -434,7 +435,8 @@ int w12_tree_attention(const w12_attention_args *a, const w12_kv_cache *cache, v
  * Y[m][n] = sum_k (X[m][k] x_scale[m][k / 128]) (W[n][k] w_scale[n / 128][k / 128]) with E4M3 X and
  * W, FP32 scales, sums and Y: one scale per row and block of 128 of X (as w12_add_rmsnorm gives
  * them), one per block of 128 x 128 of W.  Bitwise the same from run to run for the same (M, N, K).
- * ldx and ldw are multiples of 16 bytes; ldxs, ldws >= ceil(K / 128); Y is 4-byte aligned.
+ * ldx and ldw are multiples of 16 bytes; ldxs, ldws >= ceil(K / 128), (M - 1) * ldxs + ceil(K / 128)
+ * < 2^29; Y is 4-byte aligned.
  * 1 <= M <= 4096, N and K as for w12_gemm.  ws: as for w12_gemm (w12_gemm_e4m3_workspace_size
  * bytes, initialised once with w12_gemm_workspace_init; every call leaves its counters zero).
  */

@@ -2,8 +2,9 @@
 //
 // The rows of a request that read one cache head (node i, query head g: row i * group + g) are cut
 // into blocks of 128, the tokens into tiles of 64 and the tiles into chunks.  A work-group takes one
-// block over one chunk; the length of a chunk is the same for all requests, chosen on the device so that
-// the items fill the chip about evenly (unequal lengths give unequal numbers of items).  Items are numbered
+// block over one chunk; the length of a chunk is the same for all requests, chosen on the device: of one
+// request so that the items make whole rounds of the chip, of several so that they fill it
+// about evenly (unequal lengths give unequal numbers of items).  Items are numbered
 // request, head, chunk, block, and neighbouring numbers run on one XCD: the blocks of a chunk read its
 // keys and values together, once from memory.  Blocks of several chunks leave partial results, which
 // k_join adds in the order of the chunks.
@@ -16,9 +17,14 @@
 // l and O are scaled only when a score passes m by 2^8 (p stays below 2^8).  P is rounded to BF16
 // for the product (relative error 2^-8 of each p at most); everything else is FP32.
 //
-// Tiles go global -> registers -> LDS (double-buffered, 16-byte pieces swizzled by token so that
-// both reads are free of bank conflicts) while the previous tile is computed on; E4M3 caches become BF16
-// (exactly) on the way, their scales go into c and the result.
+// Tiles go to LDS (double-buffered, 16-byte pieces swizzled by token so that both reads are free of
+// bank conflicts) while the previous tile is computed on: directly where a tile of a BF16 cache lies in one page,
+// else through registers, in which E4M3 caches become BF16 (exactly); their scales go into c and the result.
+//
+// Bound (40 heads on 8 cache heads of 128): a long cache by the matrix instructions, their operand reads from LDS
+// and the exponentials, which run partly beside each other (64 nodes over 131001 tokens: 222 us, 770 TFLOP/s,
+// 2.4 TB/s); a short one by the loop's start, the partial results and the second launch (63 nodes over 8191:
+// 28 us; one over 509: 11).
 #include <type_traits>
 
 #include "w12_device.h"
@@ -40,8 +46,11 @@ constexpr int kBlockRows = 128;      // rows of a block
 constexpr int kMaxRequests = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;       // log2 of the largest p that a stale maximum may give
-constexpr int kMinChunk = 2;         // least tiles of a chunk where all rows are up to 64,
-constexpr int kMinChunkLarge = 4;    // and elsewhere: a partial result is as large as 2 tiles
+// Least tiles of a chunk where all rows are up to 64 (twice as many for more than 32 chunks: one node over 8191 tokens
+// 19.0 -> 16.3 us, 12 nodes 25 -> 19, but 2047 tokens 12.1 -> 12.9), and elsewhere, where a partial result is as
+// large as 2 tiles (63 nodes over 2047 tokens 19.2 us, with 6 tiles 19.9; over 8191 the same).
+constexpr int kMinChunk = 2;
+constexpr int kMinChunkLarge = 4;
 
 // One request: its rows and lengths, cut to what is there.
 struct Request {
@@ -135,7 +144,8 @@ __device__ __forceinline__ int chunk_of(int64_t cost, int target, int rows) {
 
 // Tiles of a chunk of one request, whose items (per = heads x blocks, for each chunk) are about equally long: they
 // go in whole rounds of the `slots` work-groups that the chip holds, the fewest that leave at most a quarter of the
-// slots empty; a few items over a round would cost another one.
+// slots empty; a few items over a round would cost another one (63 nodes over 8191 tokens in one round 29.7 us,
+// with the chunks of chunk_of 34.8; over 32767 70 and 87, 64 nodes over 131001 234 and 246).
 __device__ __forceinline__ int one_request_chunk(const Blocks& k, int slots, int per, int rows) {
   int chunks = 1;
   for (int rounds = 1; rounds <= 4; ++rounds) {
@@ -821,8 +831,9 @@ __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12
   if (a.lse && quad == 0 && hi == 0) a.lse[row * a.ld_lse + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) / kLog2e;
 }
 
-// Items of four waves that a call aims at: two rounds of the work-groups that the chip holds at once (two a
-// compute unit, one where a head of 256 takes its LDS).
+// Items of four waves that requests that share the chip aim at: two rounds of the work-groups that it holds at once (two
+// a compute unit, one where a head of 256 takes its LDS).  16 requests of 24 nodes over up to 8000 tokens: E4M3
+// 87 us, with one round 99, with four 94; BF16 107, 114 and 113.
 static int attention_target(int D) { return 2 * device_cus() * (D == 256 ? 1 : 2); }
 // Groups of 32 rows that a block can hold.
 static int attention_row_groups(int32_t T, int32_t q_heads, const w12_kv_cache& c) {
@@ -845,7 +856,8 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   const int64_t groups = attention_most_items(a.T, a.requests, a.q_heads, c);
   const int target = attention_target(D);
   const int rg = attention_row_groups(a.T, a.q_heads, c);
-  // tiles inside one page, with a thread's offsets in 32 bits
+  // tiles inside one page, with a thread's offsets in 32 bits (looked up token by token instead: 63 nodes over 32767
+  // tokens 98 us for 87, with heads of 256 over 8191 46 for 32)
   const bool whole = c.page_size >= kTile && c.token_stride <= (int64_t(1) << 24);
   const dim3 g((unsigned)groups), t(kAttnThreads);
   if (whole) hipLaunchKernelGGL((k_tree_attention<D, F8, true>), g, t, 0, stream, a, c, ws, rg, target);
@@ -853,8 +865,8 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t row_blocks = ceil_div((int64_t)a.T * (a.q_heads / c.heads), 32) + a.requests;
-  // few rows: waves share the parts (63 nodes over 8191 tokens 11.4 -> 7.7 us); many: they share the work of finding
-  // the request, and a wave's parts are few (16 requests of 24 nodes 29 -> 13 us)
+  // few rows: waves share the parts (12 nodes over 8191 tokens 25 us, else 32; one node 19 and 26); many: they share the
+  // work of finding the request, and a wave's parts are few (16 requests of 24 nodes 107 us, else 126)
   const unsigned x = (unsigned)row_blocks, y = (unsigned)c.heads;
   if (row_blocks * c.heads < device_cus())
     hipLaunchKernelGGL((k_join<D, F8, true>), dim3(x, y, D / 8), t, 0, stream, a, c, (const float*)ws, rg, target);

@@ -3,7 +3,8 @@
 // Pair i of a head turns by theta = positions[axis(i)][t] * inv_freq[i]:
 //   (a, b) -> (a cos theta - b sin theta, a sin theta + b cos theta).
 // The angle is formed in FP64 as a number of turns and reduced there to half a turn either way,
-// so a far position loses nothing; its sine and cosine are FP32.
+// so a far position loses nothing; its sine and cosine are FP32.  Bound: the launch, then positions -> sines -> the
+// turn one after another (512 rows of 56 heads of 128, 18 MB: 7.6 us; one row: 7.4, of which the kernel 2.7).
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"
