@@ -3,8 +3,8 @@
 // The rows of a request that read one cache head (node i, query head g: row i * group + g) are cut
 // into blocks of 128, the tokens into tiles of 64 and the tiles into chunks.  A work-group takes one
 // block over one chunk; the length of a chunk is the same for all requests, chosen on the device: of one
-// request so that the items make whole rounds of the chip, of several so that they fill it
-// about evenly (unequal lengths give unequal numbers of items).  Items are numbered
+// request so that the items make whole rounds of the chip, of several one round, or, if they are many, so that
+// they fill it about evenly (unequal lengths give unequal numbers of items).  Items are numbered
 // request, head, chunk, block, and neighbouring numbers run on one XCD: the blocks of a chunk read its
 // keys and values together, once from memory.  Blocks of several chunks leave partial results, which
 // k_join adds in the order of the chunks.
@@ -136,16 +136,20 @@ __device__ __forceinline__ float other_half(float v) {
   return __builtin_bit_cast(float, (threadIdx.x & 32) ? sw[0] : sw[1]);
 }
 
-// Tiles of a chunk where requests share the chip: the cost of all tiles over `target` items of four waves.
-__device__ __forceinline__ int chunk_of(int64_t cost, int target, int rows) {
-  const int64_t even = (cost + 4 * (int64_t)target - 1) / (4 * (int64_t)target);
-  return (int)max(even, (int64_t)(rows <= kBlockRows / 2 ? kMinChunk : kMinChunkLarge));
+// Tiles of a chunk where requests share the chip: the cost of all tiles over `share`.  Where twice the blocks of all heads
+// fit the chip, all items make one round: the cost is a tile of a block, half a chunk for each block is set
+// aside for last chunks that are short, and a chunk that still gives too many items is lengthened by eighths, up to
+// three times (16 requests of 24 nodes over up to 8000 tokens, in one round and in about two: E4M3 76 / 84 us, BF16 94 /
+// 106; 8 of 40 nodes, E4M3, 61 / 75; 32 of 8 nodes over 4000 90 / 114).  Otherwise two rounds, whose items even out
+// unequal lengths, the cost is that of four waves.
+__device__ __forceinline__ int chunk_of(int64_t cost, int64_t share, int rows) {
+  return (int)max((cost + share - 1) / share, (int64_t)(rows <= kBlockRows / 2 ? kMinChunk : kMinChunkLarge));
 }
 
 // Tiles of a chunk of one request, whose items (per = heads x blocks, for each chunk) are about equally long: they
 // go in whole rounds of the `slots` work-groups that the chip holds, the fewest that leave at most a quarter of the
 // slots empty; a few items over a round would cost another one (63 nodes over 8191 tokens in one round 29.7 us,
-// with the chunks of chunk_of 34.8; over 32767 70 and 87, 64 nodes over 131001 234 and 246).
+// as several requests are 34.8; over 32767 70 and 87, 64 nodes over 131001 234 and 246).
 __device__ __forceinline__ int one_request_chunk(const Blocks& k, int slots, int per, int rows) {
   int chunks = 1;
   for (int rounds = 1; rounds <= 4; ++rounds) {
@@ -174,13 +178,21 @@ __device__ __forceinline__ Plan plan_items(const w12_attention_args& a, const w1
     p.chunk = one_request_chunk(k, target / 2, c.heads * k.count(), a.T * group);
     p.items = items_of(k, c.heads, p.chunk);
   } else {
+    const int slots = target / 2;
+    const int64_t wanted = (int64_t)c.heads * max(a.requests, (a.T * group + kBlockRows - 1) / kBlockRows);
+    const bool round = 2 * wanted <= slots;
     const int64_t cost = uniform(prefix_requests(a.requests, before, sums, [&](int b) {
-      return blocks_of(request_of(a, c.page_size, b), group).cost() * c.heads;
+      const Blocks k = blocks_of(request_of(a, c.page_size, b), group);
+      return c.heads * (round ? (int64_t)k.tiles * k.count() : k.cost());
     }));
-    p.chunk = chunk_of(cost, target, a.T * group);
-    p.items = uniform(prefix_requests(a.requests, before, sums, [&](int b) {
-      return items_of(blocks_of(request_of(a, c.page_size, b), group), c.heads, p.chunk);
-    }));
+    p.chunk = chunk_of(cost, round ? slots - wanted / 2 : 4 * (int64_t)target, a.T * group);
+    for (int tries = 0;; ++tries) {
+      p.items = uniform(prefix_requests(a.requests, before, sums, [&](int b) {
+        return items_of(blocks_of(request_of(a, c.page_size, b), group), c.heads, p.chunk);
+      }));
+      if (!round || p.items <= slots || tries == 3) break;
+      p.chunk += (p.chunk + 7) / 8;
+    }
   }
   return p;
 }
@@ -831,9 +843,8 @@ __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12
   if (a.lse && quad == 0 && hi == 0) a.lse[row * a.ld_lse + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) / kLog2e;
 }
 
-// Items of four waves that requests that share the chip aim at: two rounds of the work-groups that it holds at once (two
-// a compute unit, one where a head of 256 takes its LDS).  16 requests of 24 nodes over up to 8000 tokens: E4M3
-// 87 us, with one round 99, with four 94; BF16 107, 114 and 113.
+// Items of four waves of two rounds of the work-groups that the chip holds at once (two a compute unit, one where a head
+// of 256 takes its LDS).
 static int attention_target(int D) { return 2 * device_cus() * (D == 256 ? 1 : 2); }
 // Groups of 32 rows that a block can hold.
 static int attention_row_groups(int32_t T, int32_t q_heads, const w12_kv_cache& c) {
@@ -841,7 +852,8 @@ static int attention_row_groups(int32_t T, int32_t q_heads, const w12_kv_cache& 
   return (int)(rows >= kBlockRows ? kBlockRows / 32 : ceil_div(rows, 32));
 }
 // Most items of a call.  Chunks are at least cost / (4 target) long and a tile costs at least 2, so whole chunks are
-// at most 2 target; each head of each block has at most one more.
+// at most 2 target; each head of each block has at most one more.  One request's items are at most four rounds, 2
+// target, or one for each head of each block.
 static int64_t attention_most_items(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache& c) {
   const int64_t blocks = ceil_div((int64_t)T * (q_heads / c.heads), kBlockRows) + requests;
   return 2 * (int64_t)attention_target(c.dim) + blocks * c.heads;
