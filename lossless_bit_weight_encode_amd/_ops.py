@@ -1,7 +1,8 @@
 """Binding of the operators around the products: residual RMS norm, rotary cache write, tree attention
 and the 8-bit block product.  Argument marshalling only, as in ``_lib``: every call checks that its
-tensors are on one GPU and have the shapes and types of the C ABI (include/w12.h), enqueues on the
-current stream (or ``stream``) and returns; pitches and alignment are checked by the library."""
+tensors are on one GPU, before it allocates or enqueues anything, and that they have the shapes and types of
+the C ABI (include/w12.h), enqueues on the current stream (or ``stream``) and returns; pitches and alignment
+are checked by the library."""
 from __future__ import annotations
 
 import ctypes
@@ -83,10 +84,10 @@ def add_rmsnorm(residual: torch.Tensor, weight: torch.Tensor, delta: torch.Tenso
     gemm_e4m3() takes) are the outputs that are wanted; with none given, y is allocated here, on the
     stream.  Returns y (None when only yq is wanted)."""
     m, n = _matrix2(residual, "residual")
+    _device(residual, weight, delta, residual_out, y, yq, yq_scale)
     if y is None and yq is None:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             y = torch.empty(m, (n + 7) // 8 * 8, dtype=_BF16, device=residual.device)[:, :n]
-    _device(residual, weight, delta, residual_out, y, yq, yq_scale)
     shape = (m, n)
     rt = residual.dtype
     step = 4 if rt == _F32 else 8
@@ -157,10 +158,10 @@ def rope_append(qkv: torch.Tensor, cache: KVCache, positions: torch.Tensor, slot
     dim = cache.dim
     if width != (q_heads + 2 * cache.heads) * dim:
         raise ValueError(f"qkv: expected {(q_heads + 2 * cache.heads) * dim} columns, got {width}")
+    _device(qkv, cache.k, positions, slots, inv_freq, axis, q)
     if q is None:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             q = torch.empty(t, q_heads * dim, dtype=_BF16, device=qkv.device)
-    _device(qkv, cache.k, positions, slots, inv_freq, axis, q)
     ld_x = _rows(qkv, "qkv", (t, width), _FLOATS, 8)
     axes = _matrix2(positions, "positions")[0]
     ld_p = _rows(positions, "positions", (axes, t), (torch.int32,), 1)
@@ -206,13 +207,13 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ct
     q_heads = width // dim
     if q_heads * dim != width or q_heads == 0:
         raise ValueError(f"q: {width} columns are not whole heads of {dim}")
+    _device(q, cache.k, page_table, ctx_len, node_ptr, tree_mask, out, lse, ws)
     if out is None or ws is None:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             if out is None:
                 out = torch.empty(t, width, dtype=_BF16, device=q.device)
             if ws is None:
                 ws = tree_attention_workspace(t, ctx_len.numel(), q_heads, cache)
-    _device(q, cache.k, page_table, ctx_len, node_ptr, tree_mask, out, lse, ws)
     requests = ctx_len.numel()
     _vector(ctx_len, "ctx_len", requests, torch.int32)
     _vector(node_ptr, "node_ptr", requests + 1, torch.int32)
@@ -243,6 +244,11 @@ def gemm_e4m3_workspace_size(m: int, n: int, k: int) -> int:
 
 def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
     """A ready-to-use (zero-initialised) workspace for gemm_e4m3() with M=m on W[n][k], or None."""
+    d = torch.device(device)
+    if d.type != "cuda":
+        raise ValueError("tensors must live on the GPU (libw12 has no CPU path)")
+    if d.index is not None and d.index != torch.cuda.current_device():
+        raise ValueError("the tensors' GPU is not the current one (use torch.cuda.device)")
     need = gemm_e4m3_workspace_size(m, n, k)
     if not need:
         return None
@@ -258,13 +264,13 @@ def gemm_e4m3(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     m, k = _matrix2(x, "x")
     n = _matrix2(w, "w")[0]
     kb = -(-k // QUANT_BLOCK)
+    _device(x, x_scale, w, w_scale, y, ws)
     if y is None or ws is None:
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             if y is None:
                 y = torch.empty(m, n, dtype=_F32, device=x.device)
             if ws is None:
                 ws = gemm_e4m3_workspace(m, n, k, x.device)
-    _device(x, x_scale, w, w_scale, y, ws)
     wsp, wsb = (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
     _check("w12_gemm_e4m3", lib().w12_gemm_e4m3(
         x.data_ptr(), m, _rows(x, "x", (m, k), (_E4M3,), 16),
