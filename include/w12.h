@@ -315,10 +315,11 @@ int w12_read_probe(const void *buf, uint64_t bytes, int32_t loads_per_lane, int3
  *                 (in place) but may not overlap it otherwise.
  *   y             BF16 (an operand of w12_gemm), or NULL.
  *   yq, yq_scale  E4M3 with one FP32 scale per row and block of 128 columns (an operand of
- *                 w12_gemm_e4m3), or both NULL: yq_scale[m][b] = max|y| of the block / 448 (1 for
- *                 a block of zeros), yq = y / yq_scale rounded to nearest even.  y is taken before
- *                 it is rounded to BF16.  A NaN or infinity in a block makes its scale NaN or
- *                 infinite.
+ *                 w12_gemm_e4m3), or both NULL: yq_scale[m][b] = max|y| of the block / 448 (1
+ *                 where that is 0 in FP32: a block of zeros, or of nothing above 3.1e-43),
+ *                 yq = y / yq_scale rounded to nearest even, cut off at +-448 (a scale below the
+ *                 normal range is rounded coarsely).  y is taken before it is rounded to BF16.  A
+ *                 NaN or infinity in a block makes its scale NaN or infinite.
  * At least one of y, yq and residual_out with a delta is wanted.  1 <= M <= 2^20, 1 <= N <= 65536.
  */
 typedef struct w12_norm_args {

@@ -66,7 +66,9 @@ __global__ __launch_bounds__(kNormMaxThreads) void k_add_rmsnorm(w12_norm_args a
 #pragma unroll
       for (int o = 8; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
       const float amax = __builtin_bit_cast(float, top);
-      const float scale = top ? amax / kE4M3Max : 1.0f;
+      // of a block of zeros, or one so small that the quotient leaves the subnormal range, 0: a scale of 1 rounds it to zeros
+      const float least = amax / kE4M3Max;
+      const float scale = least == 0.0f ? 1.0f : least;
       if ((t & 15) == 0 && i < N) a.yq_scale[m * a.ld_scale + i / W12_QUANT_BLOCK] = scale;
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] /= scale;

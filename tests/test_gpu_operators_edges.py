@@ -1,0 +1,51 @@
+"""GPU tests of the operators around the products at the ends of their ranges, against their formulas in 64 bits."""
+import pytest
+import torch
+
+import lossless_bit_weight_encode_amd as w12
+
+pytestmark = pytest.mark.gpu
+
+BF, F32, F8 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+E24, Q4 = 2.0 ** -24, 2.0 ** -4
+
+
+def rnd(seed, *shape, scale=1.0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale
+
+
+@pytest.mark.parametrize("rt", [F32, BF])
+def test_norm_blocks_whose_scale_is_subnormal_or_rounds_to_zero(rt):
+    """Blocks of 128 with largest magnitudes from 1e-45 to 1e-36 beside zeros, in rows with one large value: finite
+    outputs that stand for the values.  The scale is off by half the smallest FP32 step, 2^-150, which its largest
+    multiple, 448, carries into a value (cut off, or lost with a scale of 0); y itself has such steps."""
+    n, m = 640, 12
+    r = torch.zeros(m, n)
+    r[:, 0] = 1000.0
+    for i in range(m):
+        r[i, 128:180] = rnd(i, 52).clamp(-1, 1) * 10.0 ** (-43.5 + 0.75 * i)      # y: 0.0253 times that
+    r = r.to(rt)
+    w = torch.ones(n)
+    w[256:384] = 1e-40                  # tiny weights, over zeros and over the values set next
+    w[384:512] = 0
+    r[:, 300:310] = 0.01
+    w = w.to(BF)
+    y = torch.empty(m, n, dtype=BF, device="cuda")
+    yq = torch.empty(m, n, dtype=F8, device="cuda")
+    sc = torch.empty(m, 5, device="cuda")
+    w12.add_rmsnorm(r.cuda(), w.cuda(), y=y, yq=yq, yq_scale=sc, eps=1e-6)
+    assert y.isfinite().all() and yq.float().isfinite().all(), "NaN from finite rows"
+    x = r.double()
+    ref = x / torch.sqrt((x * x).mean(1, keepdim=True) + 1e-6) * w.double()
+    sc, yq = sc.cpu().double(), yq.cpu().double()
+    least = ref.view(m, 5, 128).abs().amax(2) / 448
+    assert (sc > 0).all() and sc.isfinite().all()
+    assert (sc[(least == 0)] == 1).all()
+    got = yq * sc.repeat_interleave(128, 1)
+    tol = (Q4 + 4 * (n + 12) * E24) * ref.abs() + 2.0 ** -10 * least.repeat_interleave(128, 1) + 450 * 2.0 ** -149
+    assert ((got - ref).abs() <= tol).all()
+    assert (yq[ref == 0] == 0).all()
+    # and a product of these rows is finite
+    w8 = rnd(99, 128, n, scale=50.0).clamp(-448, 448).to(F8).cuda()
+    out = w12.gemm_e4m3(yq.to(F8).cuda(), sc.float().cuda(), w8, torch.full((1, 5), 1e-3, device="cuda"))
+    assert out.isfinite().all()
