@@ -402,7 +402,8 @@ int w12_rope_append(const w12_rope_args *a, const w12_kv_cache *cache, hipStream
  * What a row does not attend never reaches it, NaN and infinity included.  A row that attends
  * nothing, or whose scores are all -inf, gives zeros and lse -inf.  Tokens past max_pages * page_size, and tokens whose page is
  * not in 0 .. pages - 1, count as absent.  Rows outside every request are left as they are;
- * ranges of node_ptr are cut to 0..T and must not decrease; negative lengths count as 0.
+ * ranges of node_ptr are cut to 0..T and must not decrease (where they do, out and lse of the rows hold
+ * anything, and nothing else is written); negative lengths count as 0.
  * node_ptr, ctx_len, page_table and tree_mask are device memory read by the kernels (a captured
  * graph follows their values).  The result is bitwise the same from run to run.
  * 1 <= T <= 2^20, 1 <= requests <= 1024, q_heads a multiple of heads (at most 64 times heads),

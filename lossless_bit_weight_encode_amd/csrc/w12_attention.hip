@@ -602,7 +602,7 @@ __device__ __forceinline__ void add_bad_tokens(const w12_attention_args& a, cons
 
 template <int D, bool F8, bool WHOLE>
 __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attention(w12_attention_args a, w12_kv_cache c,
-                                                                                    float* ws, int row_groups, int target) {
+                                                                                    float* ws, int row_groups, int target, int64_t most) {
   using T = Tile<D, F8>;
   __shared__ Lds<D> lds;
   const int group = a.q_heads / c.heads;
@@ -612,6 +612,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
   const int64_t x8 = blockIdx.x % 8, q8 = plan.items / 8, r8 = plan.items % 8, i8 = blockIdx.x / 8;
   if (i8 >= q8 + (x8 < r8)) return;
   const int64_t item = x8 * q8 + min(x8, r8) + i8;
+  if (item >= most) return;      // ranges of node_ptr that decrease overlap: more items than the workspace has places for
   const int b = a.requests == 1 ? 0 : uniform(find_request(lds.before, a.requests, item));
   const Request rq = request_of(a, c.page_size, b);
   const Blocks bl = blocks_of(rq, group);
@@ -760,7 +761,7 @@ __global__ __launch_bounds__(kAttnThreads, D == 256 ? 1 : 2) void k_tree_attenti
 // the order is the same every time, and with it every bit.
 template <int D, bool F8, bool SPLIT>
 __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12_kv_cache c, const float* ws,
-                                                       int row_groups, int target) {
+                                                       int row_groups, int target, int64_t most) {
   constexpr int kWaves = kAttnThreads / 64;
   __shared__ int64_t before[kMaxRequests + 1], rows_before[kMaxRequests + 1], sums[kWaves];
   __shared__ float quarter[SPLIT ? kWaves : 1][6][64];
@@ -784,6 +785,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_join(w12_attention_args a, w12
   const int lane = threadIdx.x & 63, col = lane & 31, hi = lane >> 5;
   // the block's items: one a chunk, count() apart
   const int64_t item0 = (a.requests > 1 ? uniform(before[b]) : 0) + (int64_t)h * chunks * bl.count() + rb;
+  if (item0 + (int64_t)(chunks - 1) * bl.count() >= most) return;
   const int64_t slot = slot_floats(D, row_groups) * 4, step = slot * bl.count();
   const char* part = reinterpret_cast<const char*>(ws) + item0 * slot;
   const uint32_t ml_off = (uint32_t)(row_groups * 32 * D * 4 + (rg * 32 + col) * 8);
@@ -872,8 +874,8 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   // tokens 98 us for 87, with heads of 256 over 8191 46 for 32)
   const bool whole = c.page_size >= kTile && c.token_stride <= (int64_t(1) << 24);
   const dim3 g((unsigned)groups), t(kAttnThreads);
-  if (whole) hipLaunchKernelGGL((k_tree_attention<D, F8, true>), g, t, 0, stream, a, c, ws, rg, target);
-  else hipLaunchKernelGGL((k_tree_attention<D, F8, false>), g, t, 0, stream, a, c, ws, rg, target);
+  if (whole) hipLaunchKernelGGL((k_tree_attention<D, F8, true>), g, t, 0, stream, a, c, ws, rg, target, groups);
+  else hipLaunchKernelGGL((k_tree_attention<D, F8, false>), g, t, 0, stream, a, c, ws, rg, target, groups);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t row_blocks = ceil_div((int64_t)a.T * (a.q_heads / c.heads), 32) + a.requests;
@@ -881,9 +883,9 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   // work of finding the request, and a wave's parts are few (16 requests of 24 nodes 107 us, else 126)
   const unsigned x = (unsigned)row_blocks, y = (unsigned)c.heads;
   if (row_blocks * c.heads < device_cus())
-    hipLaunchKernelGGL((k_join<D, F8, true>), dim3(x, y, D / 8), t, 0, stream, a, c, (const float*)ws, rg, target);
+    hipLaunchKernelGGL((k_join<D, F8, true>), dim3(x, y, D / 8), t, 0, stream, a, c, (const float*)ws, rg, target, groups);
   else
-    hipLaunchKernelGGL((k_join<D, F8, false>), dim3(x, y, D / 32), t, 0, stream, a, c, (const float*)ws, rg, target);
+    hipLaunchKernelGGL((k_join<D, F8, false>), dim3(x, y, D / 32), t, 0, stream, a, c, (const float*)ws, rg, target, groups);
   return hipGetLastError();
 }
 

@@ -49,3 +49,38 @@ def test_norm_blocks_whose_scale_is_subnormal_or_rounds_to_zero(rt):
     w8 = rnd(99, 128, n, scale=50.0).clamp(-448, 448).to(F8).cuda()
     out = w12.gemm_e4m3(yq.to(F8).cuda(), sc.float().cuda(), w8, torch.full((1, 5), 1e-3, device="cuda"))
     assert out.isfinite().all()
+
+
+def test_attention_with_decreasing_ranges_stays_inside_its_workspace():
+    """Ranges 0..T, T..0, 0..T ... overlap: 16000 items of short requests and 450 of a long one whose chunks leave
+    partial results, where the workspace has 10080 places.  What the rows get is open; nothing behind the
+    workspace, the output and lse is touched, and the next call is right."""
+    t, requests, heads, d, page, long = 512, 1000, 8, 64, 64, 910
+    k, v = (torch.randn(4, page, heads, d, dtype=BF, device="cuda") for _ in range(2))
+    cache = w12.KVCache(k, v)
+    q = torch.randn(t, heads * d, dtype=BF, device="cuda")
+    ptr = torch.zeros(requests + 1, dtype=torch.int32, device="cuda")
+    ptr[1::2] = t
+    ctx = torch.zeros(requests, dtype=torch.int32, device="cuda")
+    ctx[long] = 3000 * page
+    table = torch.zeros(requests, 3010, dtype=torch.int32, device="cuda")
+    need = w12.tree_attention_workspace_size(t, requests, heads, cache)
+    guard = 8 << 20
+    ws = torch.full((need + guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = torch.empty(2 * t, heads * d, dtype=BF, device="cuda").fill_(7.0)
+    lse = torch.full((2 * t, heads), 7.0, device="cuda")
+    torch.cuda.synchronize()
+    w12.tree_attention(q, cache, table, ctx, ptr, out=out[:t], lse=lse[:t], ws=ws[:need])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0x5A).all() and (out[t:] == 7).all() and (lse[t:] == 7).all()
+    # one request of all rows over the first page, as a chain behind 64 tokens
+    p1, c1 = torch.tensor([0, t], dtype=torch.int32, device="cuda"), torch.tensor([64], dtype=torch.int32, device="cuda")
+    t1 = (torch.arange(9, dtype=torch.int32, device="cuda") % 4)[None].contiguous()
+    got = w12.tree_attention(q, cache, t1, c1, p1).cpu().double().view(t, heads, d)
+    kk, vv = (x.cpu().double()[t1[0].long().cpu()].reshape(-1, heads, d)[:64 + t] for x in (k, v))
+    for row in (0, 1, 255, 511):
+        s = torch.einsum("hd,thd->ht", q[row].cpu().double().view(heads, d), kk[:65 + row]) * d ** -0.5
+        p = torch.softmax(s, 1)
+        ref, mag = torch.einsum("ht,thd->hd", p, vv[:65 + row]), torch.einsum("ht,thd->hd", p, vv[:65 + row].abs())
+        # the result and p rounded to BF16 (2^-8 each); scores and sums of hundreds of terms in FP32
+        assert ((got[row] - ref).abs() <= ref.abs() * 2.0 ** -8 + mag * (2.0 ** -8 * 1.01 + 4 * 1024 * E24)).all()
