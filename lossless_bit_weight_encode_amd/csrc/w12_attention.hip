@@ -27,6 +27,7 @@
 // 28 us; one over 509: 11).
 #include <type_traits>
 
+#include "w12_attention_plan.h"
 #include "w12_device.h"
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
@@ -41,16 +42,9 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
 constexpr int kAttnThreads = 256;
-constexpr int kTile = 64;            // tokens of a tile
-constexpr int kBlockRows = 128;      // rows of a block
 constexpr int kMaxRequests = 1024;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;       // log2 of the largest p that a stale maximum may give
-// Least tiles of a chunk where all rows are up to 64 (twice as many for more than 32 chunks: one node over 8191 tokens
-// 19.0 -> 16.3 us, 12 nodes 25 -> 19, but 2047 tokens 12.1 -> 12.9), and elsewhere, where a partial result is as
-// large as 2 tiles (63 nodes over 2047 tokens 19.2 us, with 6 tiles 19.9; over 8191 the same).
-constexpr int kMinChunk = 2;
-constexpr int kMinChunkLarge = 4;
 
 // One request: its rows and lengths, cut to what is there.
 struct Request {
@@ -67,22 +61,7 @@ __device__ __forceinline__ Request request_of(const w12_attention_args& a, int p
   return r;
 }
 
-// The blocks of a request: `full` of 128 rows, and a last one of `rest` waves' rows (0: none; 2: up to 64, whose
-// other two waves take half of the tokens; 4).  A tile of a block costs its waves.
-struct Blocks {
-  int tiles, full, rest;
-  __device__ int count() const { return full + (rest != 0); }
-  __device__ int64_t cost() const { return (int64_t)tiles * (4 * full + rest); }
-};
-
-__device__ __forceinline__ Blocks blocks_of(const Request& r, int group) {
-  Blocks c;
-  const int rows = r.nodes * group, rem = rows % kBlockRows;
-  c.tiles = (r.len + kTile - 1) / kTile;
-  c.full = rows / kBlockRows;
-  c.rest = rem == 0 ? 0 : rem <= kBlockRows / 2 ? 2 : 4;
-  return c;
-}
+__device__ __forceinline__ Blocks blocks_of(const Request& r, int group) { return blocks_of(r.nodes * group, r.len); }
 
 // Running sums over the requests, value(b) of each, into LDS (before[b], before[requests] the total).
 template <typename F>
@@ -136,65 +115,12 @@ __device__ __forceinline__ float other_half(float v) {
   return __builtin_bit_cast(float, (threadIdx.x & 32) ? sw[0] : sw[1]);
 }
 
-// Tiles of a chunk where requests share the chip: the cost of all tiles over `share`.  Where twice the blocks of all heads
-// fit the chip, all items make one round: the cost is a tile of a block, half a chunk for each block is set
-// aside for last chunks that are short, and a chunk that still gives too many items is lengthened by eighths, up to
-// three times (16 requests of 24 nodes over up to 8000 tokens, in one round and in about two: E4M3 76 / 84 us, BF16 94 /
-// 106; 8 of 40 nodes, E4M3, 61 / 75; 32 of 8 nodes over 4000 90 / 114).  Otherwise two rounds, whose items even out
-// unequal lengths, the cost is that of four waves.
-__device__ __forceinline__ int chunk_of(int64_t cost, int64_t share, int rows) {
-  return (int)max((cost + share - 1) / share, (int64_t)(rows <= kBlockRows / 2 ? kMinChunk : kMinChunkLarge));
-}
-
-// Tiles of a chunk of one request, whose items (per = heads x blocks, for each chunk) are about equally long: they
-// go in whole rounds of the `slots` work-groups that the chip holds, the fewest that leave at most a quarter of the
-// slots empty; a few items over a round would cost another one (63 nodes over 8191 tokens in one round 29.7 us,
-// as several requests are 34.8; over 32767 70 and 87, 64 nodes over 131001 234 and 246).
-__device__ __forceinline__ int one_request_chunk(const Blocks& k, int slots, int per, int rows) {
-  int chunks = 1;
-  for (int rounds = 1; rounds <= 4; ++rounds) {
-    chunks = max(rounds * slots / max(per, 1), 1);
-    if (4 * chunks * per >= 3 * rounds * slots) break;
-  }
-  const int least = rows <= kBlockRows / 2 ? min(max((k.tiles + 31) / 32, kMinChunk), 2 * kMinChunk) : kMinChunkLarge;
-  return max((k.tiles + chunks - 1) / chunks, least);
-}
-
 // The items of a call.  `before` (LDS) holds the number of items before each request; one request needs none.
-struct Plan {
-  int64_t items;
-  int chunk;       // tiles of a chunk
-};
-
-__device__ __forceinline__ int64_t items_of(const Blocks& c, int heads, int chunk) {
-  return (int64_t)heads * c.count() * ((c.tiles + chunk - 1) / chunk);
-}
-
 __device__ __forceinline__ Plan plan_items(const w12_attention_args& a, const w12_kv_cache& c, int group, int target, int64_t* before,
                                            int64_t* sums) {
-  Plan p;
-  if (a.requests == 1) {
-    const Blocks k = blocks_of(request_of(a, c.page_size, 0), group);
-    p.chunk = one_request_chunk(k, target / 2, c.heads * k.count(), a.T * group);
-    p.items = items_of(k, c.heads, p.chunk);
-  } else {
-    const int slots = target / 2;
-    const int64_t wanted = (int64_t)c.heads * max(a.requests, (a.T * group + kBlockRows - 1) / kBlockRows);
-    const bool round = 2 * wanted <= slots;
-    const int64_t cost = uniform(prefix_requests(a.requests, before, sums, [&](int b) {
-      const Blocks k = blocks_of(request_of(a, c.page_size, b), group);
-      return c.heads * (round ? (int64_t)k.tiles * k.count() : k.cost());
-    }));
-    p.chunk = chunk_of(cost, round ? slots - wanted / 2 : 4 * (int64_t)target, a.T * group);
-    for (int tries = 0;; ++tries) {
-      p.items = uniform(prefix_requests(a.requests, before, sums, [&](int b) {
-        return items_of(blocks_of(request_of(a, c.page_size, b), group), c.heads, p.chunk);
-      }));
-      if (!round || p.items <= slots || tries == 3) break;
-      p.chunk += (p.chunk + 7) / 8;
-    }
-  }
-  return p;
+  return plan_of(
+      a.requests, c.heads, a.T * group, target, [&](int b) { return blocks_of(request_of(a, c.page_size, b), group); },
+      [&](auto value) { return uniform(prefix_requests(a.requests, before, sums, value)); });
 }
 
 __host__ __device__ constexpr int64_t slot_floats(int D, int row_groups) { return (int64_t)row_groups * 32 * (D + 2); }
@@ -853,12 +779,8 @@ static int attention_row_groups(int32_t T, int32_t q_heads, const w12_kv_cache& 
   const int64_t rows = (int64_t)T * (q_heads / c.heads);
   return (int)(rows >= kBlockRows ? kBlockRows / 32 : ceil_div(rows, 32));
 }
-// Most items of a call.  Chunks are at least cost / (4 target) long and a tile costs at least 2, so whole chunks are
-// at most 2 target; each head of each block has at most one more.  One request's items are at most four rounds, 2
-// target, or one for each head of each block.
 static int64_t attention_most_items(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache& c) {
-  const int64_t blocks = ceil_div((int64_t)T * (q_heads / c.heads), kBlockRows) + requests;
-  return 2 * (int64_t)attention_target(c.dim) + blocks * c.heads;
+  return most_items((int64_t)T * (q_heads / c.heads), requests, c.heads, attention_target(c.dim));
 }
 
 uint64_t attention_workspace_bytes(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache& c) {

@@ -1,6 +1,8 @@
 """Host-side checks of the operators' binding and schedules: what has to happen before anything is launched, and
 what a launch is sized for.  No GPU is touched."""
 import contextlib
+import os
+import subprocess
 
 import pytest
 import torch
@@ -64,3 +66,69 @@ def test_nothing_is_launched_before_the_tensors_are_checked(recorder, monkeypatc
     with pytest.raises(ValueError, match="GPU"):
         call(torch.bfloat16, torch.float8_e4m3fn)
     assert recorder.calls == [] and made == []
+
+
+PLAN_MAIN = r"""
+#include <cstdio>
+#include <random>
+#include <vector>
+#include "w12_attention_plan.h"
+using namespace w12;
+// Plans a call and prints how it was cut; false where an item has no tile, the workspace no place for it, or the sums differ.
+static bool plan(const std::vector<int>& nodes, const std::vector<int>& lens, int heads, int group, int target, bool show) {
+  int64_t T = 0;
+  for (int n : nodes) T += n;
+  const int requests = (int)nodes.size();
+  auto blocks = [&](int b) { return blocks_of(nodes[b] * group, lens[b]); };
+  auto sum = [&](auto value) { int64_t s = 0; for (int b = 0; b < requests; ++b) s += value(b); return s; };
+  const Plan p = plan_of(requests, heads, (int)(T * group), target, blocks, sum);
+  const int64_t most = most_items(T * group, requests, heads, target);
+  const int64_t items = p.chunk > 0 ? sum([&](int b) { return items_of(blocks(b), heads, p.chunk); }) : -1;
+  const bool ok = p.chunk >= kMinChunk && items == p.items && p.items <= most;
+  if (show || !ok)
+    std::printf("%s requests %d heads %d group %d T %lld len %d: chunk %d items %lld of %lld\n", ok ? "ok" : "BAD", requests, heads,
+                group, (long long)T, lens[0], p.chunk, (long long)p.items, (long long)most);
+  return ok;
+}
+int main() {
+  bool ok = true;
+  // the largest lengths of every request, and of one beside short ones
+  for (int heads : {8, 128, 1024})
+    for (int target : {512, 1024}) {
+      ok &= plan(std::vector<int>(1024, 1), std::vector<int>(1024, (1 << 30) - 1), heads, 1, target, true);
+      ok &= plan(std::vector<int>(1024, 1024), std::vector<int>(1024, (1 << 30) - 1), heads, 1, target, true);
+      std::vector<int> one(1000, 3);
+      one[7] = (1 << 30) - 1;
+      ok &= plan(std::vector<int>(1000, 2), one, heads, 4, target, true);
+      ok &= plan({64}, {(1 << 30) - 1}, heads, 5, target, true);
+    }
+  std::mt19937 g(5);
+  auto pick = [&](int lo, int hi) {      // spread over the logarithm
+    const double l = std::uniform_real_distribution<>(0, 1)(g);
+    return (int)(lo * std::pow((double)hi / lo, l));
+  };
+  for (int i = 0; i < 20000 && ok; ++i) {
+    const int requests = i % 3 == 0 ? 1 : pick(1, 1024), heads = pick(1, 64), group = pick(1, 64);
+    std::vector<int> nodes(requests), lens(requests);
+    const int top = pick(1, 1 << 24), n = pick(1, requests == 1 ? 8192 : 300);
+    for (int b = 0; b < requests; ++b) {
+      nodes[b] = i % 2 ? n : std::uniform_int_distribution<>(0, n)(g);
+      lens[b] = nodes[b] + (i % 5 ? std::uniform_int_distribution<>(0, top)(g) : b ? 0 : top);
+    }
+    ok &= plan(nodes, lens, heads, group, i % 7 ? 1024 : 512, false);
+  }
+  return ok ? 0 : 1;
+}
+"""
+
+
+def test_attention_plan_fits_its_workspace(tmp_path):
+    """The plan of a call, compiled for the host: every chunk has tiles, and the items fit what the workspace is sized
+    for, over the lengths that the header allows (1024 requests of 2^30 - 1 tokens among them) and random batches."""
+    src = tmp_path / "plan.cpp"
+    src.write_text("#include <cmath>\n" + PLAN_MAIN)
+    csrc = os.path.join(os.path.dirname(w12.__file__), "csrc")
+    exe = str(tmp_path / "plan")
+    subprocess.run(["g++", "-O2", "-std=c++17", "-D__host__=", "-D__device__=", "-I", csrc, str(src), "-o", exe], check=True)
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout
