@@ -13,6 +13,7 @@ from ._lib import _AttentionArgs, _KVCache, _NormArgs, _RopeArgs, _c_u64, _check
 
 DTYPE_BF16, DTYPE_F32, DTYPE_E4M3 = 0, 1, 2
 QUANT_BLOCK = 128
+_COUNTER_BYTES = 16384      # the counters at the start of a product's workspace; the partial sums behind them hold anything
 
 _BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 _FLOATS = {_BF16: DTYPE_BF16, _F32: DTYPE_F32}
@@ -243,7 +244,7 @@ def gemm_e4m3_workspace_size(m: int, n: int, k: int) -> int:
 
 
 def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
-    """A ready-to-use (zero-initialised) workspace for gemm_e4m3() with M=m on W[n][k], or None."""
+    """A ready-to-use workspace (its counters are zero) for gemm_e4m3() with M=m on W[n][k], or None."""
     d = torch.device(device)
     if d.type != "cuda":
         raise ValueError("tensors must live on the GPU (libw12 has no CPU path)")
@@ -253,7 +254,8 @@ def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> t
     if not need:
         return None
     ws = torch.empty(need, dtype=torch.uint8, device=device)
-    _check("w12_gemm_workspace_init", lib().w12_gemm_workspace_init(ws.data_ptr(), need, _raw_stream(stream)))
+    _check("w12_gemm_workspace_init",
+           lib().w12_gemm_workspace_init(ws.data_ptr(), min(need, _COUNTER_BYTES), _raw_stream(stream)))
     return ws
 
 

@@ -132,3 +132,14 @@ def test_attention_plan_fits_its_workspace(tmp_path):
     subprocess.run(["g++", "-O2", "-std=c++17", "-D__host__=", "-D__device__=", "-I", csrc, str(src), "-o", exe], check=True)
     r = subprocess.run([exe], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout
+
+
+def test_only_the_counters_of_a_workspace_are_cleared(recorder, monkeypatch):
+    """The partial sums (22 MB for one row of 5120 x 17408) are written before they are read."""
+    sizes = []
+    recorder.w12_gemm_workspace_init = lambda p, n, s: sizes.append(n) or 0
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: empty(*a, **{**k, "device": "cpu"}))
+    ws = w12.gemm_e4m3_workspace(1, 5120, 17408)
+    assert ws.numel() == w12.gemm_e4m3_workspace_size(1, 5120, 17408) > 1 << 20
+    assert sizes == [w12.gemm_plan(16, 5120, 17408)["counter_bytes"]]
