@@ -439,8 +439,10 @@ int w12_tree_attention(const w12_attention_args *a, const w12_kv_cache *cache, v
  * them), one per block of 128 x 128 of W.  Bitwise the same from run to run for the same (M, N, K).
  * ldx and ldw are multiples of 16 bytes; ldxs, ldws >= ceil(K / 128), (M - 1) * ldxs + ceil(K / 128)
  * < 2^29; Y is 4-byte aligned.
- * 1 <= M <= 4096, N and K as for w12_gemm.  ws: as for w12_gemm (w12_gemm_e4m3_workspace_size
- * bytes, initialised once with w12_gemm_workspace_init; every call leaves its counters zero).
+ * 1 <= M <= 4096, N and K as for w12_gemm.  ws: as for w12_gemm (w12_gemm_e4m3_workspace_size bytes,
+ * which serve every number of rows up to M over the same N and K; initialised once with
+ * w12_gemm_workspace_init, of which the counters matter; every call leaves them zero).  A call that
+ * needs less, or none, is not refused for a smaller one.
  */
 int w12_gemm_e4m3_workspace_size(int32_t M, int32_t N, int32_t K, uint64_t *bytes);
 int w12_gemm_e4m3(const uint8_t *X, int32_t M, int64_t ldx, const float *x_scale, int64_t ldxs, const uint8_t *W,

@@ -244,7 +244,7 @@ def gemm_e4m3_workspace_size(m: int, n: int, k: int) -> int:
 
 
 def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
-    """A ready-to-use workspace (its counters are zero) for gemm_e4m3() with M=m on W[n][k], or None."""
+    """A ready-to-use workspace (its counters are zero) for gemm_e4m3() of up to m rows on W[n][k], or None."""
     d = torch.device(device)
     if d.type != "cuda":
         raise ValueError("tensors must live on the GPU (libw12 has no CPU path)")

@@ -551,7 +551,7 @@ int w12_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* x_scale
     return fail(W12_ERR_UNSUPPORTED_SHAPE, "W spans too many bytes for 32-bit buffer offsets");
   if (((int64_t)M - 1) * ldy + N >= (int64_t(1) << 29))
     return fail(W12_ERR_UNSUPPORTED_SHAPE, "Y spans too many elements for 31-bit buffer offsets");
-  const uint64_t need = w12::gemm_e4m3_workspace_bytes(M, N, K);
+  const uint64_t need = w12::gemm_e4m3_call_bytes(M, N, K);
   if (ws_bytes < need)
     return fail(W12_ERR_WORKSPACE_TOO_SMALL, "workspace %llu bytes < %llu needed", (unsigned long long)ws_bytes,
                 (unsigned long long)need);

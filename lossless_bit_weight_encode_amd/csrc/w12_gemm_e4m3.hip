@@ -457,7 +457,7 @@ static void plan_with(E4m3Plan& p, int M, int N) {
 }
 
 static E4m3Plan plan_e4m3(int M, int N, int K) {
-  E4m3Plan p;
+  E4m3Plan p{};
   p.steps = ceil_div(K, kStepK);
   p.path = M <= 4 && K >= N && (int64_t)N * K <= (int64_t(1) << 27) ? 32 : M <= 64 ? 64 : 128;
   if (p.path == 32) plan_with<E4m3Rows32>(p, M, N);
@@ -466,9 +466,18 @@ static E4m3Plan plan_e4m3(int M, int N, int K) {
   return p;
 }
 
+static uint64_t e4m3_call_bytes(const E4m3Plan& p) { return p.part_bytes ? kCounterBytes + p.part_bytes : 0; }
+
+uint64_t gemm_e4m3_call_bytes(int32_t M, int32_t N, int32_t K) { return e4m3_call_bytes(plan_e4m3(M, N, K)); }
+
+// Enough for every number of rows up to M.  Fewer rows may need more (whole tiles for each work-group leave no parts):
+// what a call needs goes by its path and its tiles along M, so one M of each is looked at.
 uint64_t gemm_e4m3_workspace_bytes(int32_t M, int32_t N, int32_t K) {
-  const E4m3Plan p = plan_e4m3(M, N, K);
-  return p.part_bytes ? kCounterBytes + p.part_bytes : 0;
+  uint64_t most = gemm_e4m3_call_bytes(M, N, K);
+  if (M > 4) most = max(most, gemm_e4m3_call_bytes(4, N, K));
+  if (M > 64) most = max(most, gemm_e4m3_call_bytes(64, N, K));
+  for (int m = E4m3Rows128::kBM; m < M; m += E4m3Rows128::kBM) most = max(most, gemm_e4m3_call_bytes(m, N, K));
+  return most;
 }
 
 hipError_t launch_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* xs, int64_t ldxs, const uint8_t* W,

@@ -84,7 +84,8 @@ hipError_t launch_add_rmsnorm(const w12_norm_args& a, hipStream_t stream);
 hipError_t launch_rope_append(const w12_rope_args& a, const w12_kv_cache& c, hipStream_t stream);
 uint64_t attention_workspace_bytes(int32_t T, int32_t requests, int32_t q_heads, const w12_kv_cache& c);
 hipError_t launch_tree_attention(const w12_attention_args& a, const w12_kv_cache& c, void* ws, hipStream_t stream);
-uint64_t gemm_e4m3_workspace_bytes(int32_t M, int32_t N, int32_t K);
+uint64_t gemm_e4m3_workspace_bytes(int32_t M, int32_t N, int32_t K);   // for up to M rows
+uint64_t gemm_e4m3_call_bytes(int32_t M, int32_t N, int32_t K);        // for M rows
 hipError_t launch_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* xs, int64_t ldxs, const uint8_t* W,
                             int32_t N, int32_t K, int64_t ldw, const float* wsc, int64_t ldws, float* Y, int64_t ldy,
                             void* ws, hipStream_t stream);

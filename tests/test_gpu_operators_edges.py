@@ -84,3 +84,17 @@ def test_attention_with_decreasing_ranges_stays_inside_its_workspace():
         ref, mag = torch.einsum("ht,thd->hd", p, vv[:65 + row]), torch.einsum("ht,thd->hd", p, vv[:65 + row].abs())
         # the result and p rounded to BF16 (2^-8 each); scores and sums of hundreds of terms in FP32
         assert ((got[row] - ref).abs() <= ref.abs() * 2.0 ** -8 + mag * (2.0 ** -8 * 1.01 + 4 * 1024 * E24)).all()
+
+
+def test_one_workspace_serves_fewer_rows():
+    """A workspace for the most rows, used by calls of other paths and tilings one after another: the bits of a call
+    with its own."""
+    n, k = 5120, 4352
+    w = rnd(1, n, k, scale=50.0).clamp(-448, 448).to(F8).cuda()
+    x = rnd(2, 600, k, scale=50.0).clamp(-448, 448).to(F8).cuda()
+    xs, wsc = torch.rand(600, 34, device="cuda") * 1e-2, torch.rand(40, 34, device="cuda") * 1e-2
+    ws = w12.gemm_e4m3_workspace(600, n, k)
+    for m in (600, 1, 512, 64, 4, 65, 5, 300, 1):
+        a = w12.gemm_e4m3(x[:m], xs[:m], w, wsc, ws=ws)
+        assert torch.equal(a, w12.gemm_e4m3(x[:m], xs[:m], w, wsc)), m
+        assert (ws[:16384] == 0).all(), "counters are left at zero"

@@ -9,7 +9,7 @@ import torch
 
 import lossless_bit_weight_encode_amd as w12
 from lossless_bit_weight_encode_amd import _lib as L
-from test_operators_host import cache
+from test_operators_host import cache, gemm
 
 
 class _Recorder:
@@ -143,3 +143,25 @@ def test_only_the_counters_of_a_workspace_are_cleared(recorder, monkeypatch):
     ws = w12.gemm_e4m3_workspace(1, 5120, 17408)
     assert ws.numel() == w12.gemm_e4m3_workspace_size(1, 5120, 17408) > 1 << 20
     assert sizes == [w12.gemm_plan(16, 5120, 17408)["counter_bytes"]]
+
+
+SHAPES = [(32768, 4096), (5120, 17408), (34816, 5120), (5120, 5120), (65536, 2048), (256, 65536), (130, 127), (8192, 28672)]
+
+
+@pytest.mark.parametrize("n,k", SHAPES)
+def test_a_workspace_for_many_rows_serves_fewer(n, k):
+    """The size never falls as rows are added, and a call of any number of rows accepts a workspace that was sized for
+    more (the call's own check comes before any launch: a misaligned workspace is its next complaint)."""
+    rows = sorted({1, 2, 4, 5, 8, 32, 63, 64, 65, 100, 128, 129, 256, 257, 384, 512, 513, 1000, 1024, 2048, 2500, 4095, 4096})
+    sizes = [w12.gemm_e4m3_workspace_size(m, n, k) for m in rows]
+    assert sizes == sorted(sizes)
+    for m in rows:
+        assert gemm(M=m, N=n, K=k, ldx=k + 15 & ~15, ldw=k + 15 & ~15, ldxs=1024, ldws=1024, ldy=n, ws=0x100008,
+                    ws_bytes=sizes[-1]) == -5
+
+
+def test_gemm_e4m3_refuses_a_workspace_that_is_too_small():
+    need = w12.gemm_e4m3_workspace_size(3, 256, 4096)
+    assert need > 16384
+    call = dict(M=3, N=256, K=4096, ldx=4096, ldw=4096, ldxs=32, ldws=32, ldy=256)
+    assert gemm(**call, ws_bytes=16384) == -3 and gemm(**call, ws=None) == -1
