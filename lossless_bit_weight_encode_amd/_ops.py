@@ -244,7 +244,8 @@ def gemm_e4m3_workspace_size(m: int, n: int, k: int) -> int:
 
 
 def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> torch.Tensor | None:
-    """A ready-to-use workspace (its counters are zero) for gemm_e4m3() of up to m rows on W[n][k], or None."""
+    """A ready-to-use workspace (its counters are zero) for gemm_e4m3() of up to m rows on W[n][k], or None.
+    With a stream, it belongs to that stream."""
     d = torch.device(device)
     if d.type != "cuda":
         raise ValueError("tensors must live on the GPU (libw12 has no CPU path)")
@@ -253,7 +254,8 @@ def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> t
     need = gemm_e4m3_workspace_size(m, n, k)
     if not need:
         return None
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
     _check("w12_gemm_workspace_init",
            lib().w12_gemm_workspace_init(ws.data_ptr(), min(need, _COUNTER_BYTES), _raw_stream(stream)))
     return ws

@@ -98,3 +98,13 @@ def test_one_workspace_serves_fewer_rows():
         a = w12.gemm_e4m3(x[:m], xs[:m], w, wsc, ws=ws)
         assert torch.equal(a, w12.gemm_e4m3(x[:m], xs[:m], w, wsc)), m
         assert (ws[:16384] == 0).all(), "counters are left at zero"
+
+
+def test_a_workspace_belongs_to_its_stream():
+    """The clearing kernel runs on the given stream, so the memory has to be that stream's: what the current stream
+    freed may still be in use by kernels that it has in flight."""
+    s = torch.cuda.Stream()
+    ws = w12.gemm_e4m3_workspace(1, 5120, 17408, stream=s)
+    owners = [g["stream"] for g in torch.cuda.memory_snapshot()
+              if g["address"] <= ws.data_ptr() < g["address"] + g["total_size"]]
+    assert owners == [s.cuda_stream]
