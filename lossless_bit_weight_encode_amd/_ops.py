@@ -5,6 +5,7 @@ the C ABI (include/w12.h), enqueues on the current stream (or ``stream``) and re
 are checked by the library."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -47,6 +48,12 @@ def _raw_stream(stream) -> int:
     return _current_raw_stream(torch.cuda.current_device()) if stream is None else stream.cuda_stream
 
 
+def _on(stream):
+    """Where a call allocates: on the stream that it was given, else where torch is (entering the current stream
+    again costs as much as a small call)."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _rows(t: torch.Tensor, what: str, shape: tuple, dtypes, step: int) -> int:
     """Checks a matrix with contiguous rows; its pitch in elements.  A single row is never stepped
     by its pitch, and torch may report any stride for it, so it gets its padded width."""
@@ -87,7 +94,7 @@ def add_rmsnorm(residual: torch.Tensor, weight: torch.Tensor, delta: torch.Tenso
     m, n = _matrix2(residual, "residual")
     _device(residual, weight, delta, residual_out, y, yq, yq_scale)
     if y is None and yq is None:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        with _on(stream):
             y = torch.empty(m, (n + 7) // 8 * 8, dtype=_BF16, device=residual.device)[:, :n]
     shape = (m, n)
     rt = residual.dtype
@@ -161,7 +168,7 @@ def rope_append(qkv: torch.Tensor, cache: KVCache, positions: torch.Tensor, slot
         raise ValueError(f"qkv: expected {(q_heads + 2 * cache.heads) * dim} columns, got {width}")
     _device(qkv, cache.k, positions, slots, inv_freq, axis, q)
     if q is None:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        with _on(stream):
             q = torch.empty(t, q_heads * dim, dtype=_BF16, device=qkv.device)
     ld_x = _rows(qkv, "qkv", (t, width), _FLOATS, 8)
     axes = _matrix2(positions, "positions")[0]
@@ -210,7 +217,7 @@ def tree_attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, ct
         raise ValueError(f"q: {width} columns are not whole heads of {dim}")
     _device(q, cache.k, page_table, ctx_len, node_ptr, tree_mask, out, lse, ws)
     if out is None or ws is None:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        with _on(stream):
             if out is None:
                 out = torch.empty(t, width, dtype=_BF16, device=q.device)
             if ws is None:
@@ -254,7 +261,7 @@ def gemm_e4m3_workspace(m: int, n: int, k: int, device="cuda", stream=None) -> t
     need = gemm_e4m3_workspace_size(m, n, k)
     if not need:
         return None
-    with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+    with _on(stream):
         ws = torch.empty(need, dtype=torch.uint8, device=device)
     _check("w12_gemm_workspace_init",
            lib().w12_gemm_workspace_init(ws.data_ptr(), min(need, _COUNTER_BYTES), _raw_stream(stream)))
@@ -270,7 +277,7 @@ def gemm_e4m3(x: torch.Tensor, x_scale: torch.Tensor, w: torch.Tensor, w_scale: 
     kb = -(-k // QUANT_BLOCK)
     _device(x, x_scale, w, w_scale, y, ws)
     if y is None or ws is None:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+        with _on(stream):
             if y is None:
                 y = torch.empty(m, n, dtype=_F32, device=x.device)
             if ws is None:
