@@ -397,11 +397,13 @@ int w12_rope_append(const w12_rope_args *a, const w12_kv_cache *cache, hipStream
  * row of tree_mask (bit j % 64 of word j / 64 for node j; its own bit is not implied; nodes past
  * the words are not attended), or with tree_mask NULL the nodes 0..i (a chain).  Query head h
  * reads cache head h / (q_heads / heads).
- *   out[row][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max),  in FP32.
+ *   out[row][h] = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale * q . k_t - max).
  *   lse[row][h] = log sum_t exp(scale * q . k_t), if lse is not NULL.
+ * Scores, p_t and all sums are FP32; for its product with v_t each p_t is rounded to BF16 (by up to 2^-8 of
+ * itself), so that out may be off by 2^-8 of sum_t p_t |v_t| / sum_t p_t beside its own rounding.  lse has no such part.
  * What a row does not attend never reaches it, NaN and infinity included.  A row that attends
- * nothing, or whose scores are all -inf, gives zeros and lse -inf.  Tokens past max_pages * page_size, and tokens whose page is
- * not in 0 .. pages - 1, count as absent.  Rows outside every request are left as they are;
+ * nothing, or whose scores are all -inf, gives zeros and lse -inf.  Tokens past max_pages * page_size, and
+ * tokens whose page is not in 0 .. pages - 1, count as absent.  Rows outside every request are left as they are;
  * ranges of node_ptr are cut to 0..T and must not decrease (where they do, out and lse of the rows hold
  * anything, and nothing else is written); negative lengths count as 0.
  * node_ptr, ctx_len, page_table and tree_mask are device memory read by the kernels (a captured
@@ -442,7 +444,8 @@ int w12_tree_attention(const w12_attention_args *a, const w12_kv_cache *cache, v
  * 1 <= M <= 4096, N and K as for w12_gemm.  ws: as for w12_gemm (w12_gemm_e4m3_workspace_size bytes,
  * which serve every number of rows up to M over the same N and K; initialised once with
  * w12_gemm_workspace_init, of which the counters matter; every call leaves them zero).  A call that
- * needs less, or none, is not refused for a smaller one.
+ * needs less, or none, is not refused for a smaller one.  The two scales of a block are multiplied
+ * first, in FP32: their product has to be a normal number or 0.
  */
 int w12_gemm_e4m3_workspace_size(int32_t M, int32_t N, int32_t K, uint64_t *bytes);
 int w12_gemm_e4m3(const uint8_t *X, int32_t M, int64_t ldx, const float *x_scale, int64_t ldxs, const uint8_t *W,

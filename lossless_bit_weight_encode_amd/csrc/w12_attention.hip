@@ -22,9 +22,10 @@
 // else through registers, in which E4M3 caches become BF16 (exactly); their scales go into c and the result.
 //
 // Bound (40 heads on 8 cache heads of 128): a long cache by the matrix instructions, their operand reads from LDS
-// and the exponentials, which run partly beside each other (64 nodes over 131001 tokens: 222 us, 770 TFLOP/s,
-// 2.4 TB/s); a short one by the loop's start, the partial results and the second launch (63 nodes over 8191:
-// 28 us; one over 509: 11).
+// and the exponentials, which run partly beside each other (64 nodes over 131001 tokens: 223 to 238 us, 720 to 770 TFLOP/s,
+// 2.4 TB/s); a short one by the loop's start, the partial results, the second launch and work-groups without an item: the
+// grid is what any lengths may need, as the host does not know them (63 nodes over 8191: 29 us, 2080 work-groups for 456
+// items; one over 509: 11).  A chain is computed above its diagonal too, and those products are dropped.
 #include <type_traits>
 
 #include "w12_attention_plan.h"
@@ -793,7 +794,7 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   const int target = attention_target(D);
   const int rg = attention_row_groups(a.T, a.q_heads, c);
   // tiles inside one page, with a thread's offsets in 32 bits (looked up token by token instead: 63 nodes over 32767
-  // tokens 98 us for 87, with heads of 256 over 8191 46 for 32)
+  // tokens 80 us for 68, with heads of 256 over 8191 44 for 32)
   const bool whole = c.page_size >= kTile && c.token_stride <= (int64_t(1) << 24);
   const dim3 g((unsigned)groups), t(kAttnThreads);
   if (whole) hipLaunchKernelGGL((k_tree_attention<D, F8, true>), g, t, 0, stream, a, c, ws, rg, target, groups);
@@ -801,8 +802,8 @@ static hipError_t launch_attention(const w12_attention_args& a, const w12_kv_cac
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t row_blocks = ceil_div((int64_t)a.T * (a.q_heads / c.heads), 32) + a.requests;
-  // few rows: waves share the parts (12 nodes over 8191 tokens 25 us, else 32; one node 19 and 26); many: they share the
-  // work of finding the request, and a wave's parts are few (16 requests of 24 nodes 107 us, else 126)
+  // few rows: waves share the parts (12 nodes over 8191 tokens 19.0 us, else 22.2; one node 16.4 and 19.9); many: they
+  // share the work of finding the request, and a wave's parts are few (16 requests of 24 nodes, BF16, 93 us, else 116)
   const unsigned x = (unsigned)row_blocks, y = (unsigned)c.heads;
   if (row_blocks * c.heads < device_cus())
     hipLaunchKernelGGL((k_join<D, F8, true>), dim3(x, y, D / 8), t, 0, stream, a, c, (const float*)ws, rg, target, groups);

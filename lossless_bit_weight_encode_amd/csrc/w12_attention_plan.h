@@ -9,9 +9,10 @@ namespace w12 {
 constexpr int kTile = 64;            // tokens of a tile
 constexpr int kBlockRows = 128;      // rows of a block
 constexpr int kMostTiles = 1 << 24;  // of a request: it holds fewer than 2^30 tokens
-// Least tiles of a chunk where all rows are up to 64 (twice as many for more than 32 chunks: one node over 8191 tokens
-// 19.0 -> 16.3 us, 12 nodes 25 -> 19, but 2047 tokens 12.1 -> 12.9), and elsewhere, where a partial result is as
-// large as 2 tiles (63 nodes over 2047 tokens 19.2 us, with 6 tiles 19.9; over 8191 the same).
+// Least tiles of a chunk where all rows are up to 64 (twice as many for more than 32 chunks; us with them / without: one
+// node over 8191 tokens 16.4 / 19.3, 12 nodes 19.0 / 21.1, but one node over 2047, always twice as many, 13.1 / 12.0), and
+// elsewhere, where a partial result is as large as 2 tiles (63 nodes over 2047 tokens 19.2 us, with 6 tiles 19.8; over
+// 8191 the same).
 constexpr int kMinChunk = 2;
 constexpr int kMinChunkLarge = 4;
 
@@ -35,18 +36,18 @@ __host__ __device__ inline Blocks blocks_of(int rows, int len) {
 // Tiles of a chunk where requests share the chip: the cost of all tiles over `share`.  Where twice the blocks of all heads
 // fit the chip, all items make one round: the cost is a tile of a block, half a chunk for each block is set
 // aside for last chunks that are short, and a chunk that still gives too many items is lengthened by eighths, up to
-// three times (16 requests of 24 nodes over up to 8000 tokens, in one round and in about two: E4M3 76 / 84 us, BF16 94 /
-// 106; 8 of 40 nodes, E4M3, 61 / 75; 32 of 8 nodes over 4000 90 / 114).  Otherwise two rounds, whose items even out
-// unequal lengths, the cost is that of four waves.
+// three times (us in one round / in about two: 16 requests of 24 nodes over up to 8000 tokens 80 / 86 in E4M3, 93 / 107 in
+// BF16; 8 of 40 nodes, E4M3, 62 / 77; 4 of 12 nodes 41 / 43; 32 of 8 nodes over 4000 88 / 112).  Otherwise two rounds,
+// whose items even out unequal lengths, and the cost is that of four waves.
 __host__ __device__ inline int chunk_of(int64_t cost, int64_t share, int rows) {
   const int64_t tiles = (cost + share - 1) / share;
   return at_least(tiles > kMostTiles ? kMostTiles : (int)tiles, rows <= kBlockRows / 2 ? kMinChunk : kMinChunkLarge);
 }
 
-// Tiles of a chunk of one request, whose items (per = heads x blocks, for each chunk) are about equally long: they
-// go in whole rounds of the `slots` work-groups that the chip holds, the fewest that leave at most a quarter of the
-// slots empty; a few items over a round would cost another one (63 nodes over 8191 tokens in one round 29.7 us,
-// as several requests are 34.8; over 32767 70 and 87, 64 nodes over 131001 234 and 246).
+// Tiles of a chunk of one request, whose items (per = heads x blocks, for each chunk) have equally many tiles (of a last
+// block of up to 64 rows, half a block's work): they go in whole rounds of the `slots` work-groups that the chip holds, the
+// fewest that leave at most a quarter of the slots empty; a few items over a round would cost another one (us so / cut as
+// several requests are: 63 nodes over 2047 tokens 19 / 27, over 8191 29 / 38, over 32767 68 / 74, 64 over 131001 232 / 233).
 __host__ __device__ inline int one_request_chunk(const Blocks& k, int slots, int per, int rows) {
   int chunks = 1;
   for (int rounds = 1; rounds <= 4; ++rounds) {

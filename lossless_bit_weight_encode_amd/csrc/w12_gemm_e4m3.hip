@@ -14,9 +14,9 @@
 // pieces are put there beside the matrix instructions.  For a few rows over a short W they load
 // straight into operand registers: a wave's W is nobody else's, and no wave waits for another.
 //
-// Bound: few rows by the read of W (63 rows of 34816 x 5120, 178 MB: 57 us, 3.3 TB/s; a bare read of W in this order
-// takes 38), many by the matrix instructions and what feeds them (512 rows: 222 us, 820 TFLOP/s; the
-// instructions alone 120).
+// Bound: few rows by the read of W (63 rows of 34816 x 5120, 178 MB: 57 us, 3.3 TB/s; a copy of the kernel that only reads
+// W in this order took 38), many by the matrix instructions and what feeds them (512 rows: 216 to 226 us, 805 to 845
+// TFLOP/s; a copy with the instructions alone took 120).
 #include "w12_device.h"
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
@@ -434,12 +434,15 @@ struct E4m3Plan {
   uint64_t part_bytes;
 };
 
-// Which tile (us, both sides): up to 64 rows Rows64, 256 channels on 8 waves, where Rows128 pads (34816 channels of 5120:
-// 16 rows 46 / 56, 64 rows 57 / 64; 96 rows 71 / 71).  Up to 4 rows, a W of long rows and up to 128 MB is faster
-// straight into registers, with three small work-groups a compute unit and partial tiles of the real rows only (Rows32
-// / Rows64: 5120 of 17408 with 1 row 26.5 / 31.2, 4 rows 29.0 / 31.6, 8 rows 32.7 / 29.5; 5120 of 5120 with 1 row
-// 13.9 / 14.8, but 5120 of 34816 51.9 / 48.2, 10240 of 8192 27.4 / 26.0, 34816 of 5120 57 / 43).  Tiles of 128
-// channels: with 256 and two work-groups a unit 5120 of 17408 takes 28.5.
+// Which tile (us, both sides): up to 64 rows Rows64, 256 channels on 8 waves, where Rows128 pads (Rows64 / Rows128, 34816
+// channels of 5120: 16 rows 46 / 55, 64 rows 57 / 63, 96 rows 76 / 70; 5120 of 17408: 64 rows 44 / 56, but 128 rows
+// 50 / 70, which the rule does not take).  Up to 4 rows, a W of long rows and up to 128 MB goes straight into registers,
+// with three small work-groups a compute unit and partial tiles of the real rows only (Rows32 / Rows64 in a graph:
+// 5120 of 17408 with 1 row 32.2 / 36.2, 4 rows 34.7 / 36.0, 8 rows 37.0 / 33.4; 5120 of 5120 with 1 row 15.1 / 17.8; 2048 of
+// 8192 10.6 / 17.2; 1024 of 16384 11.8 / 23.2; but 5120 of 34816 55.1 / 50.8, 10240 of 8192 33.9 / 31.1, 7168 of 5120
+// 22.3 / 20.4, 34816 of 5120 58 / 44).  Both bounds lie between these shapes and are no more exact than that: 8192 of
+// 8192 (29.1 / 25.3) is on the wrong side.  Tiles of 128 channels: with 256 and two work-groups a unit 5120 of 17408
+// took 2 us more.
 using E4m3Rows32 = E4m3Cfg<4, 1, 1, 1, 2, 3, false>;
 using E4m3Rows64 = E4m3Cfg<8, 1, 1, 2, 2, 1, true>;
 using E4m3Rows128 = E4m3Cfg<4, 2, 2, 2, 1, 1, true>;

@@ -4,8 +4,8 @@
 // One work-group takes one row and keeps it in registers between the sum of squares and the
 // outputs, so every value is read once and written once; the bound is memory traffic.  A lane
 // holds V pieces of eight values; 16 neighbouring lanes hold a block of 128, whose largest
-// magnitude they find among themselves.  4096 rows of 5120 from FP32 to FP32 and E4M3 (273 MB): 54 us, 5.1 TB/s, what a
-// copy reaches; up to 64 rows: 7.5 us, the launch.
+// magnitude they find among themselves.  4096 rows of 5120 from FP32 to FP32 and E4M3 (273 MB): 54 us, 5.1 TB/s (a plain
+// copy: 4.7); up to 64 rows: 2.7 to 4.6 us in a call of 7.5 to 7.9.
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"

@@ -4,7 +4,8 @@
 //   (a, b) -> (a cos theta - b sin theta, a sin theta + b cos theta).
 // The angle is formed in FP64 as a number of turns and reduced there to half a turn either way,
 // so a far position loses nothing; its sine and cosine are FP32.  Bound: the launch, then positions -> sines -> the
-// turn one after another (512 rows of 56 heads of 128, 18 MB: 7.6 us; one row: 7.4, of which the kernel 2.7).
+// turn one after another (512 rows of 56 heads of 128 into an E4M3 cache, 21 MB: 7.7 us; 4096 into a BF16 one, 176 MB:
+// 37.6, 4.7 TB/s, a copy's rate; one row: 2.7, in a call of 7.7).
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"
@@ -101,7 +102,8 @@ __global__ __launch_bounds__(kRopeThreads) void k_rope_append(w12_rope_args a, w
 
 hipError_t launch_rope_append(const w12_rope_args& a, const w12_kv_cache& c, hipStream_t stream) {
   const int dim_bits = 31 - __builtin_clz(c.dim), all = a.q_heads + 2 * c.heads;
-  // pieces of a row over as many work-groups as leave each thread one piece, while rows alone do not fill the chip
+  // pieces of a row over as many work-groups as leave each thread one piece, up to two rows a compute unit (us of 56 heads
+  // of 128, split / whole: 64 rows 3.3 / 5.3, 256 rows 4.7 / 6.0, 512 rows 8.0 / 9.9, 1024 rows 12.8 / 12.5, 4096 rows 38.4 / 37.7)
   const int64_t pieces = (int64_t)all << (dim_bits - 3);
   const int64_t groups = a.T >= 2 * device_cus() ? 1 : ceil_div(pieces, kRopeThreads);
   const int heads = (int)ceil_div(all, groups);
