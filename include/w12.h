@@ -452,6 +452,153 @@ int w12_gemm_e4m3(const uint8_t *X, int32_t M, int64_t ldx, const float *x_scale
                   int32_t N, int32_t K, int64_t ldw, const float *w_scale, int64_t ldws, float *Y, int64_t ldy,
                   void *ws, uint64_t ws_bytes, hipStream_t stream);
 
+/*
+ * Operators of a hybrid target in speculative decoding: its recurrent layers (a short causal
+ * convolution and the gated delta rule, for prompts, single tokens, and chains or trees of drafted
+ * tokens) and the verification of drafted tokens.  All conventions above apply.
+ *
+ * Which rows of a call belong to which sequence, and where the sequences' states are.  Token i of
+ * sequence b is row ptr[b] + i of the call's matrices, or row rows[ptr[b] + i] of them, for
+ * i < ptr[b + 1] - ptr[b], and with lens for i < lens[b] besides.  A row outside 0 .. T - 1 counts
+ * as zeros in every input, and has no output.  A sequence starts from the state in slot src[b] (zeros for
+ * a slot outside 0 .. slots - 1) and its new state goes to slot dst[b] (nowhere for a slot outside),
+ * which may be src[b]; a sequence without tokens has its old state put there.  dst NULL: no state is stored.
+ * Slots of dst must differ from one another, and from the src of other sequences; several may share
+ * a src.  Where outputs are wanted, no row may be named twice.
+ * Ranges of ptr are cut to 0..T and must not decrease (where they do, the outputs and the new
+ * states hold anything, and nothing else is written); negative lengths count as 0.  Rows of no
+ * sequence are left as they are.
+ *
+ * tree_mask makes every range a tree of drafted tokens in drafting order (dst, rows and lens are
+ * then NULL): row r's bits below its own place name its ancestors (bit j for node j of its range,
+ * as in w12_attention_args; its own bit and those above count as set and unset).  A node follows its
+ * ancestors only; of a range more than 64 nodes long the rest is left as it is.  The ancestors have to be a path: a
+ * node's are those of its nearest ancestor, and that ancestor (where they are not, the range's outputs hold anything).
+ *
+ * ptr, lens, rows, src, dst and tree_mask are device memory read by the kernels (a captured graph
+ * follows their values).  1 <= T <= 2^20, 1 <= count <= 1024, 1 <= slots <= 2^20, 1 <= mask_words <= 64.
+ */
+#define W12_TREE_NODES 64
+typedef struct w12_sequences {
+  int32_t T, count;
+  const int32_t *ptr;            /* [count + 1]                                              */
+  const int32_t *lens;           /* [count] or NULL                                          */
+  const int32_t *rows;           /* [T] or NULL                                              */
+  const int32_t *src, *dst;      /* [count]; dst may be NULL                                 */
+  const uint64_t *tree_mask;     /* [T][ld_mask] or NULL, 8-byte aligned                     */
+  int64_t ld_mask;
+  int32_t mask_words;            /* words of a tree_mask row (0 with tree_mask NULL)         */
+  int32_t slots;                 /* places of the state array                                */
+} w12_sequences;
+
+/*
+ * Short causal convolution of every channel: y_t = act(bias + sum_j weight[c][j] x_{t - (width - 1) + j}),
+ * FP32 sums; the tokens before the sequence's first are its state, the last width - 1 rows of x (in x's
+ * type, oldest first).  act: SiLU, y / (1 + exp(-y)), with silu != 0, else none.  In a tree the tokens before a node are its
+ * ancestors, nearest last.  y NULL: only the states move on.  What is not in a row's window never reaches it.
+ * 1 <= channels <= 2^17, 2 <= width <= 4.
+ */
+typedef struct w12_conv_args {
+  int32_t channels, width;
+  int32_t dtype;                 /* W12_DTYPE_F32 (a w12_gemm result) or W12_DTYPE_BF16: x, state */
+  int32_t silu;
+  const void *x;                 /* [T][ldx]                                                 */
+  int64_t ldx;
+  const uint16_t *weight;        /* BF16 [channels][width], 4-byte aligned                   */
+  const uint16_t *bias;          /* BF16 [channels] or NULL                                  */
+  void *state;                   /* [slots][width - 1][channels], 16-byte aligned            */
+  int64_t slot_stride, tap_stride;   /* elements, multiples of 16 bytes; tap_stride >= channels  */
+  uint16_t *y;                   /* BF16 [T][ldy] or NULL                                    */
+  int64_t ldy;
+} w12_conv_args;
+int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t stream);
+
+/*
+ * The gated delta rule.  Every value head h of a sequence has a state S of dk x dv, kept transposed:
+ * state[slot][h][j][i] = S[i][j], FP32.  A token with key k (of key head h / (v_heads / k_heads)), value v,
+ * log decay g, strength beta and query q turns it into
+ *   S' = exp(g) S + k (beta (v - exp(g) S^T k))^T      and gives      out = scale S'^T q.
+ * With l2norm, k and q are divided by sqrt(sum of squares + eps) first.  In a tree S is the state behind the node's parent.
+ * The states are FP32 throughout.  Tokens of a long range are taken 64 at a time, as a triangular system
+ *   u_i + beta_i sum_{j before i} exp(G_i - G_j) (k_i . k_j) u_j = beta_i (v_i - exp(G_i) S^T k_i),  G_i the sum of g up to i,
+ * with BF16 matrix instructions: q, k and v are exact in them, what is FP32 (S, u, the system's inverse) goes
+ * in as two BF16 values, off by 2^-16 of each value at most; for out, S, u and the q . k factors as one (2^-8).
+ * g <= 0 is expected.  The rule itself grows without bound where beta |k|^2 passes 2.  A NaN or infinity in a row reaches
+ * that row and those that come after it in its sequence (in a tree: its descendants), and the new state; nothing else.
+ * q and out NULL: only the states move on.  The result is bitwise the same from run to run.
+ * dk: 64 or 128, dv: 64, 128 or 256, v_heads a multiple of k_heads, at most 1024.
+ * ws: w12_gated_delta_workspace_size bytes for T rows in count sequences (or more), 16-byte aligned, any content; calls
+ * that overlap in time need workspaces of their own.
+ */
+typedef struct w12_delta_args {
+  int32_t k_heads, v_heads, dk, dv;
+  int32_t l2norm;
+  float eps, scale;              /* eps >= 0, scale finite                                   */
+  int32_t reserved;              /* must be 0                                                */
+  const uint16_t *q;             /* BF16 [T][ldq], head h at h * dk; or NULL                 */
+  int64_t ldq;
+  const uint16_t *k;             /* BF16 [T][ldk], head h at h * dk                          */
+  int64_t ldk;
+  const uint16_t *v;             /* BF16 [T][ldv], head h at h * dv                          */
+  int64_t ldv;
+  const float *g;                /* [T][ldg]                                                 */
+  int64_t ldg;
+  const float *beta;             /* [T][ldbeta]                                              */
+  int64_t ldbeta;
+  float *state;                  /* [slots][v_heads][dv][dk], slots slot_stride apart        */
+  int64_t slot_stride;           /* elements, a multiple of 4                                */
+  uint16_t *out;                 /* BF16 [T][ldo], head h at h * dv; or NULL                 */
+  int64_t ldo;
+} w12_delta_args;
+int w12_gated_delta_workspace_size(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv, uint64_t *bytes);
+int w12_gated_delta(const w12_delta_args *a, const w12_sequences *s, void *ws, uint64_t ws_bytes, hipStream_t stream);
+
+/*
+ * Verification of drafted tokens.  Request b has the nodes node_ptr[b] .. node_ptr[b + 1] - 1; node 0 is
+ * its last known token, tokens[r] is row r's token, and logits[r] (of vocab tokens) is what the target says after row
+ * r's node: p_r = softmax(logits[r] / temperature[b]), at temperature 0 (or less, or NaN) all of it on the largest (the lowest index of
+ * equals).  A node's parent is the nearest of its ancestors in tree_mask (its bits below its own place; a node without any, but for node 0, is never
+ * reached), with tree_mask NULL the node before it.  Random numbers are inputs in [0, 1): u[r] takes the first token whose
+ * cumulative weight, in the order of the tokens, passes u[r] times the total.
+ *   q NULL: row r's token is taken from p_r by u[r].  From node 0 on, the walk goes to the child that has the token taken at
+ *     its node (the first of several), until there is none; next is the last node's token.
+ *   q (chains only): q[r] is the distribution that row r's token was drawn from.  Node i is accepted where accept_u[r] q[r][x] < p[x],
+ *     x its token and p the distribution after the node before it.  After the first that is not, next is taken by u of the last
+ *     accepted row from max(p - q[r], 0) (from p where that is 0 throughout); after the last node, from its p.
+ * path[node_ptr[b] + i], i < count[b], are the rows of the walk (node 0 first) and -1 behind them up to the request's
+ * last row; count[b] their number, next_token[b] the token that follows.  path and count serve as rows and lens of w12_sequences.
+ * Weights, sums and comparisons are FP64.  Logits of -inf and NaN have no weight; where one or more are
+ * +inf, the first of them has all of it; a row without any weight takes no token (-1), and no child follows it.  A token outside
+ * 0 .. vocab - 1 is never accepted.  u is cut to 0 .. the largest number below 1; NaN counts as 0.
+ * A request without nodes gets count 0 and next_token -1; of one with more than 4096 nodes, the first 4096 count.  Rows of no request
+ * have their path left as it is; ranges as in w12_sequences.
+ * 1 <= T <= 2^20, 1 <= requests <= 1024, 1 <= vocab <= 2^24, T * vocab < 2^40.
+ * ws: w12_verify_draft_workspace_size bytes for T rows (or more), 16-byte aligned, any content; calls that overlap in time need
+ * workspaces of their own.
+ */
+#define W12_VERIFY_NODES 4096
+typedef struct w12_verify_draft_args {
+  int32_t T, requests, vocab;
+  int32_t logits_dtype;          /* W12_DTYPE_F32 (a w12_gemm result) or W12_DTYPE_BF16      */
+  const void *logits;            /* [T][ld_logits]                                           */
+  int64_t ld_logits;
+  const float *q;                /* [T][ldq] or NULL                                         */
+  int64_t ldq;
+  const int32_t *tokens;         /* [T]                                                      */
+  const int32_t *node_ptr;       /* [requests + 1]                                           */
+  const uint64_t *tree_mask;     /* [T][ld_mask] or NULL, 8-byte aligned                     */
+  int64_t ld_mask;
+  int32_t mask_words;            /* words of a tree_mask row (0 with tree_mask NULL)         */
+  int32_t reserved;              /* must be 0                                                */
+  const float *u;                /* [T]                                                      */
+  const float *accept_u;         /* [T], with q                                              */
+  const float *temperature;      /* [requests] or NULL: 1 throughout                         */
+  int32_t *path;                 /* [T]                                                      */
+  int32_t *count, *next_token;   /* [requests]                                               */
+} w12_verify_draft_args;
+int w12_verify_draft_workspace_size(int32_t T, int32_t requests, int32_t vocab, uint64_t *bytes);
+int w12_verify_draft(const w12_verify_draft_args *a, void *ws, uint64_t ws_bytes, hipStream_t stream);
+
 /* Stored bits per weight: (1.5*N*K + N + 4*(N+1) + 4*E) * 8 / (N*K).  -1 for N < 1, K < 1
  * or E < 0. */
 double w12_bits_per_weight(int32_t N, int32_t K, int64_t E);

@@ -76,6 +76,31 @@ class _AttentionArgs(ctypes.Structure):
                 ("out", _c_p), ("ldo", _c_i64), ("lse", _c_p), ("ld_lse", _c_i64)]
 
 
+class _Sequences(ctypes.Structure):
+    _fields_ = [("T", _c_i32), ("count", _c_i32), ("ptr", _c_p), ("lens", _c_p), ("rows", _c_p), ("src", _c_p), ("dst", _c_p),
+                ("tree_mask", _c_p), ("ld_mask", _c_i64), ("mask_words", _c_i32), ("slots", _c_i32)]
+
+
+class _ConvArgs(ctypes.Structure):
+    _fields_ = [("channels", _c_i32), ("width", _c_i32), ("dtype", _c_i32), ("silu", _c_i32), ("x", _c_p), ("ldx", _c_i64),
+                ("weight", _c_p), ("bias", _c_p), ("state", _c_p), ("slot_stride", _c_i64), ("tap_stride", _c_i64),
+                ("y", _c_p), ("ldy", _c_i64)]
+
+
+class _DeltaArgs(ctypes.Structure):
+    _fields_ = [("k_heads", _c_i32), ("v_heads", _c_i32), ("dk", _c_i32), ("dv", _c_i32), ("l2norm", _c_i32),
+                ("eps", ctypes.c_float), ("scale", ctypes.c_float), ("reserved", _c_i32), ("q", _c_p), ("ldq", _c_i64),
+                ("k", _c_p), ("ldk", _c_i64), ("v", _c_p), ("ldv", _c_i64), ("g", _c_p), ("ldg", _c_i64),
+                ("beta", _c_p), ("ldbeta", _c_i64), ("state", _c_p), ("slot_stride", _c_i64), ("out", _c_p), ("ldo", _c_i64)]
+
+
+class _VerifyDraftArgs(ctypes.Structure):
+    _fields_ = [("T", _c_i32), ("requests", _c_i32), ("vocab", _c_i32), ("logits_dtype", _c_i32), ("logits", _c_p),
+                ("ld_logits", _c_i64), ("q", _c_p), ("ldq", _c_i64), ("tokens", _c_p), ("node_ptr", _c_p),
+                ("tree_mask", _c_p), ("ld_mask", _c_i64), ("mask_words", _c_i32), ("reserved", _c_i32), ("u", _c_p),
+                ("accept_u", _c_p), ("temperature", _c_p), ("path", _c_p), ("count", _c_p), ("next_token", _c_p)]
+
+
 _SIGNATURES = {
     "w12_layout_bytes": (ctypes.c_int, [_c_i32, _c_i32, ctypes.POINTER(_c_u64), ctypes.POINTER(_c_u64)]),
     "w12_encode_count": (ctypes.c_int, [_c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p]),
@@ -105,6 +130,11 @@ _SIGNATURES = {
     "w12_gemm_e4m3_workspace_size": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, ctypes.POINTER(_c_u64)]),
     "w12_gemm_e4m3": (ctypes.c_int, [_c_p, _c_i32, _c_i64, _c_p, _c_i64, _c_p, _c_i32, _c_i32, _c_i64, _c_p, _c_i64, _c_p,
                                      _c_i64, _c_p, _c_u64, _c_p]),
+    "w12_short_conv": (ctypes.c_int, [ctypes.POINTER(_ConvArgs), ctypes.POINTER(_Sequences), _c_p]),
+    "w12_gated_delta_workspace_size": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, ctypes.POINTER(_c_u64)]),
+    "w12_gated_delta": (ctypes.c_int, [ctypes.POINTER(_DeltaArgs), ctypes.POINTER(_Sequences), _c_p, _c_u64, _c_p]),
+    "w12_verify_draft_workspace_size": (ctypes.c_int, [_c_i32, _c_i32, _c_i32, ctypes.POINTER(_c_u64)]),
+    "w12_verify_draft": (ctypes.c_int, [ctypes.POINTER(_VerifyDraftArgs), _c_p, _c_u64, _c_p]),
     "w12_bits_per_weight": (ctypes.c_double, [_c_i32, _c_i32, _c_i64]),
     "w12_tensor_bytes": (_c_u64, [_c_i32, _c_i32, _c_i64]),
     "w12_status_string": (ctypes.c_char_p, [ctypes.c_int]),

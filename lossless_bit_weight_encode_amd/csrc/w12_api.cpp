@@ -561,6 +561,156 @@ int w12_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const float* x_scale
                     "gemm_e4m3");
 }
 
+// The rows and states of a call: a state array's address is checked by the caller.
+static int check_sequences(const w12_sequences* s) {
+  if (!s) return fail(W12_ERR_INVALID_ARG, "sequences are NULL");
+  if (s->T < 1 || s->T > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "T=%d outside 1..%d", s->T, kMaxRows);
+  if (s->count < 1 || s->count > 1024) return fail(W12_ERR_UNSUPPORTED_SHAPE, "count=%d outside 1..1024", s->count);
+  if (s->slots < 1 || s->slots > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "slots=%d outside 1..%d", s->slots, kMaxRows);
+  if (!s->ptr || !s->src) return fail(W12_ERR_INVALID_ARG, "ptr or src is NULL");
+  if (!aligned(s->ptr, 4) || !aligned(s->lens, 4) || !aligned(s->rows, 4) || !aligned(s->src, 4) || !aligned(s->dst, 4))
+    return fail(W12_ERR_MISALIGNED, "ptr, lens, rows, src and dst must be 4-byte aligned");
+  if (s->tree_mask) {
+    if (s->dst || s->rows || s->lens) return fail(W12_ERR_INVALID_ARG, "a tree has no dst, rows or lens");
+    if (s->mask_words < 1 || s->mask_words > 64)
+      return fail(W12_ERR_UNSUPPORTED_SHAPE, "mask_words=%d outside 1..64", s->mask_words);
+    return check_table(s->tree_mask, s->ld_mask, s->T, s->mask_words, 8, "tree_mask");
+  }
+  if (s->mask_words != 0) return fail(W12_ERR_INVALID_ARG, "mask_words without tree_mask");
+  return W12_OK;
+}
+
+// A state array of `each` elements a slot.
+static int check_state(const void* p, int64_t slot_stride, int64_t each, int32_t slots, int elem_bytes) {
+  if (!p) return fail(W12_ERR_INVALID_ARG, "state is NULL");
+  if (!aligned(p, 16)) return fail(W12_ERR_MISALIGNED, "state must be 16-byte aligned");
+  if (slot_stride < each)
+    return fail(W12_ERR_INVALID_ARG, "slot stride %lld < %lld elements of a state", (long long)slot_stride, (long long)each);
+  if (slot_stride % (16 / elem_bytes))
+    return fail(W12_ERR_MISALIGNED, "slot stride %lld must be a multiple of 16 bytes", (long long)slot_stride);
+  if (slot_stride > (int64_t(1) << 42) / slots) return fail(W12_ERR_UNSUPPORTED_SHAPE, "slot stride too large");
+  return W12_OK;
+}
+
+int w12_short_conv(const w12_conv_args* a, const w12_sequences* s, hipStream_t stream) {
+  if (!a) return fail(W12_ERR_INVALID_ARG, "arguments are NULL");
+  int rc = check_sequences(s);
+  if (rc) return rc;
+  if (a->channels < 1 || a->channels > (1 << 17))
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "channels=%d outside 1..%d", a->channels, 1 << 17);
+  if (a->width < 2 || a->width > 4) return fail(W12_ERR_UNSUPPORTED_SHAPE, "width=%d outside 2..4", a->width);
+  if (!float_dtype(a->dtype)) return fail(W12_ERR_INVALID_ARG, "x and state are BF16 or FP32");
+  const int eb = a->dtype == W12_DTYPE_F32 ? 4 : 2;
+  if ((rc = check_matrix(a->x, a->ldx, s->T, a->channels, eb, "x"))) return rc;
+  if (!a->weight) return fail(W12_ERR_INVALID_ARG, "weight is NULL");
+  if (!aligned(a->weight, 4) || !aligned(a->bias, 2)) return fail(W12_ERR_MISALIGNED, "weight must be 4-byte, bias 2-byte aligned");
+  if (a->tap_stride < a->channels)
+    return fail(W12_ERR_INVALID_ARG, "tap stride %lld < %d channels", (long long)a->tap_stride, a->channels);
+  if (a->tap_stride % (16 / eb))
+    return fail(W12_ERR_MISALIGNED, "tap stride %lld must be a multiple of 16 bytes", (long long)a->tap_stride);
+  if (a->tap_stride > (int64_t(1) << 40)) return fail(W12_ERR_UNSUPPORTED_SHAPE, "tap stride too large");
+  if ((rc = check_state(a->state, a->slot_stride, (a->width - 2) * a->tap_stride + a->channels, s->slots, eb))) return rc;
+  if (a->y && (rc = check_matrix(a->y, a->ldy, s->T, a->channels, 2, "y"))) return rc;
+  if (!a->y && !s->dst) return fail(W12_ERR_INVALID_ARG, "neither outputs nor states are wanted");
+  return hip_status(w12::launch_short_conv(*a, *s, stream), "short_conv");
+}
+
+static int check_delta_shape(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) {
+  if (T < 1 || T > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "T=%d outside 1..%d", T, kMaxRows);
+  if (count < 1 || count > 1024) return fail(W12_ERR_UNSUPPORTED_SHAPE, "count=%d outside 1..1024", count);
+  if (v_heads < 1 || v_heads > 1024) return fail(W12_ERR_UNSUPPORTED_SHAPE, "v_heads=%d outside 1..1024", v_heads);
+  if (dk != 64 && dk != 128) return fail(W12_ERR_UNSUPPORTED_SHAPE, "dk=%d is not 64 or 128", dk);
+  if (dv != 64 && dv != 128 && dv != 256) return fail(W12_ERR_UNSUPPORTED_SHAPE, "dv=%d is not 64, 128 or 256", dv);
+  return W12_OK;
+}
+
+int w12_gated_delta_workspace_size(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv, uint64_t* bytes) {
+  int rc = check_delta_shape(T, count, v_heads, dk, dv);
+  if (rc) return rc;
+  if (!bytes) return fail(W12_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = w12::gated_delta_workspace_bytes(T, count, v_heads, dk, dv);
+  return ok();
+}
+
+int w12_gated_delta(const w12_delta_args* a, const w12_sequences* s, void* ws, uint64_t ws_bytes, hipStream_t stream) {
+  if (!a) return fail(W12_ERR_INVALID_ARG, "arguments are NULL");
+  int rc = check_sequences(s);
+  if (rc) return rc;
+  if ((rc = check_delta_shape(s->T, s->count, a->v_heads, a->dk, a->dv))) return rc;
+  if (a->reserved != 0) return fail(W12_ERR_INVALID_ARG, "reserved field must be 0");
+  if (a->k_heads < 1 || a->v_heads % a->k_heads)
+    return fail(W12_ERR_UNSUPPORTED_SHAPE, "v_heads=%d is not a multiple of k_heads=%d", a->v_heads, a->k_heads);
+  if (!(a->eps >= 0.0f)) return fail(W12_ERR_INVALID_ARG, "eps must not be negative");
+  if (!(a->scale >= -1e30f && a->scale <= 1e30f)) return fail(W12_ERR_INVALID_ARG, "scale must be finite");
+  const int64_t kw = (int64_t)a->k_heads * a->dk, vw = (int64_t)a->v_heads * a->dv;
+  if ((a->q == nullptr) != (a->out == nullptr)) return fail(W12_ERR_INVALID_ARG, "q and out go together");
+  if (a->q && (rc = check_matrix(a->q, a->ldq, s->T, kw, 2, "q"))) return rc;
+  if ((rc = check_matrix(a->k, a->ldk, s->T, kw, 2, "k"))) return rc;
+  if ((rc = check_matrix(a->v, a->ldv, s->T, vw, 2, "v"))) return rc;
+  if ((rc = check_table(a->g, a->ldg, s->T, a->v_heads, 4, "g"))) return rc;
+  if ((rc = check_table(a->beta, a->ldbeta, s->T, a->v_heads, 4, "beta"))) return rc;
+  if ((rc = check_state(a->state, a->slot_stride, vw * a->dk, s->slots, 4))) return rc;
+  if (a->out && (rc = check_matrix(a->out, a->ldo, s->T, vw, 2, "out"))) return rc;
+  if (!a->out && !s->dst) return fail(W12_ERR_INVALID_ARG, "neither outputs nor states are wanted");
+  const uint64_t need = w12::gated_delta_workspace_bytes(s->T, s->count, a->v_heads, a->dk, a->dv);
+  if (ws_bytes < need)
+    return fail(W12_ERR_WORKSPACE_TOO_SMALL, "workspace %llu bytes < %llu needed", (unsigned long long)ws_bytes,
+                (unsigned long long)need);
+  if (need && !ws) return fail(W12_ERR_INVALID_ARG, "ws is NULL");
+  if (ws && !aligned(ws, 16)) return fail(W12_ERR_MISALIGNED, "ws must be 16-byte aligned");
+  return hip_status(w12::launch_gated_delta(*a, *s, ws, stream), "gated_delta");
+}
+
+static int check_verify_draft_shape(int32_t T, int32_t requests, int32_t vocab) {
+  if (T < 1 || T > kMaxRows) return fail(W12_ERR_UNSUPPORTED_SHAPE, "T=%d outside 1..%d", T, kMaxRows);
+  if (requests < 1 || requests > 1024) return fail(W12_ERR_UNSUPPORTED_SHAPE, "requests=%d outside 1..1024", requests);
+  if (vocab < 1 || vocab > (1 << 24)) return fail(W12_ERR_UNSUPPORTED_SHAPE, "vocab=%d outside 1..2^24", vocab);
+  if ((int64_t)T * vocab >= (int64_t(1) << 40)) return fail(W12_ERR_UNSUPPORTED_SHAPE, "T * vocab must be below 2^40");
+  return W12_OK;
+}
+
+int w12_verify_draft_workspace_size(int32_t T, int32_t requests, int32_t vocab, uint64_t* bytes) {
+  int rc = check_verify_draft_shape(T, requests, vocab);
+  if (rc) return rc;
+  if (!bytes) return fail(W12_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = w12::verify_draft_workspace_bytes(T, requests, vocab);
+  return ok();
+}
+
+int w12_verify_draft(const w12_verify_draft_args* a, void* ws, uint64_t ws_bytes, hipStream_t stream) {
+  if (!a) return fail(W12_ERR_INVALID_ARG, "arguments are NULL");
+  int rc = check_verify_draft_shape(a->T, a->requests, a->vocab);
+  if (rc) return rc;
+  if (a->reserved != 0) return fail(W12_ERR_INVALID_ARG, "reserved field must be 0");
+  if (!float_dtype(a->logits_dtype)) return fail(W12_ERR_INVALID_ARG, "logits are BF16 or FP32");
+  if ((rc = check_matrix(a->logits, a->ld_logits, a->T, a->vocab, a->logits_dtype == W12_DTYPE_F32 ? 4 : 2, "logits"))) return rc;
+  if (a->q) {
+    if (a->tree_mask) return fail(W12_ERR_INVALID_ARG, "q goes with chains, not with a tree_mask");
+    if ((rc = check_matrix(a->q, a->ldq, a->T, a->vocab, 4, "q"))) return rc;
+  }
+  if ((a->q == nullptr) != (a->accept_u == nullptr)) return fail(W12_ERR_INVALID_ARG, "q and accept_u go together");
+  if (a->tree_mask) {
+    if (a->mask_words < 1 || a->mask_words > 64)
+      return fail(W12_ERR_UNSUPPORTED_SHAPE, "mask_words=%d outside 1..64", a->mask_words);
+    if ((rc = check_table(a->tree_mask, a->ld_mask, a->T, a->mask_words, 8, "tree_mask"))) return rc;
+  } else if (a->mask_words != 0) {
+    return fail(W12_ERR_INVALID_ARG, "mask_words without tree_mask");
+  }
+  if (!a->tokens || !a->node_ptr || !a->u || !a->path || !a->count || !a->next_token)
+    return fail(W12_ERR_INVALID_ARG, "tokens, node_ptr, u, path, count or next_token is NULL");
+  const void* words[] = {a->tokens, a->node_ptr, a->u, a->accept_u, a->temperature, a->path, a->count, a->next_token};
+  for (const void* p : words)
+    if (!aligned(p, 4))
+      return fail(W12_ERR_MISALIGNED, "tokens, node_ptr, random numbers, temperature and outputs must be 4-byte aligned");
+  const uint64_t need = w12::verify_draft_workspace_bytes(a->T, a->requests, a->vocab);
+  if (ws_bytes < need)
+    return fail(W12_ERR_WORKSPACE_TOO_SMALL, "workspace %llu bytes < %llu needed", (unsigned long long)ws_bytes,
+                (unsigned long long)need);
+  if (!ws) return fail(W12_ERR_INVALID_ARG, "ws is NULL");
+  if (!aligned(ws, 16)) return fail(W12_ERR_MISALIGNED, "ws must be 16-byte aligned");
+  return hip_status(w12::launch_verify_draft(*a, ws, stream), "verify_draft");
+}
+
 double w12_bits_per_weight(int32_t N, int32_t K, int64_t E) {
   if (N < 1 || K < 1 || E < 0) return -1.0;
   const double nk = (double)N * (double)K;

@@ -1,0 +1,159 @@
+// The gated delta rule, token by token.
+//
+//   S <- exp(g) S + k (beta (v - exp(g) S^T k))^T,  out = scale S^T q.
+//
+// The columns of S (one per element of v) do not depend on one another.  A column lies along the lanes of a wave,
+// 8 values a lane, so that S^T k and S^T q are sums over 8 or 16 lanes (of the old state both: S'^T q = exp(g) S^T q + (k . q) u);
+// a wave holds 16 columns in registers and walks through its tokens without a barrier.
+#include "w12_gemm_common.h"
+#include "w12_kernels.h"
+#include "w12_rows.h"
+#include "w12_sequences.h"
+
+namespace w12 {
+
+constexpr int kDeltaThreads = 256;
+constexpr int kWaveColumns = 16;
+constexpr int kGroupColumns = kWaveColumns * kDeltaThreads / 64;
+
+// The sum over the L lanes (8 or 16) that share a column; every lane gets it.
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, true));
+}
+template <int L>
+__device__ __forceinline__ float lane_sum(float v) {
+  v = dpp_add<0xB1>(v);       // lanes 1 away
+  v = dpp_add<0x4E>(v);       // 2 away
+  v = dpp_add<0x141>(v);      // the other four of eight
+  if constexpr (L == 16) v = dpp_add<0x140>(v);   // the other eight
+  return v;
+}
+
+// A token of one value head: this lane's piece of k and q, its columns' values, and the scalars.
+template <int PASSES>
+struct Token {
+  float k[8], q[8], v[PASSES], g, beta;
+};
+
+template <int DK>
+__global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a, w12_sequences s) {
+  constexpr int L = DK / 8, P = 64 / L, PASSES = kWaveColumns / P;
+  const int lane = threadIdx.x & 63, h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
+  const int col = blockIdx.z * kGroupColumns + wave_id() * kWaveColumns + lane / L, piece = lane % L * 8;
+  // a tree's row goes down its own path; a sequence's tokens one after another
+  int b = blockIdx.x, node = 0;
+  Range r;
+  if (s.tree_mask) {
+    const int row = blockIdx.x;
+    int lo = 0, hi = s.count;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.ptr[mid] <= row) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    r = range_of(s, b);
+    node = row - r.start;
+    if (node < 0 || node >= r.n) return;
+  } else {
+    r = range_of(s, b);
+  }
+  const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
+  float st[PASSES][8];
+#pragma unroll
+  for (int p = 0; p < PASSES; ++p) {
+    if (src >= 0) {
+      const float4* at = reinterpret_cast<const float4*>(a.state + src * a.slot_stride + ((int64_t)h * a.dv + col + p * P) * DK + piece);
+      const float4 x = at[0], y = at[1];
+      st[p][0] = x.x; st[p][1] = x.y; st[p][2] = x.z; st[p][3] = x.w;
+      st[p][4] = y.x; st[p][5] = y.y; st[p][6] = y.z; st[p][7] = y.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) st[p][e] = 0.0f;
+    }
+  }
+  auto load = [&](int row, Token<PASSES>& t) {
+    if (row < 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) t.k[e] = t.q[e] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < PASSES; ++p) t.v[p] = 0.0f;
+      t.g = t.beta = 0.0f;
+      return;
+    }
+    unpack_bf16x8(*reinterpret_cast<const uint4*>(a.k + row * a.ldk + hk * DK + piece), t.k);
+    if (a.q) unpack_bf16x8(*reinterpret_cast<const uint4*>(a.q + row * a.ldq + hk * DK + piece), t.q);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) t.v[p] = bf16_float(a.v[row * a.ldv + h * a.dv + col + p * P]);
+    t.g = a.g[row * a.ldg + h];
+    t.beta = a.beta[row * a.ldbeta + h];
+  };
+  uint64_t path = s.tree_mask ? ancestors(s, r.start, node) | (uint64_t)1 << node : 0;
+  for (int i = 0; s.tree_mask ? path != 0 : i < r.n; ++i) {
+    int at = i;
+    if (s.tree_mask) {
+      at = __builtin_ctzll(path);
+      path &= path - 1;
+    }
+    const int row = row_of(s, r.start + at);
+    Token<PASSES> t;
+    load(row, t);
+    float kk = 0.0f, qq = 0.0f, kq = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      kk += t.k[e] * t.k[e];
+      if (a.q) {
+        qq += t.q[e] * t.q[e];
+        kq += t.k[e] * t.q[e];
+      }
+    }
+    kk = lane_sum<L>(kk);
+    float rk = 1.0f, rq = a.scale;
+    if (a.l2norm) rk = 1.0f / sqrtf(kk + a.eps);
+    if (a.q) {
+      qq = lane_sum<L>(qq);
+      kq = lane_sum<L>(kq);
+      if (a.l2norm) rq *= 1.0f / sqrtf(qq + a.eps);
+    }
+    const float grown = expf(t.g);
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      float sk = 0.0f, sq = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sk += st[p][e] * t.k[e];
+        if (a.q) sq += st[p][e] * t.q[e];
+      }
+      sk = lane_sum<L>(sk);
+      const float u = t.beta * (t.v[p] - grown * rk * sk);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) st[p][e] = grown * st[p][e] + rk * t.k[e] * u;
+      if (a.q) {
+        sq = lane_sum<L>(sq);
+        const float o = rq * (grown * sq + rk * kq * u);
+        if (lane % L == 0 && row >= 0 && (!s.tree_mask || at == node))
+          a.out[row * a.ldo + h * a.dv + col + p * P] = (uint16_t)bf16_pair(o, o);
+      }
+    }
+  }
+  if (dst >= 0) {
+#pragma unroll
+    for (int p = 0; p < PASSES; ++p) {
+      float4* at = reinterpret_cast<float4*>(a.state + dst * a.slot_stride + ((int64_t)h * a.dv + col + p * P) * DK + piece);
+      at[0] = make_float4(st[p][0], st[p][1], st[p][2], st[p][3]);
+      at[1] = make_float4(st[p][4], st[p][5], st[p][6], st[p][7]);
+    }
+  }
+}
+
+uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) { return 0; }
+
+hipError_t launch_gated_delta(const w12_delta_args& a, const w12_sequences& s, void* ws, hipStream_t stream) {
+  const dim3 grid((unsigned)(s.tree_mask ? s.T : s.count), (unsigned)a.v_heads, (unsigned)(a.dv / kGroupColumns));
+  if (a.dk == 64) k_delta_steps<64><<<grid, kDeltaThreads, 0, stream>>>(a, s);
+  else k_delta_steps<128><<<grid, kDeltaThreads, 0, stream>>>(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace w12
