@@ -29,7 +29,7 @@ ARCH = os.environ.get("W12_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["w12_encode.hip", "w12_decode.hip", "w12_gemm.hip", "w12_gemm_wide.hip", "w12_probe.hip", "w12_noalloc.hip",
            "w12_norm.hip", "w12_rope.hip", "w12_attention.hip", "w12_gemm_e4m3.hip",
-           "w12_conv.hip", "w12_delta.hip", "w12_verify_draft.hip", "w12_api.cpp", "w12_file.cpp"]
+           "w12_conv.hip", "w12_delta.hip", "w12_delta_chunk.hip", "w12_verify_draft.hip", "w12_api.cpp", "w12_file.cpp"]
 
 COMMON = [
     f"--offload-arch={ARCH}",

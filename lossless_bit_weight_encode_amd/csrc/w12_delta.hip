@@ -41,24 +41,8 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
   constexpr int L = DK / 8, P = 64 / L, PASSES = kWaveColumns / P;
   const int lane = threadIdx.x & 63, h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
   const int col = blockIdx.z * kGroupColumns + wave_id() * kWaveColumns + lane / L, piece = lane % L * 8;
-  // a tree's row goes down its own path; a sequence's tokens one after another
-  int b = blockIdx.x, node = 0;
-  Range r;
-  if (s.tree_mask) {
-    const int row = blockIdx.x;
-    int lo = 0, hi = s.count;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s.ptr[mid] <= row) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    r = range_of(s, b);
-    node = row - r.start;
-    if (node < 0 || node >= r.n) return;
-  } else {
-    r = range_of(s, b);
-  }
+  const int b = blockIdx.x;
+  const Range r = range_of(s, b);
   const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
   float st[PASSES][8];
 #pragma unroll
@@ -89,14 +73,8 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
     t.g = a.g[row * a.ldg + h];
     t.beta = a.beta[row * a.ldbeta + h];
   };
-  uint64_t path = s.tree_mask ? ancestors(s, r.start, node) | (uint64_t)1 << node : 0;
-  for (int i = 0; s.tree_mask ? path != 0 : i < r.n; ++i) {
-    int at = i;
-    if (s.tree_mask) {
-      at = __builtin_ctzll(path);
-      path &= path - 1;
-    }
-    const int row = row_of(s, r.start + at);
+  for (int i = 0; i < r.n; ++i) {
+    const int row = row_of(s, r.start + i);
     Token<PASSES> t;
     load(row, t);
     float kk = 0.0f, qq = 0.0f, kq = 0.0f;
@@ -132,7 +110,7 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
       if (a.q) {
         sq = lane_sum<L>(sq);
         const float o = rq * (grown * sq + rk * kq * u);
-        if (lane % L == 0 && row >= 0 && (!s.tree_mask || at == node))
+        if (lane % L == 0 && row >= 0)
           a.out[row * a.ldo + h * a.dv + col + p * P] = (uint16_t)bf16_pair(o, o);
       }
     }
@@ -147,10 +125,17 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
   }
 }
 
-uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) { return 0; }
+// Tokens a sequence has, on average, from which they are taken 64 at a time.
+constexpr int kChunkFrom = 16;
+static bool in_chunks(const w12_sequences& s) { return s.tree_mask || s.T >= (int64_t)kChunkFrom * s.count; }
+
+uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) {
+  return delta_chunk_workspace_bytes(T, count, v_heads);
+}
 
 hipError_t launch_gated_delta(const w12_delta_args& a, const w12_sequences& s, void* ws, hipStream_t stream) {
-  const dim3 grid((unsigned)(s.tree_mask ? s.T : s.count), (unsigned)a.v_heads, (unsigned)(a.dv / kGroupColumns));
+  if (in_chunks(s)) return launch_delta_chunks(a, s, ws, stream);
+  const dim3 grid((unsigned)s.count, (unsigned)a.v_heads, (unsigned)(a.dv / kGroupColumns));
   if (a.dk == 64) k_delta_steps<64><<<grid, kDeltaThreads, 0, stream>>>(a, s);
   else k_delta_steps<128><<<grid, kDeltaThreads, 0, stream>>>(a, s);
   return hipGetLastError();

@@ -1,0 +1,33 @@
+// What the two kernels of the chunked gated delta rule hand over, by chunk and value head.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace w12 {
+
+constexpr int kChunk = 64;
+
+// Operands of rows 16 rt .. and tokens 32 ks .. of a lower triangular 64 x 64 matrix: of those that are not all zero, the number.
+__host__ __device__ constexpr int fragment_of(int rt, int ks) { return rt < 2 ? rt : 2 * rt - 2 + ks; }
+constexpr int kFragments = 6;
+// Its 16 x 16 blocks (r, s), r >= s.
+__host__ __device__ constexpr int block_of(int r, int s) { return r * (r + 1) / 2 + s; }
+
+// The workspace starts with a row of zeros, in place of tokens that are not there.
+constexpr int kZeroBytes = 256;
+
+// T = (I + A)^-1 as two BF16 matrices, P as one (each fragment 16 bytes a lane), then FP32 vectors over the rows: beta e^G / |k|, beta,
+// scale e^G / |q|, e^(G_last - G) / |k|, and behind them e^G_last and (2 words further) a bit for each row that is no number.
+constexpr int kTermsBytes = (3 * kFragments + 2) * 1024;
+struct Terms {
+  char* at;
+  typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+  __device__ Terms(char* ws, int64_t i) : at(ws + i * kTermsBytes) {}
+  __device__ bf8* t_high(int f) const { return reinterpret_cast<bf8*>(at + f * 1024); }
+  __device__ bf8* t_low(int f) const { return t_high(kFragments + f); }
+  __device__ bf8* p(int f) const { return t_high(2 * kFragments + f); }
+  __device__ float* vectors() const { return reinterpret_cast<float*>(at + 3 * kFragments * 1024); }
+};
+
+}  // namespace w12

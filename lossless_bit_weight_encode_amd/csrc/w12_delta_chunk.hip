@@ -1,0 +1,522 @@
+// The gated delta rule, 64 tokens at a time.
+//
+// With G_i the sum of g up to token i of a chunk (in a tree: down its path) and "before" the tokens before (ancestors of) one,
+//   (I + A) U = diag(beta) (V - diag(e^G) K S),   A_ij = beta_i e^(G_i - G_j) k_i . k_j   for j before i,
+//   out = scale (diag(e^G) Q S + (e^(G_i - G_j) q_i . k_j) U),    S' = e^G_last S + sum_j e^(G_last - G_j) k_j u_j^T.
+// k_delta_terms makes what does not depend on S, for all chunks at once: T = (I + A)^-1, the factors P of out and the rows'
+// scalars.  k_delta_scan walks through a sequence's chunks with 16 columns of S in a wave's registers.
+//
+// Matrix instructions: 16x16x32 BF16.  Their results (a lane: one column, 4 neighbouring rows) are the next ones' right operand
+// (a lane: one column, 8 of the summed index) without a move: where a result's rows are tokens, T and P are laid out in
+// the order that this gives, and where they are S's, the rows of S are numbered so that it is the order of K in memory.
+// k, q and v are BF16 and exact; K S, T R and K^T U take what is FP32 as two BF16 values (hi + lo, off by 2^-16 at most; of T R
+// without the product of the two lows), so that the states keep nearly all of FP32; out, which is rounded to
+// BF16, takes one each of S, U and P.  T is made in FP32 throughout: 16 x 16 blocks by substitution (which does not
+// cancel as powers of A would), joined by FP32 matrix instructions.
+#include "w12_delta_chunk.h"
+#include "w12_gemm_common.h"
+#include "w12_kernels.h"
+#include "w12_rows.h"
+#include "w12_sequences.h"
+
+namespace w12 {
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4v __attribute__((ext_vector_type(4)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+constexpr int kChunkThreads = 256;
+
+__device__ __forceinline__ f32x4v mma(bf8 a, bf8 b, f32x4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ f32x4v mma32(float a, float b, f32x4v c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(a, b, c, 0, 0, 0); }
+// a 16 x 16 product of FP32: a holds A[row][4 g .. 4 g + 3] of the lane's row, b a result (its column, rows 4 g .. 4 g + 3)
+__device__ __forceinline__ f32x4v mma_block(f32x4v a, f32x4v b, f32x4v c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = mma32(a[i], b[i], c);
+  return c;
+}
+
+__device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
+
+// Eight FP32 values as BF16, and what that leaves over as BF16.
+__device__ __forceinline__ bf8 high(f32x4v a, f32x4v b) {
+  const u32x4v r = {bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
+  return __builtin_bit_cast(bf8, r);
+}
+__device__ __forceinline__ bf8 low(f32x4v a, f32x4v b, bf8 hi) {
+  const u32x4v h = __builtin_bit_cast(u32x4v, hi);
+  u32x4v r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+    r[i] = bf16_pair(x - bf16_float(h[i]), y - __builtin_bit_cast(float, h[i] & 0xFFFF0000u));
+  }
+  return __builtin_bit_cast(bf8, r);
+}
+
+// Rows of keys or queries in LDS: 16-byte pieces, swizzled by row so that a column of pieces (of 16 rows) and 4 neighbouring
+// pieces of 4 neighbouring rows both spread over the banks.
+template <int DK>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+  constexpr int P = DK / 8;
+  const int s = P == 16 ? (row & 3) << 2 | (row >> 2 & 3) : (row & 1) << 2 | (row >> 1 & 3);
+  return (row * P + (piece ^ s)) * 16;
+}
+// A lane's operand of rows 16 rt .. + 15 (row lane % 16) and values 32 ks + 8 (lane / 16) .. + 7.
+template <int DK>
+__device__ __forceinline__ bf8 rows_operand(const char* m, int rt, int ks) {
+  const int lane = threadIdx.x & 63;
+  return *reinterpret_cast<const bf8*>(m + piece_at<DK>(16 * rt + (lane & 15), 4 * ks + (lane >> 4)));
+}
+
+// ------------------------------------------------------------------------------------------- terms
+
+template <int DK>
+__global__ __launch_bounds__(kChunkThreads) void k_delta_terms(w12_delta_args a, w12_sequences s, char* ws) {
+  __shared__ __attribute__((aligned(16))) char km[kChunk * DK * 2], qm[kChunk * DK * 2];
+  __shared__ f32x4v ablk[10][64];                // A's blocks (r, s), r >= s: a lane's column, rows 4 g .. + 3
+  __shared__ f32x4v dblk[4][64];                 // inverses of the diagonal blocks, the same
+  __shared__ float turn[4][16][20];
+  __shared__ double total[kChunk];
+  __shared__ float rk[kChunk], rq[kChunk], beta[kChunk];
+  __shared__ uint64_t anc[kChunk];
+  __shared__ uint32_t badrow[2];
+  __shared__ int found[2];
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
+  const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
+  if (blockIdx.x == 0 && h == 0 && tid < kZeroBytes / 16) reinterpret_cast<uint4*>(ws)[tid] = make_uint4(0, 0, 0, 0);
+  int b, chunk;
+  Range r;
+  if (!find_piece(s, blockIdx.x, kChunk, found, b, r, chunk)) return;
+  const int first = chunk * kChunk, m = min(kChunk, r.n - first);
+  if (m <= 0) return;
+  if (tid < 2) badrow[tid] = 0;
+  // rows of K and Q, four threads a row; the sums of their squares
+  {
+    const int row_in = tid >> 2, quarter = tid & 3;
+    const int row = row_in < m ? row_of(s, r.start + first + row_in) : -1;
+    constexpr int N = DK / 32;                   // 16-byte pieces of a quarter
+    float kk = 0.0f, qq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int p = i * 4 + quarter;
+      uint4 ku = make_uint4(0, 0, 0, 0), qu = ku;
+      if (row >= 0) {
+        ku = *reinterpret_cast<const uint4*>(a.k + row * a.ldk + hk * DK + p * 8);
+        if (a.q) qu = *reinterpret_cast<const uint4*>(a.q + row * a.ldq + hk * DK + p * 8);
+      }
+      float v[8];
+      unpack_bf16x8(ku, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) kk += v[e] * v[e];
+      unpack_bf16x8(qu, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) qq += v[e] * v[e];
+      *reinterpret_cast<uint4*>(km + piece_at<DK>(row_in, p)) = ku;
+      *reinterpret_cast<uint4*>(qm + piece_at<DK>(row_in, p)) = qu;
+    }
+    kk += __shfl_xor(kk, 1);
+    kk += __shfl_xor(kk, 2);
+    qq += __shfl_xor(qq, 1);
+    qq += __shfl_xor(qq, 2);
+    float ik = 0.0f, iq = 0.0f, gv = 0.0f, bv = 0.0f;
+    if (row >= 0) {
+      ik = a.l2norm ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
+      iq = a.scale * (a.l2norm ? 1.0f / sqrtf(qq + a.eps) : 1.0f);
+      gv = a.g[row * a.ldg + h];
+      bv = a.beta[row * a.ldbeta + h];
+    }
+    // a row whose key, decay or strength is no number is taken out here, and made up for where the results are stored; -inf for a
+    // decay is one: like anything below -1e4 it clears the state
+    const bool bad = !finite(kk) || !finite(ik) || !(gv < INFINITY) || !finite(bv);
+    __syncthreads();
+    if (bad) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(km + piece_at<DK>(row_in, i * 4 + quarter)) = make_uint4(0, 0, 0, 0);
+    }
+    if (quarter == 0) {
+      if (bad) atomicOr(&badrow[row_in >> 5], 1u << (row_in & 31));
+      rk[row_in] = bad ? 0.0f : ik;
+      rq[row_in] = iq;
+      beta[row_in] = bad ? 0.0f : bv;
+      total[row_in] = bad ? 0.0 : (double)fmaxf(gv, -1e4f);
+      anc[row_in] = row_in < m ? ancestors(s, r.start + first, row_in) : 0;
+    }
+  }
+  __syncthreads();
+  // sums of g: of all tokens up to a row's, or down its path; every wave for itself, as all need the last one
+  double gsum = total[lane];
+  if (s.tree_mask) {
+    uint64_t path = anc[lane];
+    while (path) {
+      gsum += total[__builtin_ctzll(path)];
+      path &= path - 1;
+    }
+  } else {
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const double u = __shfl_up(gsum, o);
+      if (lane >= o) gsum += u;
+    }
+  }
+  __syncthreads();
+  if (w == 0) total[lane] = gsum;
+  __syncthreads();
+  Terms out(ws + kZeroBytes, (int64_t)blockIdx.x * a.v_heads + h);
+  const double last = total[kChunk - 1];
+  if (w == 0) {
+    const float grown = expf((float)gsum);
+    float* vec = out.vectors();
+    vec[lane] = beta[lane] * grown * rk[lane];
+    vec[64 + lane] = beta[lane];
+    vec[128 + lane] = grown * rq[lane];
+    vec[192 + lane] = expf((float)(last - gsum)) * rk[lane];
+    if (lane == 0) {
+      vec[256] = expf((float)last);
+      vec[257] = 0.0f;
+      reinterpret_cast<uint32_t*>(vec)[258] = badrow[0];
+      reinterpret_cast<uint32_t*>(vec)[259] = badrow[1];
+    }
+  }
+  // block row w of A (rows of tile w against columns of tiles 0 .. w), and of P turned (a lane: a row of P, 4 neighbouring columns)
+  f32x4v pt[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    pt[t] = f32x4v{0, 0, 0, 0};
+    if (t > w) continue;
+    f32x4v kk = {0, 0, 0, 0}, kq = kk;
+#pragma unroll
+    for (int ks = 0; ks < DK / 32; ++ks) {
+      const bf8 kt = rows_operand<DK>(km, t, ks);
+      kk = mma(rows_operand<DK>(km, w, ks), kt, kk);
+      if (a.q) kq = mma(kt, rows_operand<DK>(qm, w, ks), kq);
+    }
+    f32x4v ab;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = 16 * w + 4 * g4 + i, col = 16 * t + c16;
+      ab[i] = anc[row] >> col & 1 ? beta[row] * rk[row] * rk[col] * expf((float)(total[row] - total[col])) * kk[i] : 0.0f;
+      const int prow = 16 * w + c16, pcol = 16 * t + 4 * g4 + i;
+      const bool sees = (anc[prow] | (uint64_t)1 << prow) >> pcol & 1;
+      pt[t][i] = sees ? rq[prow] * rk[pcol] * expf((float)(total[prow] - total[pcol])) * kq[i] : 0.0f;
+    }
+    ablk[block_of(w, t)][lane] = ab;
+  }
+  __syncthreads();
+  // the inverse of diagonal block w: a lane's column by substitution (the four groups of lanes do the same)
+  float d[16];
+  {
+    const float* blk = reinterpret_cast<const float*>(ablk[block_of(w, w)]);      // [column][4 (row / 4)][row % 4]
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x = i == c16 ? 1.0f : 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) x -= blk[(j + 16 * (i >> 2)) * 4 + (i & 3)] * d[j];
+      d[i] = x;
+    }
+  }
+  f32x4v mine;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mine[i] = g4 == 0 ? d[i] : g4 == 1 ? d[4 + i] : g4 == 2 ? d[8 + i] : d[12 + i];
+  dblk[w][lane] = mine;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) turn[w][4 * g4 + i][c16] = mine[i];
+  __syncthreads();
+  // block row w of T, turned: X_w = D_w^T, X_t = -D_t^T sum_{t < u <= w} A_ut^T X_u
+  f32x4v x[4];
+#pragma unroll
+  for (int t = 3; t >= 0; --t) {
+    x[t] = f32x4v{0, 0, 0, 0};
+    if (t == w) x[t] = *reinterpret_cast<const f32x4v*>(&turn[w][c16][4 * g4]);
+    if (t >= w) continue;
+    f32x4v sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 3; u > t; --u)
+      if (u <= w) sum = mma_block(ablk[block_of(u, t)][lane], x[u], sum);
+    const f32x4v none = {0, 0, 0, 0};
+    x[t] = none - mma_block(dblk[t][lane], sum, none);
+  }
+#pragma unroll
+  for (int ks = 0; ks < 2; ++ks) {
+    if (ks > w >> 1) continue;
+    const int f = fragment_of(w, ks);
+    const bf8 hi = high(x[2 * ks], x[2 * ks + 1]);
+    out.t_high(f)[lane] = hi;
+    out.t_low(f)[lane] = low(x[2 * ks], x[2 * ks + 1], hi);
+    if (a.q) out.p(f)[lane] = high(pt[2 * ks], pt[2 * ks + 1]);
+  }
+}
+
+// -------------------------------------------------------------------------------------------- scan
+
+// 16 bytes a lane from memory to the wave's 1 KB of LDS at `at`.  Not through the builtin: the compiler would wait for it before
+// every read of LDS.
+__device__ __forceinline__ void to_lds(const void* from, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               : : "s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(from) : "memory", "m0");
+}
+
+constexpr int kPairs = 2;                        // pairs of waves of a work-group, of 16 columns each
+constexpr int kScanColumns = 16 * kPairs;
+
+template <int DK>
+struct ScanLds {
+  char k[2][kChunk * DK * 2], q[2][kChunk * DK * 2];
+  bf8 t[2][2 * kFragments][64], p[2][kFragments][64];
+  float vec[2][512];
+  bf8 s[kPairs][2][DK / 32][64];                 // from a pair's first wave to its second: S before a chunk,
+  bf8 u[kPairs][2][2][64];                       // its U,
+  uint64_t bad[kPairs][2][16];                   // and by column the tokens that were no numbers
+  float a2[2][kChunk];
+};
+
+// A pair's first wave carries S through the chunks; its second makes the outputs of the chunk before, from what the first left.
+template <int DK>
+__global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args a, w12_sequences s, const char* ws) {
+  constexpr int KS = DK / 32, RT = DK / 16;
+  __shared__ __attribute__((aligned(16))) ScanLds<DK> lds;
+  const int lane = threadIdx.x & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
+  const int pair = w >> 1;
+  const bool second = w & 1;
+  // the column blocks of a head read the same rows and terms: neighbours, on one XCD
+  const int blocks = a.dv / kScanColumns;
+  const int64_t at = logical_wg(blockIdx.x, gridDim.x);
+  const int cb = (int)(at % blocks), h = (int)(at / blocks % a.v_heads), b = (int)(at / blocks / a.v_heads);
+  const int hk = h / (a.v_heads / a.k_heads);
+  const Range r = range_of(s, b);
+  const int chunks = (r.n + kChunk - 1) / kChunk;
+  const int64_t piece0 = first_piece(r, b, kChunk);
+  const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
+  const int col = cb * kScanColumns + pair * 16 + c16;
+  const int64_t state_at = ((int64_t)h * a.dv + col) * DK + 8 * g4;
+  const char* zeros = ws;                        // the first row of the workspace
+  const char* terms = ws + kZeroBytes;
+
+  f32x4v st[RT];
+  if (!second) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      f32x4v x = {0, 0, 0, 0}, y = x;
+      if (src >= 0) {
+        const f32x4v* p = reinterpret_cast<const f32x4v*>(a.state + src * a.slot_stride + state_at + 32 * ks);
+        x = p[0];
+        y = p[1];
+      }
+      st[2 * ks] = x;
+      st[2 * ks + 1] = y;
+    }
+  }
+  // rows of K or Q on their way: 16 bytes a lane, 1024 / (2 DK) rows an instruction of a wave
+  constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kEach = kChunk / kRows / 4;
+  auto fetch_rows = [&](const uint16_t* from, int64_t ld, int chunk, const char* to) {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int first = (w * kEach + i) * kRows, row_in = first + lane / kLanes, token = chunk * kChunk + row_in;
+      const int row = token < r.n ? row_of(s, r.start + token) : -1;
+      const int piece = (piece_at<DK>(row_in, lane % kLanes) >> 4) % kLanes;      // the piece that belongs in this place
+      const void* p = row >= 0 ? static_cast<const void*>(from + row * ld + hk * DK + piece * 8) : zeros + piece * 16;
+      to_lds(p, lds_off(to) + first * DK * 2);
+    }
+  };
+  auto fetch_fragments = [&](const void* from, int count, const void* to) {
+    for (int i = w; i < count; i += 4) to_lds(static_cast<const char*>(from) + i * 1024 + lane * 16, lds_off(to) + i * 1024);
+  };
+  auto terms_of = [&](int chunk) { return Terms(const_cast<char*>(terms), (piece0 + chunk) * a.v_heads + h); };
+  auto fetch_first = [&](int chunk) {
+    Terms t = terms_of(chunk);
+    fetch_rows(a.k, a.ldk, chunk, lds.k[chunk & 1]);
+    fetch_fragments(t.t_high(0), 2 * kFragments, lds.t[chunk & 1]);
+    fetch_fragments(t.vectors(), 2, lds.vec[chunk & 1]);
+  };
+  auto fetch_second = [&](int chunk) {
+    if (!a.q) return;
+    fetch_rows(a.q, a.ldq, chunk, lds.q[chunk & 1]);
+    fetch_fragments(terms_of(chunk).p(0), kFragments, lds.p[chunk & 1]);
+  };
+  uint16_t v[16];
+  auto fetch_v = [&](int chunk) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int token = chunk * kChunk + 16 * (i >> 2) + 4 * g4 + (i & 3);
+      const int row = token < r.n ? row_of(s, r.start + token) : -1;
+      v[i] = row >= 0 ? a.v[row * a.ldv + h * a.dv + col] : (uint16_t)0;
+    }
+  };
+  if (chunks) {
+    fetch_first(0);
+    if (!second) fetch_v(0);
+  }
+  wait_vm_all();
+  lds_barrier();
+  for (int c = 0; c <= chunks; ++c) {
+    const int buf = c & 1;
+    if (c + 1 < chunks) fetch_first(c + 1);
+    if (c < chunks) fetch_second(c);
+    if (!second && c < chunks) {
+      const float* vec = lds.vec[buf];
+      bf8 sh[KS], sl[KS];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
+        sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
+        lds.s[pair][buf][ks][lane] = sh[ks];
+      }
+      f32x4v ks_[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) ks_[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const bf8 k = rows_operand<DK>(lds.k[buf], rt, ks);
+          ks_[rt] = mma(k, sh[ks], ks_[rt]);
+          ks_[rt] = mma(k, sl[ks], ks_[rt]);
+        }
+      bool bad = false;
+      f32x4v rr[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const f32x4v a1 = *reinterpret_cast<const f32x4v*>(vec + 16 * rt + 4 * g4);
+        const f32x4v be = *reinterpret_cast<const f32x4v*>(vec + 64 + 16 * rt + 4 * g4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          rr[rt][i] = be[i] * bf16_float(v[4 * rt + i]) - a1[i] * ks_[rt][i];
+          bad |= !finite(rr[rt][i]);
+        }
+      }
+      const uint64_t bad_rows = (uint64_t)__builtin_bit_cast(uint32_t, vec[259]) << 32 | __builtin_bit_cast(uint32_t, vec[258]);
+      uint64_t bad_col = bad_rows;
+      if (__any(bad)) {
+        uint64_t mine = 0;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!finite(rr[rt][i])) {
+              mine |= (uint64_t)1 << (16 * rt + 4 * g4 + i);
+              rr[rt][i] = 0.0f;
+            }
+        mine |= __shfl_xor(mine, 16);
+        mine |= __shfl_xor(mine, 32);
+        bad_col |= mine;
+      }
+      if (g4 == 0) lds.bad[pair][buf][c16] = bad_col;
+      if (c + 1 < chunks) fetch_v(c + 1);
+      bf8 rh[2], rl[2];
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        rh[ks] = high(rr[2 * ks], rr[2 * ks + 1]);
+        rl[ks] = low(rr[2 * ks], rr[2 * ks + 1], rh[ks]);
+      }
+      f32x4v u[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        u[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks <= rt >> 1; ++ks) {
+          const bf8 th = lds.t[buf][fragment_of(rt, ks)][lane], tl = lds.t[buf][kFragments + fragment_of(rt, ks)][lane];
+          u[rt] = mma(th, rh[ks], u[rt]);
+          u[rt] = mma(th, rl[ks], u[rt]);
+          u[rt] = mma(tl, rh[ks], u[rt]);
+        }
+      }
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) lds.u[pair][buf][ks][lane] = high(u[2 * ks], u[2 * ks + 1]);
+      if (dst >= 0 || c + 1 < chunks) {
+        const float grown = vec[256];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const f32x4v a3 = *reinterpret_cast<const f32x4v*>(vec + 192 + 16 * rt + 4 * g4);
+          u[rt] *= a3;
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) st[i] *= grown;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const bf8 uh = high(u[2 * ks], u[2 * ks + 1]), ul = low(u[2 * ks], u[2 * ks + 1], uh);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            // K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows of S's tile i are
+            const int row = 32 * ks + 4 * g4 + (c16 >> 2), piece = 4 * (i >> 1) + (c16 & 3);
+            const i16x4 k0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds.k[buf] + piece_at<DK>(row, piece) + (i & 1) * 8));
+            const i16x4 k1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds.k[buf] + piece_at<DK>(row + 16, piece) + (i & 1) * 8));
+            const bf8 kt = __builtin_bit_cast(bf8, __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7));
+            st[i] = mma(kt, uh, st[i]);
+            st[i] = mma(kt, ul, st[i]);
+          }
+        }
+        if (__any(bad_col != 0)) {
+#pragma unroll
+          for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
+        }
+      }
+      // the second wave reads these after the vectors' buffer is on its way to being filled anew
+      if (pair == 0) lds.a2[buf][lane] = vec[128 + lane];
+    }
+    if (second && c > 0 && a.q) {
+      const int was = buf ^ 1;
+      f32x4v o[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) o[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const bf8 sh = lds.s[pair][was][ks][lane];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) o[rt] = mma(rows_operand<DK>(lds.q[was], rt, ks), sh, o[rt]);
+      }
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) o[rt] *= *reinterpret_cast<const f32x4v*>(lds.a2[was] + 16 * rt + 4 * g4);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        const bf8 uh = lds.u[pair][was][ks][lane];
+#pragma unroll
+        for (int rt = 2 * ks; rt < 4; ++rt) o[rt] = mma(lds.p[was][fragment_of(rt, ks)][lane], uh, o[rt]);
+      }
+      const uint64_t bad_col = lds.bad[pair][was][c16];
+      const bool any = __any(bad_col != 0);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int in = 16 * (i >> 2) + 4 * g4 + (i & 3), token = (c - 1) * kChunk + in;
+        if (token >= r.n) continue;
+        float x = o[i >> 2][i & 3];
+        if (any && ((ancestors(s, r.start + (c - 1) * kChunk, in) | (uint64_t)1 << in) & bad_col)) x = NAN;
+        const int row = row_of(s, r.start + token);
+        if (row >= 0) a.out[row * a.ldo + h * a.dv + col] = (uint16_t)bf16_pair(x, x);
+      }
+    }
+    wait_vm_all();
+    lds_barrier();
+  }
+  if (!second && dst >= 0) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      f32x4v* p = reinterpret_cast<f32x4v*>(a.state + dst * a.slot_stride + state_at + 32 * ks);
+      p[0] = st[2 * ks];
+      p[1] = st[2 * ks + 1];
+    }
+  }
+}
+
+uint64_t delta_chunk_workspace_bytes(int32_t T, int32_t count, int32_t v_heads) {
+  return kZeroBytes + (uint64_t)most_pieces(T, count, kChunk) * v_heads * kTermsBytes;
+}
+
+template <int DK>
+static hipError_t chunk_launches(const w12_delta_args& a, const w12_sequences& s, char* ws, hipStream_t stream) {
+  const dim3 terms((unsigned)most_pieces(s.T, s.count, kChunk), (unsigned)a.v_heads);
+  k_delta_terms<DK><<<terms, kChunkThreads, 0, stream>>>(a, s, ws);
+  const unsigned scans = (unsigned)((int64_t)s.count * a.v_heads * (a.dv / kScanColumns));
+  k_delta_scan<DK><<<scans, kChunkThreads, 0, stream>>>(a, s, ws);
+  return hipGetLastError();
+}
+
+hipError_t launch_delta_chunks(const w12_delta_args& a, const w12_sequences& s, void* ws, hipStream_t stream) {
+  return a.dk == 64 ? chunk_launches<64>(a, s, static_cast<char*>(ws), stream) : chunk_launches<128>(a, s, static_cast<char*>(ws), stream);
+}
+
+}  // namespace w12

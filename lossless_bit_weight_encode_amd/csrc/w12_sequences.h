@@ -37,7 +37,7 @@ __device__ __forceinline__ int slot_of(const w12_sequences& s, const int32_t* wh
   return (uint32_t)i < (uint32_t)s.slots ? i : -1;
 }
 
-// Node i's ancestors in its tree or, without one, every token before it.
+// Of up to 64 tokens from `start` on, those before token i: all of them, or in a tree its ancestors.
 __device__ __forceinline__ uint64_t ancestors(const w12_sequences& s, int start, int i) {
   const uint64_t below = ((uint64_t)1 << i) - 1;
   return s.tree_mask ? s.tree_mask[(int64_t)(start + i) * s.ld_mask] & below : below;
