@@ -17,17 +17,22 @@ __host__ __device__ constexpr int block_of(int r, int s) { return r * (r + 1) / 
 // The workspace starts with a row of zeros, in place of tokens that are not there.
 constexpr int kZeroBytes = 256;
 
-// T = (I + A)^-1 as two BF16 matrices, P as one (each fragment 16 bytes a lane), then FP32 vectors over the rows: beta e^G / |k|, beta,
-// scale e^G / |q|, e^(G_last - G) / |k|, and behind them e^G_last and (2 words further) a bit for each row that is no number.
-constexpr int kTermsBytes = (3 * kFragments + 2) * 1024;
+// T = (I + A)^-1 as two BF16 matrices (each fragment 16 bytes a lane) and 256 words: beta e^G / |k|, beta and e^(G_last - G) / |k| of
+// the rows, e^G_last, and a bit for each row that is no number; then P as one matrix, and scale e^G / |q|.
+constexpr int kFirstPages = 2 * kFragments + 1, kSecondPages = kFragments + 1;      // of 1 KB
+constexpr int kTermsBytes = (kFirstPages + kSecondPages) * 1024;
 struct Terms {
   char* at;
   typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
   __device__ Terms(char* ws, int64_t i) : at(ws + i * kTermsBytes) {}
   __device__ bf8* t_high(int f) const { return reinterpret_cast<bf8*>(at + f * 1024); }
   __device__ bf8* t_low(int f) const { return t_high(kFragments + f); }
-  __device__ bf8* p(int f) const { return t_high(2 * kFragments + f); }
-  __device__ float* vectors() const { return reinterpret_cast<float*>(at + 3 * kFragments * 1024); }
+  __device__ float* rows() const { return reinterpret_cast<float*>(at + 2 * kFragments * 1024); }
+  __device__ char* second() const { return at + kFirstPages * 1024; }
+  __device__ bf8* p(int f) const { return reinterpret_cast<bf8*>(second() + f * 1024); }
+  __device__ float* out_rows() const { return reinterpret_cast<float*>(second() + kFragments * 1024); }
 };
+// Words of rows().
+constexpr int kStrength = 0, kBeta = 64, kLeft = 128, kGrown = 192, kBad = 194;
 
 }  // namespace w12

@@ -169,16 +169,15 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_terms(w12_delta_args a,
   const double last = total[kChunk - 1];
   if (w == 0) {
     const float grown = expf((float)gsum);
-    float* vec = out.vectors();
-    vec[lane] = beta[lane] * grown * rk[lane];
-    vec[64 + lane] = beta[lane];
-    vec[128 + lane] = grown * rq[lane];
-    vec[192 + lane] = expf((float)(last - gsum)) * rk[lane];
+    float* rows = out.rows();
+    rows[kStrength + lane] = beta[lane] * grown * rk[lane];
+    rows[kBeta + lane] = beta[lane];
+    rows[kLeft + lane] = expf((float)(last - gsum)) * rk[lane];
+    out.out_rows()[lane] = grown * rq[lane];
     if (lane == 0) {
-      vec[256] = expf((float)last);
-      vec[257] = 0.0f;
-      reinterpret_cast<uint32_t*>(vec)[258] = badrow[0];
-      reinterpret_cast<uint32_t*>(vec)[259] = badrow[1];
+      rows[kGrown] = expf((float)last);
+      reinterpret_cast<uint32_t*>(rows)[kBad] = badrow[0];
+      reinterpret_cast<uint32_t*>(rows)[kBad + 1] = badrow[1];
     }
   }
   // block row w of A (rows of tile w against columns of tiles 0 .. w), and of P turned (a lane: a row of P, 4 neighbouring columns)
@@ -258,23 +257,31 @@ __device__ __forceinline__ void to_lds(const void* from, uint32_t at) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                : : "s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(from) : "memory", "m0");
 }
+__device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               : : "s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(off), "s"(base) : "memory", "m0");
+}
 
 constexpr int kPairs = 2;                        // pairs of waves of a work-group, of 16 columns each
 constexpr int kScanColumns = 16 * kPairs;
 
 template <int DK>
 struct ScanLds {
-  char k[2][kChunk * DK * 2], q[2][kChunk * DK * 2];
-  bf8 t[2][2 * kFragments][64], p[2][kFragments][64];
-  float vec[2][512];
+  char k[2][kChunk * DK * 2], q[2][kChunk * DK * 2], v[2][kChunk * kScanColumns * 2];
+  char first[2][kFirstPages * 1024], second[2][kSecondPages * 1024];      // terms
   bf8 s[kPairs][2][DK / 32][64];                 // from a pair's first wave to its second: S before a chunk,
   bf8 u[kPairs][2][2][64];                       // its U,
   uint64_t bad[kPairs][2][16];                   // and by column the tokens that were no numbers
-  float a2[2][kChunk];
 };
 
+__device__ __forceinline__ bf8 turned(const char* at, int further) {
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + further));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // A pair's first wave carries S through the chunks; its second makes the outputs of the chunk before, from what the first left.
-template <int DK>
+template <int DK, bool ROWS>
 __global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args a, w12_sequences s, const char* ws) {
   constexpr int KS = DK / 32, RT = DK / 16;
   __shared__ __attribute__((aligned(16))) ScanLds<DK> lds;
@@ -283,170 +290,192 @@ __global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args 
   const bool second = w & 1;
   // the column blocks of a head read the same rows and terms: neighbours, on one XCD
   const int blocks = a.dv / kScanColumns;
-  const int64_t at = logical_wg(blockIdx.x, gridDim.x);
-  const int cb = (int)(at % blocks), h = (int)(at / blocks % a.v_heads), b = (int)(at / blocks / a.v_heads);
+  const int at = (int)logical_wg(blockIdx.x, gridDim.x);
+  const int cb = at % blocks, h = at / blocks % a.v_heads, b = at / blocks / a.v_heads;
   const int hk = h / (a.v_heads / a.k_heads);
   const Range r = range_of(s, b);
   const int chunks = (r.n + kChunk - 1) / kChunk;
-  const int64_t piece0 = first_piece(r, b, kChunk);
   const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
-  const int col = cb * kScanColumns + pair * 16 + c16;
-  const int64_t state_at = ((int64_t)h * a.dv + col) * DK + 8 * g4;
+  const int col0 = cb * kScanColumns;
+  const int64_t state_at = ((int64_t)h * a.dv + col0 + pair * 16 + c16) * DK + 8 * g4;
   const char* zeros = ws;                        // the first row of the workspace
-  const char* terms = ws + kZeroBytes;
 
   f32x4v st[RT];
-  if (!second) {
+#pragma unroll
+  for (int i = 0; i < RT; ++i) st[i] = f32x4v{0, 0, 0, 0};
+  if (!second && src >= 0) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      f32x4v x = {0, 0, 0, 0}, y = x;
-      if (src >= 0) {
-        const f32x4v* p = reinterpret_cast<const f32x4v*>(a.state + src * a.slot_stride + state_at + 32 * ks);
-        x = p[0];
-        y = p[1];
-      }
-      st[2 * ks] = x;
-      st[2 * ks + 1] = y;
+      const f32x4v* p = reinterpret_cast<const f32x4v*>(a.state + src * a.slot_stride + state_at + 32 * ks);
+      st[2 * ks] = p[0];
+      st[2 * ks + 1] = p[1];
     }
   }
-  // rows of K or Q on their way: 16 bytes a lane, 1024 / (2 DK) rows an instruction of a wave
+  // Rows of K and Q on their way: a lane's places of a chunk, kRows rows an instruction of a wave; of V 16 rows, one instruction a wave.
   constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kEach = kChunk / kRows / 4;
-  auto fetch_rows = [&](const uint16_t* from, int64_t ld, int chunk, const char* to) {
+  const char *kp[kEach], *qp[kEach], *vp;
+  const int vrow = 16 * w + (lane >> 2);
+  auto row_in = [&](int i) { return (w * kEach + i) * kRows + lane / kLanes; };
+  auto piece_in = [&](int i) { return (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes; };
+  auto from = [&](const uint16_t* m, int64_t ld, int row, int64_t at) { return reinterpret_cast<const char*>(m + row * ld + at); };
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int first = (w * kEach + i) * kRows, row_in = first + lane / kLanes, token = chunk * kChunk + row_in;
-      const int row = token < r.n ? row_of(s, r.start + token) : -1;
-      const int piece = (piece_at<DK>(row_in, lane % kLanes) >> 4) % kLanes;      // the piece that belongs in this place
-      const void* p = row >= 0 ? static_cast<const void*>(from + row * ld + hk * DK + piece * 8) : zeros + piece * 16;
-      to_lds(p, lds_off(to) + first * DK * 2);
+  for (int i = 0; i < kEach; ++i) {
+    const int64_t e = hk * DK + piece_in(i) * 8;
+    kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), e);
+    qp[i] = a.q ? from(a.q, a.ldq, ROWS ? 0 : r.start + row_in(i), e) : nullptr;
+  }
+  vp = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow, h * a.dv + col0 + (lane & 3) * 8);
+  const int64_t kstep = kChunk * 2 * a.ldk, qstep = kChunk * 2 * a.ldq, vstep = kChunk * 2 * a.ldv;
+  // `p`: of the chunk that is fetched; with rows, of row 0
+  auto send = [&](const char*& p, int64_t step, int64_t ld, int chunk, int row, const char* to) {
+    const char* x = p;
+    const int token = chunk * kChunk + row;
+    if constexpr (ROWS) {
+      const int in = token < r.n ? row_of(s, r.start + token) : -1;
+      x = in >= 0 ? p + in * (2 * ld) : zeros;
+    } else {
+      if ((chunk + 1) * kChunk > r.n) x = token < r.n ? p : zeros;
+      p += step;
     }
+    to_lds(x, lds_off(to));
   };
-  auto fetch_fragments = [&](const void* from, int count, const void* to) {
-    for (int i = w; i < count; i += 4) to_lds(static_cast<const char*>(from) + i * 1024 + lane * 16, lds_off(to) + i * 1024);
-  };
-  auto terms_of = [&](int chunk) { return Terms(const_cast<char*>(terms), (piece0 + chunk) * a.v_heads + h); };
+  const uint32_t page_at = (uint32_t)(w * 1024 + lane * 16);
+  uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
+  const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
   auto fetch_first = [&](int chunk) {
-    Terms t = terms_of(chunk);
-    fetch_rows(a.k, a.ldk, chunk, lds.k[chunk & 1]);
-    fetch_fragments(t.t_high(0), 2 * kFragments, lds.t[chunk & 1]);
-    fetch_fragments(t.vectors(), 2, lds.vec[chunk & 1]);
+    const int buf = chunk & 1;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) send(kp[i], kstep, a.ldk, chunk, row_in(i), lds.k[buf] + (w * kEach + i) * 1024);
+    send(vp, vstep, a.ldv, chunk, vrow, lds.v[buf] + w * 1024);
+    const uint64_t t = terms + chunk * terms_step;
+#pragma unroll
+    for (int i = 0; i < (kFirstPages + 3) / 4; ++i)
+      if (i * 4 + w < kFirstPages) to_lds(t, page_at + i * 4096, lds_off(lds.first[buf]) + i * 4096 + w * 1024);
   };
   auto fetch_second = [&](int chunk) {
-    if (!a.q) return;
-    fetch_rows(a.q, a.ldq, chunk, lds.q[chunk & 1]);
-    fetch_fragments(terms_of(chunk).p(0), kFragments, lds.p[chunk & 1]);
-  };
-  uint16_t v[16];
-  auto fetch_v = [&](int chunk) {
+    const int buf = chunk & 1;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int token = chunk * kChunk + 16 * (i >> 2) + 4 * g4 + (i & 3);
-      const int row = token < r.n ? row_of(s, r.start + token) : -1;
-      v[i] = row >= 0 ? a.v[row * a.ldv + h * a.dv + col] : (uint16_t)0;
-    }
+    for (int i = 0; i < kEach; ++i) send(qp[i], qstep, a.ldq, chunk, row_in(i), lds.q[buf] + (w * kEach + i) * 1024);
+    const uint64_t t = terms + chunk * terms_step + kFirstPages * 1024;
+#pragma unroll
+    for (int i = 0; i < (kSecondPages + 3) / 4; ++i)
+      if (i * 4 + w < kSecondPages) to_lds(t, page_at + i * 4096, lds_off(lds.second[buf]) + i * 4096 + w * 1024);
   };
-  if (chunks) {
-    fetch_first(0);
-    if (!second) fetch_v(0);
+  if (chunks) fetch_first(0);
+  bf8 sh[KS], sl[KS];
+#pragma unroll
+  for (int ks = 0; ks < KS; ++ks) {
+    sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
+    sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
   }
   wait_vm_all();
   lds_barrier();
   for (int c = 0; c <= chunks; ++c) {
     const int buf = c & 1;
     if (c + 1 < chunks) fetch_first(c + 1);
-    if (c < chunks) fetch_second(c);
+    if (c < chunks && a.q) fetch_second(c);
     if (!second && c < chunks) {
-      const float* vec = lds.vec[buf];
-      bf8 sh[KS], sl[KS];
+      const char* const first = lds.first[buf];
+      const float* const rows = reinterpret_cast<const float*>(first + 2 * kFragments * 1024) + 4 * g4;
+      const bf8* const tf = reinterpret_cast<const bf8*>(first) + lane;
+      bf8 k[KS][4];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
-        sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
-        lds.s[pair][buf][ks][lane] = sh[ks];
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) k[ks][rt] = rows_operand<DK>(lds.k[buf], rt, ks);
+      f32x4v a1[4], be[4];
+      i16x4 v[4];
+      // V turned: a lane's column of 4 neighbouring tokens
+      const char* const vat = lds.v[buf] + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + pair * 32 + (c16 & 3) * 8;
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        a1[rt] = *reinterpret_cast<const f32x4v*>(rows + kStrength + 16 * rt);
+        be[rt] = *reinterpret_cast<const f32x4v*>(rows + kBeta + 16 * rt);
+        v[rt] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vat + rt * 16 * kScanColumns * 2));
       }
-      f32x4v ks_[4];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) ks_[rt] = f32x4v{0, 0, 0, 0};
+      for (int ks = 0; ks < KS; ++ks) lds.s[pair][buf][ks][lane] = sh[ks];
+      f32x4v x[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4v{0, 0, 0, 0};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) {
-          const bf8 k = rows_operand<DK>(lds.k[buf], rt, ks);
-          ks_[rt] = mma(k, sh[ks], ks_[rt]);
-          ks_[rt] = mma(k, sl[ks], ks_[rt]);
+          x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
+          x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
         }
-      bool bad = false;
-      f32x4v rr[4];
+      bf8 t[2 * kFragments];
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const f32x4v a1 = *reinterpret_cast<const f32x4v*>(vec + 16 * rt + 4 * g4);
-        const f32x4v be = *reinterpret_cast<const f32x4v*>(vec + 64 + 16 * rt + 4 * g4);
+      for (int i = 0; i < 2 * kFragments; ++i) t[i] = tf[i * 64];
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          rr[rt][i] = be[i] * bf16_float(v[4 * rt + i]) - a1[i] * ks_[rt][i];
-          bad |= !finite(rr[rt][i]);
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[rt][i] = be[rt][i] * bf16_float((uint16_t)v[rt][i]) - a1[rt][i] * x[rt][i];
+      uint64_t bad_col = reinterpret_cast<const uint64_t*>(first + 2 * kFragments * 1024)[kBad / 2];
+      f32x4v u[4];
+      for (int pass = 0;; ++pass) {
+        bf8 rh[2], rl[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          rh[ks] = high(x[2 * ks], x[2 * ks + 1]);
+          rl[ks] = low(x[2 * ks], x[2 * ks + 1], rh[ks]);
         }
-      }
-      const uint64_t bad_rows = (uint64_t)__builtin_bit_cast(uint32_t, vec[259]) << 32 | __builtin_bit_cast(uint32_t, vec[258]);
-      uint64_t bad_col = bad_rows;
-      if (__any(bad)) {
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int rt = 2 * ks; rt < 4; ++rt) {
+            const int f = fragment_of(rt, ks);
+            u[rt] = mma(t[f], rh[ks], u[rt]);
+            u[rt] = mma(t[f], rl[ks], u[rt]);
+            u[rt] = mma(t[kFragments + f], rh[ks], u[rt]);
+          }
+        // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out
+        // then, as it would reach tokens that do not follow its own, and remembered.
+        if (pass || !__any(!finite(u[3][0]))) break;
         uint64_t mine = 0;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (!finite(rr[rt][i])) {
+            if (!finite(x[rt][i])) {
               mine |= (uint64_t)1 << (16 * rt + 4 * g4 + i);
-              rr[rt][i] = 0.0f;
+              x[rt][i] = 0.0f;
             }
         mine |= __shfl_xor(mine, 16);
         mine |= __shfl_xor(mine, 32);
         bad_col |= mine;
       }
       if (g4 == 0) lds.bad[pair][buf][c16] = bad_col;
-      if (c + 1 < chunks) fetch_v(c + 1);
-      bf8 rh[2], rl[2];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        rh[ks] = high(rr[2 * ks], rr[2 * ks + 1]);
-        rl[ks] = low(rr[2 * ks], rr[2 * ks + 1], rh[ks]);
-      }
-      f32x4v u[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        u[rt] = f32x4v{0, 0, 0, 0};
-#pragma unroll
-        for (int ks = 0; ks <= rt >> 1; ++ks) {
-          const bf8 th = lds.t[buf][fragment_of(rt, ks)][lane], tl = lds.t[buf][kFragments + fragment_of(rt, ks)][lane];
-          u[rt] = mma(th, rh[ks], u[rt]);
-          u[rt] = mma(th, rl[ks], u[rt]);
-          u[rt] = mma(tl, rh[ks], u[rt]);
-        }
-      }
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) lds.u[pair][buf][ks][lane] = high(u[2 * ks], u[2 * ks + 1]);
       if (dst >= 0 || c + 1 < chunks) {
-        const float grown = vec[256];
+        const float grown = rows[kGrown - 4 * g4];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const f32x4v a3 = *reinterpret_cast<const f32x4v*>(vec + 192 + 16 * rt + 4 * g4);
-          u[rt] *= a3;
+        for (int rt = 0; rt < 4; ++rt) u[rt] *= *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
+        bf8 uh[2], ul[2];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          uh[ks] = high(u[2 * ks], u[2 * ks + 1]);
+          ul[ks] = low(u[2 * ks], u[2 * ks + 1], uh[ks]);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) st[i] *= grown;
+        // K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows of S's tile i are
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const bf8 uh = high(u[2 * ks], u[2 * ks + 1]), ul = low(u[2 * ks], u[2 * ks + 1], uh);
+        for (int p = 0; p < KS; ++p) {
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            // K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows of S's tile i are
-            const int row = 32 * ks + 4 * g4 + (c16 >> 2), piece = 4 * (i >> 1) + (c16 & 3);
-            const i16x4 k0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds.k[buf] + piece_at<DK>(row, piece) + (i & 1) * 8));
-            const i16x4 k1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(lds.k[buf] + piece_at<DK>(row + 16, piece) + (i & 1) * 8));
-            const bf8 kt = __builtin_bit_cast(bf8, __builtin_shufflevector(k0, k1, 0, 1, 2, 3, 4, 5, 6, 7));
-            st[i] = mma(kt, uh, st[i]);
-            st[i] = mma(kt, ul, st[i]);
-          }
+          for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bf8 kt = turned(lds.k[buf] + piece_at<DK>(32 * ks + 4 * g4 + (c16 >> 2), 4 * p + (c16 & 3)) + e * 8, 16 * DK * 2);
+              st[2 * p + e] = mma(kt, uh[ks], st[2 * p + e]);
+              st[2 * p + e] = mma(kt, ul[ks], st[2 * p + e]);
+            }
         }
         if (__any(bad_col != 0)) {
 #pragma unroll
@@ -454,42 +483,58 @@ __global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args 
 #pragma unroll
             for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
         }
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
+          sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
+        }
       }
-      // the second wave reads these after the vectors' buffer is on its way to being filled anew
-      if (pair == 0) lds.a2[buf][lane] = vec[128 + lane];
     }
     if (second && c > 0 && a.q) {
+      // out turned: a lane's token (of each 16), 4 neighbouring columns
       const int was = buf ^ 1;
+      const bf8* const pf = reinterpret_cast<const bf8*>(lds.second[was]) + lane;
+      const float* const rows = reinterpret_cast<const float*>(lds.second[was] + kFragments * 1024) + c16;
       f32x4v o[4];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) o[rt] = f32x4v{0, 0, 0, 0};
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const bf8 sh = lds.s[pair][was][ks][lane];
+        const bf8 sw = lds.s[pair][was][ks][lane];
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) o[rt] = mma(rows_operand<DK>(lds.q[was], rt, ks), sh, o[rt]);
+        for (int rt = 0; rt < 4; ++rt) o[rt] = mma(sw, rows_operand<DK>(lds.q[was], rt, ks), o[rt]);
       }
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) o[rt] *= *reinterpret_cast<const f32x4v*>(lds.a2[was] + 16 * rt + 4 * g4);
+      for (int rt = 0; rt < 4; ++rt) o[rt] *= rows[16 * rt];
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        const bf8 uh = lds.u[pair][was][ks][lane];
+        const bf8 uw = lds.u[pair][was][ks][lane];
 #pragma unroll
-        for (int rt = 2 * ks; rt < 4; ++rt) o[rt] = mma(lds.p[was][fragment_of(rt, ks)][lane], uh, o[rt]);
+        for (int rt = 2 * ks; rt < 4; ++rt) o[rt] = mma(uw, pf[fragment_of(rt, ks) * 64], o[rt]);
       }
-      const uint64_t bad_col = lds.bad[pair][was][c16];
-      const bool any = __any(bad_col != 0);
+      const uint64_t* const bad = lds.bad[pair][was];
+      if (__any(bad[c16] != 0)) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int in = 16 * (i >> 2) + 4 * g4 + (i & 3), token = (c - 1) * kChunk + in;
-        if (token >= r.n) continue;
-        float x = o[i >> 2][i & 3];
-        if (any && ((ancestors(s, r.start + (c - 1) * kChunk, in) | (uint64_t)1 << in) & bad_col)) x = NAN;
-        const int row = row_of(s, r.start + token);
-        if (row >= 0) a.out[row * a.ldo + h * a.dv + col] = (uint16_t)bf16_pair(x, x);
+        for (int rt = 0; rt < 4; ++rt) {
+          const int in = 16 * rt + c16;
+          const uint64_t path = (c - 1) * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (path & bad[4 * g4 + i]) o[rt][i] = NAN;
+        }
       }
+      wait_vm_all();      // before the stores, which may take their time
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        const int token = (c - 1) * kChunk + 16 * rt + c16;
+        const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
+        if (row >= 0)
+          *reinterpret_cast<uint2*>(a.out + row * a.ldo + h * a.dv + col0 + pair * 16 + 4 * g4) =
+              make_uint2(bf16_pair(o[rt][0], o[rt][1]), bf16_pair(o[rt][2], o[rt][3]));
+      }
+    } else {
+      wait_vm_all();
     }
-    wait_vm_all();
     lds_barrier();
   }
   if (!second && dst >= 0) {
@@ -511,7 +556,8 @@ static hipError_t chunk_launches(const w12_delta_args& a, const w12_sequences& s
   const dim3 terms((unsigned)most_pieces(s.T, s.count, kChunk), (unsigned)a.v_heads);
   k_delta_terms<DK><<<terms, kChunkThreads, 0, stream>>>(a, s, ws);
   const unsigned scans = (unsigned)((int64_t)s.count * a.v_heads * (a.dv / kScanColumns));
-  k_delta_scan<DK><<<scans, kChunkThreads, 0, stream>>>(a, s, ws);
+  if (s.rows) k_delta_scan<DK, true><<<scans, kChunkThreads, 0, stream>>>(a, s, ws);
+  else k_delta_scan<DK, false><<<scans, kChunkThreads, 0, stream>>>(a, s, ws);
   return hipGetLastError();
 }
 
