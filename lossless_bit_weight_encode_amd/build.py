@@ -42,6 +42,9 @@ COMMON = [
     "-I", os.path.join(ROOT, "include"),
 ]
 
+# Matrix results in ordinary registers: what follows them there is vector arithmetic, and accumulation registers cost a move a value.
+FLAGS = {"w12_delta_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+
 
 def hipcc() -> str:
     h = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -53,7 +56,7 @@ def hipcc() -> str:
 def _compile(src: str, build_dir: str = BUILD, defines: tuple = ()) -> str:
     obj = os.path.join(build_dir, os.path.splitext(src)[0] + ".o")
     lang = ["-x", "hip"] if src.endswith(".cpp") else []
-    cmd = [hipcc(), *COMMON, *defines, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [hipcc(), *COMMON, *FLAGS.get(src, []), *defines, *lang, "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")

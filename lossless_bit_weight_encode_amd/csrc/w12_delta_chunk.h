@@ -17,8 +17,8 @@ __host__ __device__ constexpr int block_of(int r, int s) { return r * (r + 1) / 
 // The workspace starts with a row of zeros, in place of tokens that are not there.
 constexpr int kZeroBytes = 256;
 
-// T = (I + A)^-1 as two BF16 matrices (each fragment 16 bytes a lane) and 256 words: beta e^G / |k|, beta and e^(G_last - G) / |k| of
-// the rows, e^G_last, and a bit for each row that is no number; then P as one matrix, and scale e^G / |q|.
+// T = (I + A)^-1 diag(beta) as two BF16 matrices (each fragment 16 bytes a lane) and 256 words: e^G / |k| and e^(G_last - G) / |k|
+// of the rows, e^G_last, and a bit for each row that is no number; then P as one matrix, and scale e^G / |q|.
 constexpr int kFirstPages = 2 * kFragments + 1, kSecondPages = kFragments + 1;      // of 1 KB
 constexpr int kTermsBytes = (kFirstPages + kSecondPages) * 1024;
 struct Terms {
@@ -33,6 +33,6 @@ struct Terms {
   __device__ float* out_rows() const { return reinterpret_cast<float*>(second() + kFragments * 1024); }
 };
 // Words of rows().
-constexpr int kStrength = 0, kBeta = 64, kLeft = 128, kGrown = 192, kBad = 194;
+constexpr int kTaken = 0, kLeft = 64, kGrown = 128, kBad = 130;
 
 }  // namespace w12

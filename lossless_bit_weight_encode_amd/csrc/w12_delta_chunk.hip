@@ -170,8 +170,7 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_terms(w12_delta_args a,
   if (w == 0) {
     const float grown = expf((float)gsum);
     float* rows = out.rows();
-    rows[kStrength + lane] = beta[lane] * grown * rk[lane];
-    rows[kBeta + lane] = beta[lane];
+    rows[kTaken + lane] = grown * rk[lane];
     rows[kLeft + lane] = expf((float)(last - gsum)) * rk[lane];
     out.out_rows()[lane] = grown * rq[lane];
     if (lane == 0) {
@@ -242,6 +241,10 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_terms(w12_delta_args a,
   for (int ks = 0; ks < 2; ++ks) {
     if (ks > w >> 1) continue;
     const int f = fragment_of(w, ks);
+#pragma unroll
+    for (int t = 2 * ks; t < 2 * ks + 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[t][i] *= beta[16 * t + 4 * g4 + i];
     const bf8 hi = high(x[2 * ks], x[2 * ks + 1]);
     out.t_high(f)[lane] = hi;
     out.t_low(f)[lane] = low(x[2 * ks], x[2 * ks + 1], hi);
@@ -262,16 +265,17 @@ __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at)
                : : "s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(off), "s"(base) : "memory", "m0");
 }
 
-constexpr int kPairs = 2;                        // pairs of waves of a work-group, of 16 columns each
-constexpr int kScanColumns = 16 * kPairs;
+// Waves of a work-group: one for every 16 columns of S, one for the outputs of all of them, the others for the loads (a wave starts
+// one to LDS in 75 cycles or more, a chunk takes 56).
+constexpr int kTiles = 2, kScanColumns = 16 * kTiles, kScanThreads = 512, kLoaders = kScanThreads / 64 - kTiles - 1;
 
 template <int DK>
 struct ScanLds {
-  char k[2][kChunk * DK * 2], q[2][kChunk * DK * 2], v[2][kChunk * kScanColumns * 2];
+  char k[3][kChunk * DK * 2], q[2][kChunk * DK * 2], v[2][kChunk * kScanColumns * 2];
   char first[2][kFirstPages * 1024], second[2][kSecondPages * 1024];      // terms
-  bf8 s[kPairs][2][DK / 32][64];                 // from a pair's first wave to its second: S before a chunk,
-  bf8 u[kPairs][2][2][64];                       // its U,
-  uint64_t bad[kPairs][2][16];                   // and by column the tokens that were no numbers
+  bf8 s[kTiles][2][DK / 32][64];                 // for the outputs: S before a chunk,
+  bf8 u[kTiles][2][2][64];                       // the chunk's U,
+  uint64_t bad[kTiles][2][16];                   // and by column the tokens that were no numbers
 };
 
 __device__ __forceinline__ bf8 turned(const char* at, int further) {
@@ -280,14 +284,21 @@ __device__ __forceinline__ bf8 turned(const char* at, int further) {
   return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// A pair's first wave carries S through the chunks; its second makes the outputs of the chunk before, from what the first left.
+// Asks the scheduler for `n` matrix instructions with `each` vector instructions behind every one: they run beside it, if they stand there.
+template <int N, int EACH>
+__device__ __forceinline__ void beside_matrix() {
+  if constexpr (N > 0) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, EACH, 0);
+    beside_matrix<N - 1, EACH>();
+  }
+}
+
 template <int DK, bool ROWS>
-__global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args a, w12_sequences s, const char* ws) {
+__global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w12_sequences s, const char* ws) {
   constexpr int KS = DK / 32, RT = DK / 16;
   __shared__ __attribute__((aligned(16))) ScanLds<DK> lds;
   const int lane = threadIdx.x & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
-  const int pair = w >> 1;
-  const bool second = w & 1;
   // the column blocks of a head read the same rows and terms: neighbours, on one XCD
   const int blocks = a.dv / kScanColumns;
   const int at = (int)logical_wg(blockIdx.x, gridDim.x);
@@ -295,15 +306,164 @@ __global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args 
   const int hk = h / (a.v_heads / a.k_heads);
   const Range r = range_of(s, b);
   const int chunks = (r.n + kChunk - 1) / kChunk;
-  const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
   const int col0 = cb * kScanColumns;
-  const int64_t state_at = ((int64_t)h * a.dv + col0 + pair * 16 + c16) * DK + 8 * g4;
-  const char* zeros = ws;                        // the first row of the workspace
 
+  if (w > kTiles) {
+    // ---- loads: of K, Q and V a lane's places in a chunk, of the terms whole pages
+    const int me = w - kTiles - 1;
+    constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kCount = kChunk / kRows, kEach = (kCount + kLoaders - 1) / kLoaders;
+    const char* const zeros = ws;                // the first row of the workspace
+    const char *kp[kEach], *qp[kEach], *vp;
+    auto row_in = [&](int i) { return (i * kLoaders + me) * kRows + lane / kLanes; };
+    auto piece_in = [&](int i) { return (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes; };
+    auto from = [&](const uint16_t* m, int64_t ld, int row, int64_t at) { return reinterpret_cast<const char*>(m + row * ld + at); };
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int64_t e = hk * DK + piece_in(i) * 8;
+      kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), e);
+      qp[i] = a.q ? from(a.q, a.ldq, ROWS ? 0 : r.start + row_in(i), e) : nullptr;
+    }
+    const int vrow = 16 * me + (lane >> 2);      // of the first four
+    vp = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow, h * a.dv + col0 + (lane & 3) * 8);
+    const int64_t kstep = kChunk * 2 * a.ldk, qstep = kChunk * 2 * a.ldq, vstep = kChunk * 2 * a.ldv;
+    // `p`: of the chunk that is fetched; with rows, of row 0
+    auto send = [&](const char*& p, int64_t step, int64_t ld, int chunk, int row, const char* to) {
+      const char* x = p;
+      const int token = chunk * kChunk + row;
+      if constexpr (ROWS) {
+        const int in = token < r.n ? row_of(s, r.start + token) : -1;
+        x = in >= 0 ? p + in * (2 * ld) : zeros;
+      } else {
+        if ((chunk + 1) * kChunk > r.n) x = token < r.n ? p : zeros;
+        p += step;
+      }
+      to_lds(x, lds_off(to));
+    };
+    auto fetch_rows = [&](const char** p, int64_t step, int64_t ld, int chunk, const char* to) {
+#pragma unroll
+      for (int i = 0; i < kEach; ++i)
+        if (i * kLoaders + me < kCount) send(p[i], step, ld, chunk, row_in(i), to + (i * kLoaders + me) * 1024);
+    };
+    auto fetch_v = [&](int chunk) {
+      if (me < 4) send(vp, vstep, a.ldv, chunk, vrow, lds.v[chunk & 1] + me * 1024);
+    };
+    const uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
+    const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
+    // pages go round from the other end, so that every wave starts about as many loads
+    auto fetch_pages = [&](uint64_t from, int pages, const char* to) {
+#pragma unroll
+      for (int i = 0; i < (kFirstPages + kLoaders - 1) / kLoaders; ++i) {
+        const int page = i * kLoaders + kLoaders - 1 - me;
+        if (page < pages) to_lds(from, (uint32_t)(page * 1024 + lane * 16), lds_off(to) + page * 1024);
+      }
+    };
+    auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, lds.first[chunk & 1]); };
+    if (chunks) {
+      fetch_rows(kp, kstep, a.ldk, 0, lds.k[0]);
+      fetch_first(0);
+      fetch_v(0);
+    }
+    if (chunks > 1) fetch_rows(kp, kstep, a.ldk, 1, lds.k[1]);
+    wait_vm_all();
+    barrier();
+    int k2 = 2;
+    for (int c = 0; c <= chunks; ++c) {
+      if (c + 1 < chunks) {
+        fetch_first(c + 1);
+        fetch_v(c + 1);
+      }
+      if (c < chunks && a.q) {
+        fetch_rows(qp, qstep, a.ldq, c, lds.q[c & 1]);
+        fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, lds.second[c & 1]);
+      }
+      if (c + 2 < chunks) fetch_rows(kp, kstep, a.ldk, c + 2, lds.k[k2]);
+      k2 = k2 == 2 ? 0 : k2 + 1;
+      wait_vm_all();
+      barrier();
+    }
+    return;
+  }
+
+  if (w == kTiles) {
+    // ---- outputs of the chunk before, turned: a lane's token (of each 16), 4 neighbouring columns
+    barrier();
+    for (int c = 0; c <= chunks; ++c) {
+      if (c > 0 && a.q) {
+        const int was = (c - 1) & 1;
+        const bf8* const pf = reinterpret_cast<const bf8*>(lds.second[was]) + lane;
+        const float* const rows = reinterpret_cast<const float*>(lds.second[was] + kFragments * 1024) + c16;
+        f32x4v o[kTiles][4];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) o[n][rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          bf8 sw[kTiles];
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) sw[n] = lds.s[n][was][ks][lane];
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            const bf8 q = rows_operand<DK>(lds.q[was], rt, ks);
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) o[n][rt] = mma(sw[n], q, o[n][rt]);
+          }
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const float x = rows[16 * rt];
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) o[n][rt] *= x;
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          bf8 uw[kTiles];
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) uw[n] = lds.u[n][was][ks][lane];
+#pragma unroll
+          for (int rt = 2 * ks; rt < 4; ++rt) {
+            const bf8 p = pf[fragment_of(rt, ks) * 64];
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) o[n][rt] = mma(uw[n], p, o[n][rt]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+          const uint64_t* const bad = lds.bad[n][was];
+          if (!__any(bad[c16] != 0)) continue;
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) {
+            const int in = 16 * rt + c16;
+            const uint64_t path = (c - 1) * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (path & bad[4 * g4 + i]) o[n][rt][i] = NAN;
+          }
+        }
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) {
+          const int token = (c - 1) * kChunk + 16 * rt + c16;
+          const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
+          if (row >= 0) {
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n)
+              *reinterpret_cast<uint2*>(a.out + row * a.ldo + h * a.dv + col0 + 16 * n + 4 * g4) =
+                  make_uint2(bf16_pair(o[n][rt][0], o[n][rt][1]), bf16_pair(o[n][rt][2], o[n][rt][3]));
+          }
+        }
+      }
+      lds_barrier();
+    }
+    return;
+  }
+
+  // ---- 16 columns of S through the chunks: what the kernel's time is made of
+  const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
+  const int64_t state_at = ((int64_t)h * a.dv + col0 + w * 16 + c16) * DK + 8 * g4;
   f32x4v st[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) st[i] = f32x4v{0, 0, 0, 0};
-  if (!second && src >= 0) {
+  if (src >= 0) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       const f32x4v* p = reinterpret_cast<const f32x4v*>(a.state + src * a.slot_stride + state_at + 32 * ks);
@@ -311,132 +471,94 @@ __global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args 
       st[2 * ks + 1] = p[1];
     }
   }
-  // Rows of K and Q on their way: a lane's places of a chunk, kRows rows an instruction of a wave; of V 16 rows, one instruction a wave.
-  constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kEach = kChunk / kRows / 4;
-  const char *kp[kEach], *qp[kEach], *vp;
-  const int vrow = 16 * w + (lane >> 2);
-  auto row_in = [&](int i) { return (w * kEach + i) * kRows + lane / kLanes; };
-  auto piece_in = [&](int i) { return (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes; };
-  auto from = [&](const uint16_t* m, int64_t ld, int row, int64_t at) { return reinterpret_cast<const char*>(m + row * ld + at); };
+  bf8 k[KS][4];
+  auto read_k = [&](int buf) {
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int64_t e = hk * DK + piece_in(i) * 8;
-    kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), e);
-    qp[i] = a.q ? from(a.q, a.ldq, ROWS ? 0 : r.start + row_in(i), e) : nullptr;
-  }
-  vp = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow, h * a.dv + col0 + (lane & 3) * 8);
-  const int64_t kstep = kChunk * 2 * a.ldk, qstep = kChunk * 2 * a.ldq, vstep = kChunk * 2 * a.ldv;
-  // `p`: of the chunk that is fetched; with rows, of row 0
-  auto send = [&](const char*& p, int64_t step, int64_t ld, int chunk, int row, const char* to) {
-    const char* x = p;
-    const int token = chunk * kChunk + row;
-    if constexpr (ROWS) {
-      const int in = token < r.n ? row_of(s, r.start + token) : -1;
-      x = in >= 0 ? p + in * (2 * ld) : zeros;
-    } else {
-      if ((chunk + 1) * kChunk > r.n) x = token < r.n ? p : zeros;
-      p += step;
-    }
-    to_lds(x, lds_off(to));
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) k[ks][rt] = rows_operand<DK>(lds.k[buf], rt, ks);
   };
-  const uint32_t page_at = (uint32_t)(w * 1024 + lane * 16);
-  uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
-  const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
-  auto fetch_first = [&](int chunk) {
-    const int buf = chunk & 1;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) send(kp[i], kstep, a.ldk, chunk, row_in(i), lds.k[buf] + (w * kEach + i) * 1024);
-    send(vp, vstep, a.ldv, chunk, vrow, lds.v[buf] + w * 1024);
-    const uint64_t t = terms + chunk * terms_step;
-#pragma unroll
-    for (int i = 0; i < (kFirstPages + 3) / 4; ++i)
-      if (i * 4 + w < kFirstPages) to_lds(t, page_at + i * 4096, lds_off(lds.first[buf]) + i * 4096 + w * 1024);
-  };
-  auto fetch_second = [&](int chunk) {
-    const int buf = chunk & 1;
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) send(qp[i], qstep, a.ldq, chunk, row_in(i), lds.q[buf] + (w * kEach + i) * 1024);
-    const uint64_t t = terms + chunk * terms_step + kFirstPages * 1024;
-#pragma unroll
-    for (int i = 0; i < (kSecondPages + 3) / 4; ++i)
-      if (i * 4 + w < kSecondPages) to_lds(t, page_at + i * 4096, lds_off(lds.second[buf]) + i * 4096 + w * 1024);
-  };
-  if (chunks) fetch_first(0);
-  bf8 sh[KS], sl[KS];
-#pragma unroll
-  for (int ks = 0; ks < KS; ++ks) {
-    sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
-    sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
-  }
-  wait_vm_all();
-  lds_barrier();
+  barrier();
+  __builtin_amdgcn_s_setprio(2);
+  if (chunks) read_k(0);
+  int k0 = 0, k1 = 1;                            // the buffers of this chunk's K, and the next one's
   for (int c = 0; c <= chunks; ++c) {
-    const int buf = c & 1;
-    if (c + 1 < chunks) fetch_first(c + 1);
-    if (c < chunks && a.q) fetch_second(c);
-    if (!second && c < chunks) {
+    if (c < chunks) {
+      const int buf = c & 1;
       const char* const first = lds.first[buf];
       const float* const rows = reinterpret_cast<const float*>(first + 2 * kFragments * 1024) + 4 * g4;
       const bf8* const tf = reinterpret_cast<const bf8*>(first) + lane;
-      bf8 k[KS][4];
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) k[ks][rt] = rows_operand<DK>(lds.k[buf], rt, ks);
-      f32x4v a1[4], be[4];
+      // K S, and beside it the rest of S's split and its decay.  What a step reads from LDS is read a step ahead.
+      f32x4v taken[4];
       i16x4 v[4];
+      bf8 t[2 * kFragments], sh[KS], sl[KS];
       // V turned: a lane's column of 4 neighbouring tokens
-      const char* const vat = lds.v[buf] + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + pair * 32 + (c16 & 3) * 8;
+      const char* const vat = lds.v[buf] + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + w * 32 + (c16 & 3) * 8;
+      const float grown = rows[kGrown - 4 * g4];
+      uint64_t bad_col = reinterpret_cast<const uint64_t*>(first + 2 * kFragments * 1024)[kBad / 2];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) {
-        a1[rt] = *reinterpret_cast<const f32x4v*>(rows + kStrength + 16 * rt);
-        be[rt] = *reinterpret_cast<const f32x4v*>(rows + kBeta + 16 * rt);
+        taken[rt] = *reinterpret_cast<const f32x4v*>(rows + kTaken + 16 * rt);
         v[rt] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vat + rt * 16 * kScanColumns * 2));
       }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) lds.s[pair][buf][ks][lane] = sh[ks];
       f32x4v x[4];
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4v{0, 0, 0, 0};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+      for (int ks = 0; ks < KS; ++ks) {
+        sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
+        sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
+        lds.s[w][buf][ks][lane] = sh[ks];
+        st[2 * ks] *= grown;
+        st[2 * ks + 1] *= grown;
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
-          x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
-        }
-      bf8 t[2 * kFragments];
+        for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x002, 24, 0);
+      beside_matrix<8 * KS, 4>();
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int i = 0; i < 2 * kFragments; ++i) t[i] = tf[i * 64];
-      __builtin_amdgcn_sched_barrier(0);
+      // R = V - e^G K S / |k|
 #pragma unroll
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[rt][i] = be[rt][i] * bf16_float((uint16_t)v[rt][i]) - a1[rt][i] * x[rt][i];
-      uint64_t bad_col = reinterpret_cast<const uint64_t*>(first + 2 * kFragments * 1024)[kBad / 2];
+        for (int i = 0; i < 4; ++i) x[rt][i] = __builtin_fmaf(-taken[rt][i], x[rt][i], bf16_float((uint16_t)v[rt][i]));
+      __builtin_amdgcn_sched_barrier(0);
+      // K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows of S's tile i are
+      bf8 kt[RT][2];
+      f32x4v left[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) left[rt] = *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          kt[i][ks] = turned(lds.k[k0] + piece_at<DK>(32 * ks + 4 * g4 + (c16 >> 2), 4 * (i >> 1) + (c16 & 3)) + (i & 1) * 8, 16 * DK * 2);
       f32x4v u[4];
-      for (int pass = 0;; ++pass) {
+      auto solve = [&] {
         bf8 rh[2], rl[2];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           rh[ks] = high(x[2 * ks], x[2 * ks + 1]);
           rl[ks] = low(x[2 * ks], x[2 * ks + 1], rh[ks]);
         }
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
-#pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int rt = 2 * ks; rt < 4; ++rt) {
-            const int f = fragment_of(rt, ks);
-            u[rt] = mma(t[f], rh[ks], u[rt]);
-            u[rt] = mma(t[f], rl[ks], u[rt]);
-            u[rt] = mma(t[kFragments + f], rh[ks], u[rt]);
-          }
-        // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out
-        // then, as it would reach tokens that do not follow its own, and remembered.
-        if (pass || !__any(!finite(u[3][0]))) break;
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int rt = 2 * ks; rt < 4; ++rt)
+              u[rt] = mma(t[fragment_of(rt, ks) + (part == 2 ? kFragments : 0)], part == 1 ? rl[ks] : rh[ks], u[rt]);
+      };
+      solve();
+      // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out
+      // then, as it would reach tokens that do not follow its own, and remembered.
+      if (__any(!finite(u[3][0]))) {
         uint64_t mine = 0;
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt)
@@ -449,95 +571,39 @@ __global__ __launch_bounds__(kChunkThreads, 1) void k_delta_scan(w12_delta_args 
         mine |= __shfl_xor(mine, 16);
         mine |= __shfl_xor(mine, 32);
         bad_col |= mine;
+        solve();
       }
-      if (g4 == 0) lds.bad[pair][buf][c16] = bad_col;
+      if (g4 == 0) lds.bad[w][buf][c16] = bad_col;
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) lds.u[pair][buf][ks][lane] = high(u[2 * ks], u[2 * ks + 1]);
+      for (int ks = 0; ks < 2; ++ks) lds.u[w][buf][ks][lane] = high(u[2 * ks], u[2 * ks + 1]);
       if (dst >= 0 || c + 1 < chunks) {
-        const float grown = rows[kGrown - 4 * g4];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) u[rt] *= *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
-        bf8 uh[2], ul[2];
+        // S, half of the tokens at a time: the other half's split runs beside
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          uh[ks] = high(u[2 * ks], u[2 * ks + 1]);
-          ul[ks] = low(u[2 * ks], u[2 * ks + 1], uh[ks]);
+          u[2 * ks] *= left[2 * ks];
+          u[2 * ks + 1] *= left[2 * ks + 1];
+          const bf8 uh = high(u[2 * ks], u[2 * ks + 1]), ul = low(u[2 * ks], u[2 * ks + 1], uh);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) st[i] = mma(kt[i][ks], uh, st[i]);
+#pragma unroll
+          for (int i = 0; i < RT; ++i) st[i] = mma(kt[i][ks], ul, st[i]);
         }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) st[i] *= grown;
-        // K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows of S's tile i are
-#pragma unroll
-        for (int p = 0; p < KS; ++p) {
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bf8 kt = turned(lds.k[buf] + piece_at<DK>(32 * ks + 4 * g4 + (c16 >> 2), 4 * p + (c16 & 3)) + e * 8, 16 * DK * 2);
-              st[2 * p + e] = mma(kt, uh[ks], st[2 * p + e]);
-              st[2 * p + e] = mma(kt, ul[ks], st[2 * p + e]);
-            }
-        }
+        __builtin_amdgcn_sched_group_barrier(0x002, 32, 0);
+        beside_matrix<2 * RT, 2>();
         if (__any(bad_col != 0)) {
 #pragma unroll
           for (int i = 0; i < RT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
         }
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
-          sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
-        }
       }
-    }
-    if (second && c > 0 && a.q) {
-      // out turned: a lane's token (of each 16), 4 neighbouring columns
-      const int was = buf ^ 1;
-      const bf8* const pf = reinterpret_cast<const bf8*>(lds.second[was]) + lane;
-      const float* const rows = reinterpret_cast<const float*>(lds.second[was] + kFragments * 1024) + c16;
-      f32x4v o[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) o[rt] = f32x4v{0, 0, 0, 0};
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const bf8 sw = lds.s[pair][was][ks][lane];
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) o[rt] = mma(sw, rows_operand<DK>(lds.q[was], rt, ks), o[rt]);
-      }
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) o[rt] *= rows[16 * rt];
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        const bf8 uw = lds.u[pair][was][ks][lane];
-#pragma unroll
-        for (int rt = 2 * ks; rt < 4; ++rt) o[rt] = mma(uw, pf[fragment_of(rt, ks) * 64], o[rt]);
-      }
-      const uint64_t* const bad = lds.bad[pair][was];
-      if (__any(bad[c16] != 0)) {
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const int in = 16 * rt + c16;
-          const uint64_t path = (c - 1) * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (path & bad[4 * g4 + i]) o[rt][i] = NAN;
-        }
-      }
-      wait_vm_all();      // before the stores, which may take their time
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        const int token = (c - 1) * kChunk + 16 * rt + c16;
-        const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
-        if (row >= 0)
-          *reinterpret_cast<uint2*>(a.out + row * a.ldo + h * a.dv + col0 + pair * 16 + 4 * g4) =
-              make_uint2(bf16_pair(o[rt][0], o[rt][1]), bf16_pair(o[rt][2], o[rt][3]));
-      }
-    } else {
-      wait_vm_all();
+      read_k(k1);      // also behind the last chunk: its registers are then free from their use on, whichever way this went
     }
     lds_barrier();
+    k0 = k1;
+    k1 = k1 == 2 ? 0 : k1 + 1;
   }
-  if (!second && dst >= 0) {
+  if (dst >= 0) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       f32x4v* p = reinterpret_cast<f32x4v*>(a.state + dst * a.slot_stride + state_at + 32 * ks);
@@ -556,8 +622,8 @@ static hipError_t chunk_launches(const w12_delta_args& a, const w12_sequences& s
   const dim3 terms((unsigned)most_pieces(s.T, s.count, kChunk), (unsigned)a.v_heads);
   k_delta_terms<DK><<<terms, kChunkThreads, 0, stream>>>(a, s, ws);
   const unsigned scans = (unsigned)((int64_t)s.count * a.v_heads * (a.dv / kScanColumns));
-  if (s.rows) k_delta_scan<DK, true><<<scans, kChunkThreads, 0, stream>>>(a, s, ws);
-  else k_delta_scan<DK, false><<<scans, kChunkThreads, 0, stream>>>(a, s, ws);
+  if (s.rows) k_delta_scan<DK, true><<<scans, kScanThreads, 0, stream>>>(a, s, ws);
+  else k_delta_scan<DK, false><<<scans, kScanThreads, 0, stream>>>(a, s, ws);
   return hipGetLastError();
 }
 
