@@ -74,16 +74,39 @@ __device__ __forceinline__ bf8 rows_operand(const char* m, int rt, int ks) {
 
 // ------------------------------------------------------------------------------------------- terms
 
+// The sum of a wave's values up to each lane's.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double lanes_before(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_up(double v) {
+  v += lanes_before<0x111, 0xF>(v);      // 1, 2, 4 and 8 lanes down, in rows of 16
+  v += lanes_before<0x112, 0xF>(v);
+  v += lanes_before<0x114, 0xF>(v);
+  v += lanes_before<0x118, 0xF>(v);
+  v += lanes_before<0x142, 0xA>(v);      // the last of the row below, into rows 1 and 3
+  v += lanes_before<0x143, 0xC>(v);      // and of the lower half, into the upper
+  return v;
+}
+
 template <int DK>
-__global__ __launch_bounds__(kChunkThreads) void k_delta_terms(w12_delta_args a, w12_sequences s, char* ws) {
-  __shared__ __attribute__((aligned(16))) char km[kChunk * DK * 2], qm[kChunk * DK * 2];
+__global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args a, w12_sequences s, char* ws) {
+  constexpr int KS = DK / 32;
+  // keys, and once they are used the inverses of A's diagonal blocks
+  union Shared {
+    char k[kChunk * DK * 2];
+    struct {
+      f32x4v d[4][64];                           // a lane's column, rows 4 g .. + 3
+      float turn[4][16][20];
+    } inverse;
+  };
+  __shared__ __attribute__((aligned(16))) Shared lds;
   __shared__ f32x4v ablk[10][64];                // A's blocks (r, s), r >= s: a lane's column, rows 4 g .. + 3
-  __shared__ f32x4v dblk[4][64];                 // inverses of the diagonal blocks, the same
-  __shared__ float turn[4][16][20];
-  __shared__ double total[kChunk];
-  __shared__ float rk[kChunk], rq[kChunk], beta[kChunk];
+  __shared__ __attribute__((aligned(16))) float rk[kChunk], rq[kChunk], beta[kChunk], gh[kChunk], gl[kChunk];
   __shared__ uint64_t anc[kChunk];
-  __shared__ uint32_t badrow[2];
   __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
   const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
@@ -93,162 +116,174 @@ __global__ __launch_bounds__(kChunkThreads) void k_delta_terms(w12_delta_args a,
   if (!find_piece(s, blockIdx.x, kChunk, found, b, r, chunk)) return;
   const int first = chunk * kChunk, m = min(kChunk, r.n - first);
   if (m <= 0) return;
-  if (tid < 2) badrow[tid] = 0;
-  // rows of K and Q, four threads a row; the sums of their squares
-  {
-    const int row_in = tid >> 2, quarter = tid & 3;
-    const int row = row_in < m ? row_of(s, r.start + first + row_in) : -1;
-    constexpr int N = DK / 32;                   // 16-byte pieces of a quarter
-    float kk = 0.0f, qq = 0.0f;
+  auto row_at = [&](int i) { return i < m ? row_of(s, r.start + first + i) : -1; };
+  auto operand = [&](const uint16_t* p, int64_t ld, int row, bf8 x[KS]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = i * 4 + quarter;
-      uint4 ku = make_uint4(0, 0, 0, 0), qu = ku;
-      if (row >= 0) {
-        ku = *reinterpret_cast<const uint4*>(a.k + row * a.ldk + hk * DK + p * 8);
-        if (a.q) qu = *reinterpret_cast<const uint4*>(a.q + row * a.ldq + hk * DK + p * 8);
-      }
-      float v[8];
-      unpack_bf16x8(ku, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) kk += v[e] * v[e];
-      unpack_bf16x8(qu, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) qq += v[e] * v[e];
-      *reinterpret_cast<uint4*>(km + piece_at<DK>(row_in, p)) = ku;
-      *reinterpret_cast<uint4*>(qm + piece_at<DK>(row_in, p)) = qu;
+    for (int ks = 0; ks < KS; ++ks) {
+      u32x4v u = {0, 0, 0, 0};
+      if (row >= 0) u = *reinterpret_cast<const u32x4v*>(p + row * ld + hk * DK + 32 * ks + 8 * g4);
+      x[ks] = __builtin_bit_cast(bf8, u);
     }
-    kk += __shfl_xor(kk, 1);
-    kk += __shfl_xor(kk, 2);
-    qq += __shfl_xor(qq, 1);
-    qq += __shfl_xor(qq, 2);
-    float ik = 0.0f, iq = 0.0f, gv = 0.0f, bv = 0.0f;
-    if (row >= 0) {
-      ik = a.l2norm ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
-      iq = a.scale * (a.l2norm ? 1.0f / sqrtf(qq + a.eps) : 1.0f);
-      gv = a.g[row * a.ldg + h];
-      bv = a.beta[row * a.ldbeta + h];
-    }
-    // a row whose key, decay or strength is no number is taken out here, and made up for where the results are stored; -inf for a
-    // decay is one: like anything below -1e4 it clears the state
-    const bool bad = !finite(kk) || !finite(ik) || !(gv < INFINITY) || !finite(bv);
-    __syncthreads();
-    if (bad) {
+  };
+  // Tile w of K, the tiles of Q that this wave's fragments are of, and (all waves) decays and strengths of every row.
+  bf8 kt[KS], qt[2][KS];
+  const int krow = row_at(16 * w + c16);
+  operand(a.k, a.ldk, krow, kt);
+  const int q0 = w == 0 ? 0 : w == 1 ? 2 : 3;
+  const int qrow = a.q ? row_at(16 * q0 + c16) : -1, qrow1 = a.q && w == 0 ? row_at(16 + c16) : -1;
+  operand(a.q, a.ldq, qrow, qt[0]);
+  if (w == 0) operand(a.q, a.ldq, qrow1, qt[1]);
+  const int lrow = row_at(lane);
+  float gv = 0.0f, bv = 0.0f;
+  if (lrow >= 0) {
+    gv = a.g[lrow * a.ldg + h];
+    bv = a.beta[lrow * a.ldbeta + h];
+  }
+  const uint64_t path = lane < m ? ancestors(s, r.start + first, lane) : 0;
 #pragma unroll
-      for (int i = 0; i < N; ++i) *reinterpret_cast<uint4*>(km + piece_at<DK>(row_in, i * 4 + quarter)) = make_uint4(0, 0, 0, 0);
-    }
-    if (quarter == 0) {
-      if (bad) atomicOr(&badrow[row_in >> 5], 1u << (row_in & 31));
-      rk[row_in] = bad ? 0.0f : ik;
-      rq[row_in] = iq;
-      beta[row_in] = bad ? 0.0f : bv;
-      total[row_in] = bad ? 0.0 : (double)fmaxf(gv, -1e4f);
-      anc[row_in] = row_in < m ? ancestors(s, r.start + first, row_in) : 0;
+  for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<bf8*>(lds.k + piece_at<DK>(16 * w + c16, 4 * ks + g4)) = kt[ks];
+  // squares of the norms: the diagonal of a tile with itself, which lanes of 4 g + i = c16 hold
+  auto square = [&](const bf8 x[KS]) {
+    f32x4v t = {0, 0, 0, 0};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) t = mma(x[ks], x[ks], t);
+    const int i = c16 & 3;
+    return i == 0 ? t[0] : i == 1 ? t[1] : i == 2 ? t[2] : t[3];
+  };
+  const bool diagonal = g4 == c16 >> 2;
+  const float kk = square(kt);
+  const float ik = krow < 0 ? 0.0f : a.l2norm ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
+  if (diagonal) rk[16 * w + c16] = finite(kk) && finite(ik) ? ik : NAN;
+  if (a.q) {
+    const float qq = square(qt[0]);
+    if (diagonal && w < 3) rq[16 * q0 + c16] = qrow < 0 ? 0.0f : a.scale * (a.l2norm ? 1.0f / sqrtf(qq + a.eps) : 1.0f);
+    if (w == 0) {
+      const float qq1 = square(qt[1]);
+      if (diagonal) rq[16 + c16] = qrow1 < 0 ? 0.0f : a.scale * (a.l2norm ? 1.0f / sqrtf(qq1 + a.eps) : 1.0f);
     }
   }
   __syncthreads();
-  // sums of g: of all tokens up to a row's, or down its path; every wave for itself, as all need the last one
-  double gsum = total[lane];
+  // A row whose key, decay or strength is no number is left out here, and made up for where the results are stored.  -inf is a number for
+  // a decay: like anything below -1e4 it clears the state.
+  const float ikl = rk[lane];
+  const bool bad = !finite(ikl) || !(gv < INFINITY) || !finite(bv);
+  const uint64_t bads = __ballot(bad);
+  const double g1 = bad ? 0.0 : (double)fmaxf(gv, -1e4f) * 1.4426950408889634;
+  double gsum;
   if (s.tree_mask) {
-    uint64_t path = anc[lane];
-    while (path) {
-      gsum += total[__builtin_ctzll(path)];
-      path &= path - 1;
-    }
+    if (w == 0) *reinterpret_cast<double*>(&ablk[0][lane]) = g1;
+    __syncthreads();
+    gsum = g1;
+    for (uint64_t p = path; p; p &= p - 1) gsum += *reinterpret_cast<const double*>(&ablk[0][__builtin_ctzll(p)]);
   } else {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const double u = __shfl_up(gsum, o);
-      if (lane >= o) gsum += u;
-    }
+    gsum = sum_up(g1);
   }
-  __syncthreads();
-  if (w == 0) total[lane] = gsum;
-  __syncthreads();
+  const uint64_t gbits = __builtin_bit_cast(uint64_t, gsum);
+  const double last = __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(gbits >> 32), 63) << 32 |
+                                                     (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)gbits, 63));
   Terms out(ws + kZeroBytes, (int64_t)blockIdx.x * a.v_heads + h);
-  const double last = total[kChunk - 1];
+  const float rkl = bad ? 0.0f : ikl;
   if (w == 0) {
-    const float grown = expf((float)gsum);
+    const float hi = (float)gsum;
+    gh[lane] = hi;
+    gl[lane] = (float)(gsum - hi);
+    beta[lane] = bad ? 0.0f : bv;
+    anc[lane] = bad ? 0 : path & ~bads;
+  } else if (w == 1) {
+    const float grown = __builtin_amdgcn_exp2f((float)gsum);
     float* rows = out.rows();
-    rows[kTaken + lane] = grown * rk[lane];
-    rows[kLeft + lane] = expf((float)(last - gsum)) * rk[lane];
-    out.out_rows()[lane] = grown * rq[lane];
+    rows[kTaken + lane] = grown * rkl;
+    rows[kLeft + lane] = __builtin_amdgcn_exp2f((float)(last - gsum)) * rkl;
     if (lane == 0) {
-      rows[kGrown] = expf((float)last);
-      reinterpret_cast<uint32_t*>(rows)[kBad] = badrow[0];
-      reinterpret_cast<uint32_t*>(rows)[kBad + 1] = badrow[1];
+      rows[kGrown] = __builtin_amdgcn_exp2f((float)last);
+      reinterpret_cast<uint64_t*>(rows)[kBad / 2] = bads;
     }
+  } else if (w == 2 && a.q) {
+    out.out_rows()[lane] = __builtin_amdgcn_exp2f((float)gsum) * rq[lane];
   }
-  // block row w of A (rows of tile w against columns of tiles 0 .. w), and of P turned (a lane: a row of P, 4 neighbouring columns)
-  f32x4v pt[4];
+  __syncthreads();
+  // This wave's fragments of P (rt, ks): (0, 0) and (1, 0), (2, 0) and (2, 1), (3, 0), (3, 1), 2 or 3 tiles each; and the same tiles
+  // of A.  A: a lane's column, 4 neighbouring rows; P turned: a lane's row, 4 neighbouring columns.
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    pt[t] = f32x4v{0, 0, 0, 0};
-    if (t > w) continue;
-    f32x4v kk = {0, 0, 0, 0}, kq = kk;
+  for (int j = 0; j < 2; ++j) {
+    const int rt = w == 0 ? j : w == 1 ? 2 : 3, ks0 = w == 1 ? j : w == 3 ? 1 : 0;
+    if (w >= 2 && j) continue;
+    f32x4v pt[2];
 #pragma unroll
-    for (int ks = 0; ks < DK / 32; ++ks) {
-      const bf8 kt = rows_operand<DK>(km, t, ks);
-      kk = mma(rows_operand<DK>(km, w, ks), kt, kk);
-      if (a.q) kq = mma(kt, rows_operand<DK>(qm, w, ks), kq);
+    for (int n = 0; n < 2; ++n) {
+      const int t = 2 * ks0 + n;
+      pt[n] = f32x4v{0, 0, 0, 0};
+      if (t > rt) continue;
+      f32x4v kk = {0, 0, 0, 0}, kq = kk;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const bf8 x = rows_operand<DK>(lds.k, t, ks);
+        kk = mma(rows_operand<DK>(lds.k, rt, ks), x, kk);
+        if (a.q) kq = mma(x, w == 0 && j ? qt[1][ks] : qt[0][ks], kq);
+      }
+      const int col = 16 * t + c16, prow = 16 * rt + c16;
+      const float hc = gh[col], lc = gl[col], rc = rk[col], hp = gh[prow], lp = gl[prow], rp = rq[prow];
+      const uint64_t sees = (anc[prow] | (uint64_t)1 << prow) & ~bads;
+      f32x4v ab;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * rt + 4 * g4 + i, pcol = 16 * t + 4 * g4 + i;
+        const float e = __builtin_amdgcn_exp2f((gh[row] - hc) + (gl[row] - lc));
+        ab[i] = anc[row] >> col & 1 ? beta[row] * rk[row] * rc * e * kk[i] : 0.0f;
+        const float f = __builtin_amdgcn_exp2f((hp - gh[pcol]) + (lp - gl[pcol]));
+        pt[n][i] = sees >> pcol & 1 ? rp * rk[pcol] * f * kq[i] : 0.0f;
+      }
+      ablk[block_of(rt, t)][lane] = ab;
     }
-    f32x4v ab;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = 16 * w + 4 * g4 + i, col = 16 * t + c16;
-      ab[i] = anc[row] >> col & 1 ? beta[row] * rk[row] * rk[col] * expf((float)(total[row] - total[col])) * kk[i] : 0.0f;
-      const int prow = 16 * w + c16, pcol = 16 * t + 4 * g4 + i;
-      const bool sees = (anc[prow] | (uint64_t)1 << prow) >> pcol & 1;
-      pt[t][i] = sees ? rq[prow] * rk[pcol] * expf((float)(total[prow] - total[pcol])) * kq[i] : 0.0f;
-    }
-    ablk[block_of(w, t)][lane] = ab;
+    if (a.q) out.p(fragment_of(rt, ks0))[lane] = high(pt[0], pt[1]);
   }
   __syncthreads();
   // the inverse of diagonal block w: a lane's column by substitution (the four groups of lanes do the same)
   float d[16];
   {
-    const float* blk = reinterpret_cast<const float*>(ablk[block_of(w, w)]);      // [column][4 (row / 4)][row % 4]
+    const f32x4v* const blk = ablk[block_of(w, w)];      // [16 (row / 4) + column], row % 4
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float x = i == c16 ? 1.0f : 0.0f;
+    for (int i = 0; i < 16; ++i) d[i] = i == c16 ? 1.0f : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j) x -= blk[(j + 16 * (i >> 2)) * 4 + (i & 3)] * d[j];
-      d[i] = x;
-    }
+    for (int j = 0; j < 15; ++j)
+#pragma unroll
+      for (int q = j / 4; q < 4; ++q) {
+        const f32x4v x = blk[16 * q + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * q + i > j) d[4 * q + i] -= x[i] * d[j];
+      }
   }
   f32x4v mine;
 #pragma unroll
   for (int i = 0; i < 4; ++i) mine[i] = g4 == 0 ? d[i] : g4 == 1 ? d[4 + i] : g4 == 2 ? d[8 + i] : d[12 + i];
-  dblk[w][lane] = mine;
+  lds.inverse.d[w][lane] = mine;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) turn[w][4 * g4 + i][c16] = mine[i];
+  for (int i = 0; i < 4; ++i) lds.inverse.turn[w][4 * g4 + i][c16] = mine[i];
   __syncthreads();
   // block row w of T, turned: X_w = D_w^T, X_t = -D_t^T sum_{t < u <= w} A_ut^T X_u
   f32x4v x[4];
 #pragma unroll
   for (int t = 3; t >= 0; --t) {
     x[t] = f32x4v{0, 0, 0, 0};
-    if (t == w) x[t] = *reinterpret_cast<const f32x4v*>(&turn[w][c16][4 * g4]);
+    if (t == w) x[t] = *reinterpret_cast<const f32x4v*>(&lds.inverse.turn[w][c16][4 * g4]);
     if (t >= w) continue;
     f32x4v sum = {0, 0, 0, 0};
 #pragma unroll
     for (int u = 3; u > t; --u)
       if (u <= w) sum = mma_block(ablk[block_of(u, t)][lane], x[u], sum);
     const f32x4v none = {0, 0, 0, 0};
-    x[t] = none - mma_block(dblk[t][lane], sum, none);
+    x[t] = none - mma_block(lds.inverse.d[t][lane], sum, none);
   }
 #pragma unroll
   for (int ks = 0; ks < 2; ++ks) {
     if (ks > w >> 1) continue;
     const int f = fragment_of(w, ks);
 #pragma unroll
-    for (int t = 2 * ks; t < 2 * ks + 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[t][i] *= beta[16 * t + 4 * g4 + i];
+    for (int t = 2 * ks; t < 2 * ks + 2; ++t) x[t] *= *reinterpret_cast<const f32x4v*>(beta + 16 * t + 4 * g4);
     const bf8 hi = high(x[2 * ks], x[2 * ks + 1]);
     out.t_high(f)[lane] = hi;
     out.t_low(f)[lane] = low(x[2 * ks], x[2 * ks + 1], hi);
-    if (a.q) out.p(f)[lane] = high(pt[2 * ks], pt[2 * ks + 1]);
   }
 }
 
@@ -301,8 +336,9 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
   const int lane = threadIdx.x & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
   // the column blocks of a head read the same rows and terms: neighbours, on one XCD
   const int blocks = a.dv / kScanColumns;
-  const int at = (int)logical_wg(blockIdx.x, gridDim.x);
-  const int cb = at % blocks, h = at / blocks % a.v_heads, b = at / blocks / a.v_heads;
+  // (and every sequence on all of them: lengths differ)
+  const int of = blocks * a.v_heads, b = blockIdx.x / of, at = (int)logical_wg(blockIdx.x % of, of);
+  const int cb = at % blocks, h = at / blocks;
   const int hk = h / (a.v_heads / a.k_heads);
   const Range r = range_of(s, b);
   const int chunks = (r.n + kChunk - 1) / kChunk;
