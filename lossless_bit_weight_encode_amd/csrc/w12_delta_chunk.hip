@@ -52,17 +52,20 @@ __device__ __forceinline__ bf8 low(f32x4v a, f32x4v b, bf8 hi) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float x = i < 2 ? a[2 * i] : b[2 * i - 4], y = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-    r[i] = bf16_pair(x - bf16_float(h[i]), y - __builtin_bit_cast(float, h[i] & 0xFFFF0000u));
+    float xh;
+    asm("v_lshlrev_b32 %0, 16, %1" : "=v"(xh) : "v"(h[i]));      // written as a shift it becomes a second conversion, and the shift
+    r[i] = bf16_pair(x - xh, y - __builtin_bit_cast(float, h[i] & 0xFFFF0000u));
   }
   return __builtin_bit_cast(bf8, r);
 }
 
-// Rows of keys or queries in LDS: 16-byte pieces, swizzled by row so that a column of pieces (of 16 rows) and 4 neighbouring
-// pieces of 4 neighbouring rows both spread over the banks.
+// Rows of keys or queries in LDS: 16-byte pieces, swizzled by row so that neither the reads of a column of pieces (16 rows; taken
+// as lanes 0-3, 12-15 and 20-27, and their like) nor, with 16 pieces, the turning reads of 4 pieces of 4 rows meet in a bank.
 template <int DK>
 __device__ __forceinline__ int piece_at(int row, int piece) {
   constexpr int P = DK / 8;
-  const int s = P == 16 ? (row & 3) << 2 | (row >> 2 & 3) : (row & 1) << 2 | (row >> 1 & 3);
+  const int q = row >> 2 & 3;
+  const int s = P == 16 ? (row & 3) << 2 | ((q ^ q >> 1) & 1) << 1 | q >> 1 : row >> 1 & 7;
   return (row * P + (piece ^ s)) * 16;
 }
 // A lane's operand of rows 16 rt .. + 15 (row lane % 16) and values 32 ks + 8 (lane / 16) .. + 7.
@@ -304,35 +307,47 @@ __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at)
 // one to LDS in 75 cycles or more, a chunk takes 56).
 constexpr int kTiles = 2, kScanColumns = 16 * kTiles, kScanThreads = 512, kLoaders = kScanThreads / 64 - kTiles - 1;
 
+// What a chunk has in LDS; in one piece what the waves that carry S read, so that a lane's few addresses reach all of it.
+template <int DK>
+struct ChunkLds {
+  char first[kFirstPages * 1024];                // terms
+  bf8 s[kTiles][DK / 32][64];                    // for the outputs: S before the chunk,
+  bf8 u[kTiles][2][64];                          // U,
+  uint64_t bad[kTiles][16];                      // and by column the tokens that were no numbers
+  char v[kChunk * kScanColumns * 2];
+};
 template <int DK>
 struct ScanLds {
-  char k[3][kChunk * DK * 2], q[2][kChunk * DK * 2], v[2][kChunk * kScanColumns * 2];
-  char first[2][kFirstPages * 1024], second[2][kSecondPages * 1024];      // terms
-  bf8 s[kTiles][2][DK / 32][64];                 // for the outputs: S before a chunk,
-  bf8 u[kTiles][2][2][64];                       // the chunk's U,
-  uint64_t bad[kTiles][2][16];                   // and by column the tokens that were no numbers
+  char k[3][kChunk * DK * 2];
+  ChunkLds<DK> chunk[2];
+  char q[2][kChunk * DK * 2], second[2][kSecondPages * 1024];
 };
 
-__device__ __forceinline__ bf8 turned(const char* at, int further) {
-  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)at);
-  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(at + further));
+// 16 bytes of LDS at an address.
+__device__ __forceinline__ u32x4v lds_at(uint32_t at) { return *reinterpret_cast<__attribute__((address_space(3))) const u32x4v*>(at); }
+
+__device__ __forceinline__ bf8 turned(uint32_t at, int further) {
+  const i16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_i16x4*>(at));
+  const i16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_i16x4*>(at + further));
   return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Asks the scheduler for `n` matrix instructions with `each` vector instructions behind every one: they run beside it, if they stand there.
-template <int N, int EACH>
+// Asks the scheduler for N matrix instructions, each with so many vector instructions and reads of LDS behind it: they run beside it, if
+// they stand there (a wave issues in order).
+template <int N, int VECTOR, int READS>
 __device__ __forceinline__ void beside_matrix() {
   if constexpr (N > 0) {
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    __builtin_amdgcn_sched_group_barrier(0x002, EACH, 0);
-    beside_matrix<N - 1, EACH>();
+    if constexpr (READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
+    if constexpr (VECTOR > 0) __builtin_amdgcn_sched_group_barrier(0x002, VECTOR, 0);
+    beside_matrix<N - 1, VECTOR, READS>();
   }
 }
 
 template <int DK, bool ROWS>
 __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w12_sequences s, const char* ws) {
   constexpr int KS = DK / 32, RT = DK / 16;
-  __shared__ __attribute__((aligned(16))) ScanLds<DK> lds;
+  __shared__ __attribute__((aligned(1024))) ScanLds<DK> lds;
   const int lane = threadIdx.x & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
   // the column blocks of a head read the same rows and terms: neighbours, on one XCD
   const int blocks = a.dv / kScanColumns;
@@ -381,7 +396,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         if (i * kLoaders + me < kCount) send(p[i], step, ld, chunk, row_in(i), to + (i * kLoaders + me) * 1024);
     };
     auto fetch_v = [&](int chunk) {
-      if (me < 4) send(vp, vstep, a.ldv, chunk, vrow, lds.v[chunk & 1] + me * 1024);
+      if (me < 4) send(vp, vstep, a.ldv, chunk, vrow, lds.chunk[chunk & 1].v + me * 1024);
     };
     const uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
     const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
@@ -393,7 +408,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         if (page < pages) to_lds(from, (uint32_t)(page * 1024 + lane * 16), lds_off(to) + page * 1024);
       }
     };
-    auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, lds.first[chunk & 1]); };
+    auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, lds.chunk[chunk & 1].first); };
     if (chunks) {
       fetch_rows(kp, kstep, a.ldk, 0, lds.k[0]);
       fetch_first(0);
@@ -437,7 +452,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         for (int ks = 0; ks < KS; ++ks) {
           bf8 sw[kTiles];
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) sw[n] = lds.s[n][was][ks][lane];
+          for (int n = 0; n < kTiles; ++n) sw[n] = lds.chunk[was].s[n][ks][lane];
 #pragma unroll
           for (int rt = 0; rt < 4; ++rt) {
             const bf8 q = rows_operand<DK>(lds.q[was], rt, ks);
@@ -455,7 +470,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         for (int ks = 0; ks < 2; ++ks) {
           bf8 uw[kTiles];
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) uw[n] = lds.u[n][was][ks][lane];
+          for (int n = 0; n < kTiles; ++n) uw[n] = lds.chunk[was].u[n][ks][lane];
 #pragma unroll
           for (int rt = 2 * ks; rt < 4; ++rt) {
             const bf8 p = pf[fragment_of(rt, ks) * 64];
@@ -465,7 +480,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         }
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-          const uint64_t* const bad = lds.bad[n][was];
+          const uint64_t* const bad = lds.chunk[was].bad[n];
           if (!__any(bad[c16] != 0)) continue;
 #pragma unroll
           for (int rt = 0; rt < 4; ++rt) {
@@ -508,137 +523,165 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     }
   }
   bf8 k[KS][4];
+  // A lane's places in the first buffer of K, of the operands of K S and of those of K turned (pieces 4 ks further lie where these bits
+  // differ).  The compiler is not to know that they stay the same: it would keep every address made from them.
+  uint32_t kplace = lds_off(lds.k[0]) + piece_at<DK>(c16, g4);
+  uint32_t tplace = lds_off(lds.k[0]) + piece_at<DK>(4 * g4 + (c16 >> 2), c16 & 3);
   auto read_k = [&](int buf) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) k[ks][rt] = rows_operand<DK>(lds.k[buf], rt, ks);
+      for (int rt = 0; rt < 4; ++rt)
+        k[ks][rt] = __builtin_bit_cast(bf8, lds_at((kplace ^ (ks * 64)) + buf * (kChunk * DK * 2) + rt * 16 * DK * 2));
   };
   barrier();
   __builtin_amdgcn_s_setprio(2);
   if (chunks) read_k(0);
   int k0 = 0, k1 = 1;                            // the buffers of this chunk's K, and the next one's
-  for (int c = 0; c <= chunks; ++c) {
-    if (c < chunks) {
-      const int buf = c & 1;
-      const char* const first = lds.first[buf];
-      const float* const rows = reinterpret_cast<const float*>(first + 2 * kFragments * 1024) + 4 * g4;
-      const bf8* const tf = reinterpret_cast<const bf8*>(first) + lane;
-      // K S, and beside it the rest of S's split and its decay.  What a step reads from LDS is read a step ahead.
-      f32x4v taken[4];
-      i16x4 v[4];
-      bf8 t[2 * kFragments], sh[KS], sl[KS];
-      // V turned: a lane's column of 4 neighbouring tokens
-      const char* const vat = lds.v[buf] + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + w * 32 + (c16 & 3) * 8;
-      const float grown = rows[kGrown - 4 * g4];
-      uint64_t bad_col = reinterpret_cast<const uint64_t*>(first + 2 * kFragments * 1024)[kBad / 2];
+  for (int c = 0; c < chunks; ++c) {
+    asm volatile("" : "+v"(kplace), "+v"(tplace));
+    ChunkLds<DK>& here = lds.chunk[c & 1];
+    const float* const rows = reinterpret_cast<const float*>(here.first + 2 * kFragments * 1024) + 4 * g4;
+    const bf8* const tf = reinterpret_cast<const bf8*>(here.first) + lane;
+    // K S, and beside it the rest of S's split, its decay, and what the next step reads from LDS
+    const float grown = rows[kGrown - 4 * g4];
+    uint64_t bad_col = reinterpret_cast<const uint64_t*>(here.first + 2 * kFragments * 1024)[kBad / 2];
+    __builtin_amdgcn_sched_barrier(0);
+    f32x4v taken[4];
+    i16x4 v[4];
+    bf8 t[2 * kFragments], sh[KS], sl[KS];
+    // V turned: a lane's column of 4 neighbouring tokens
+    const uint32_t vat = lds_off(here.v) + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + w * 32 + (c16 & 3) * 8;
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) {
-        taken[rt] = *reinterpret_cast<const f32x4v*>(rows + kTaken + 16 * rt);
-        v[rt] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(vat + rt * 16 * kScanColumns * 2));
+    for (int rt = 0; rt < 4; ++rt) {
+      taken[rt] = *reinterpret_cast<const f32x4v*>(rows + kTaken + 16 * rt);
+      v[rt] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_i16x4*>(vat + rt * 16 * kScanColumns * 2));
+    }
+    f32x4v x[4];
+#pragma unroll
+    for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
+      sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
+      here.s[w][ks][lane] = sh[ks];
+      st[2 * ks] *= grown;
+      st[2 * ks + 1] *= grown;
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
+      if (ks == KS / 2 - 1) {
+        __builtin_amdgcn_sched_group_barrier(0x002, 24, 0);
+        beside_matrix<4 * KS, 4, 1>();
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2 * kFragments; ++i) t[i] = tf[i * 64];
       }
-      f32x4v x[4];
+    }
+    beside_matrix<4 * KS, 4, 1>();
+    __builtin_amdgcn_sched_barrier(0);
+    // R = V - e^G K S / |k|, U = T R, and beside them K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows
+    // of S's tile i are
+    bf8 kt[RT];
+    auto read_turned = [&](int ks) {
 #pragma unroll
-      for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4v{0, 0, 0, 0};
+      for (int i = 0; i < RT; ++i)
+        kt[i] = turned((tplace ^ ((i >> 1) * 64)) + k0 * (kChunk * DK * 2) + ks * 32 * DK * 2 + (i & 1) * 8, 16 * DK * 2);
+    };
+    f32x4v left[4], u[4];
+    bf8 uh, ul;
+    auto finish = [&](int ks) {
+      u[2 * ks] *= left[2 * ks];
+      u[2 * ks + 1] *= left[2 * ks + 1];
+      uh = high(u[2 * ks], u[2 * ks + 1]);
+      ul = low(u[2 * ks], u[2 * ks + 1], uh);
+    };
+    auto solve = [&] {
+      bf8 rh[2], rl[2];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
-        sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
-        lds.s[w][buf][ks][lane] = sh[ks];
-        st[2 * ks] *= grown;
-        st[2 * ks + 1] *= grown;
+      for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
+      for (int ks = 0; ks < 2; ++ks) {
+        rh[ks] = high(x[2 * ks], x[2 * ks + 1]);
+        rl[ks] = low(x[2 * ks], x[2 * ks + 1], rh[ks]);
       }
-      __builtin_amdgcn_sched_group_barrier(0x002, 24, 0);
-      beside_matrix<8 * KS, 4>();
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int i = 0; i < 2 * kFragments; ++i) t[i] = tf[i * 64];
-      // R = V - e^G K S / |k|
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[rt][i] = __builtin_fmaf(-taken[rt][i], x[rt][i], bf16_float((uint16_t)v[rt][i]));
-      __builtin_amdgcn_sched_barrier(0);
-      // K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows of S's tile i are
-      bf8 kt[RT][2];
-      f32x4v left[4];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) left[rt] = *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          kt[i][ks] = turned(lds.k[k0] + piece_at<DK>(32 * ks + 4 * g4 + (c16 >> 2), 4 * (i >> 1) + (c16 & 3)) + (i & 1) * 8, 16 * DK * 2);
-      f32x4v u[4];
-      auto solve = [&] {
-        bf8 rh[2], rl[2];
+        for (int part = 0; part < 3; ++part)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
+          for (int rt = 2 * ks; rt < 4; ++rt)
+            u[rt] = mma(t[fragment_of(rt, ks) + (part == 2 ? kFragments : 0)], part == 1 ? rl[ks] : rh[ks], u[rt]);
+      here.u[w][0][lane] = high(u[0], u[1]);
+      finish(0);
+    };
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          rh[ks] = high(x[2 * ks], x[2 * ks + 1]);
-          rl[ks] = low(x[2 * ks], x[2 * ks + 1], rh[ks]);
-        }
+    for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
+      for (int i = 0; i < 4; ++i) x[rt][i] = __builtin_fmaf(-taken[rt][i], x[rt][i], bf16_float((uint16_t)v[rt][i]));
 #pragma unroll
-          for (int part = 0; part < 3; ++part)
+    for (int rt = 0; rt < 4; ++rt) left[rt] = *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
+    read_turned(0);
+    solve();
+    __builtin_amdgcn_sched_group_barrier(0x002, 40, 0);
+    beside_matrix<12, 3, 2>();
+    beside_matrix<6, 6, 0>();
+    __builtin_amdgcn_sched_barrier(0);
+    // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out then, as
+    // it would reach tokens that do not follow its own, and remembered.
+    if (__any(!finite(u[3][0]))) {
+      uint64_t mine = 0;
+      int row0 = 4 * g4;
+      asm volatile("" : "+v"(row0));               // else the bits of all rows are made before the loop, and kept
 #pragma unroll
-            for (int rt = 2 * ks; rt < 4; ++rt)
-              u[rt] = mma(t[fragment_of(rt, ks) + (part == 2 ? kFragments : 0)], part == 1 ? rl[ks] : rh[ks], u[rt]);
-      };
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!finite(x[rt][i])) {
+            mine |= (uint64_t)1 << (16 * rt + row0 + i);
+            x[rt][i] = 0.0f;
+          }
+      mine |= __shfl_xor(mine, 16);
+      mine |= __shfl_xor(mine, 32);
+      bad_col |= mine;
       solve();
-      // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out
-      // then, as it would reach tokens that do not follow its own, and remembered.
-      if (__any(!finite(u[3][0]))) {
-        uint64_t mine = 0;
-#pragma unroll
-        for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!finite(x[rt][i])) {
-              mine |= (uint64_t)1 << (16 * rt + 4 * g4 + i);
-              x[rt][i] = 0.0f;
-            }
-        mine |= __shfl_xor(mine, 16);
-        mine |= __shfl_xor(mine, 32);
-        bad_col |= mine;
-        solve();
-      }
-      if (g4 == 0) lds.bad[w][buf][c16] = bad_col;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) lds.u[w][buf][ks][lane] = high(u[2 * ks], u[2 * ks + 1]);
-      if (dst >= 0 || c + 1 < chunks) {
-        // S, half of the tokens at a time: the other half's split runs beside
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          u[2 * ks] *= left[2 * ks];
-          u[2 * ks + 1] *= left[2 * ks + 1];
-          const bf8 uh = high(u[2 * ks], u[2 * ks + 1]), ul = low(u[2 * ks], u[2 * ks + 1], uh);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) st[i] = mma(kt[i][ks], uh, st[i]);
-#pragma unroll
-          for (int i = 0; i < RT; ++i) st[i] = mma(kt[i][ks], ul, st[i]);
-        }
-        __builtin_amdgcn_sched_group_barrier(0x002, 32, 0);
-        beside_matrix<2 * RT, 2>();
-        if (__any(bad_col != 0)) {
-#pragma unroll
-          for (int i = 0; i < RT; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
-        }
-      }
-      read_k(k1);      // also behind the last chunk: its registers are then free from their use on, whichever way this went
     }
-    lds_barrier();
+    if (g4 == 0) here.bad[w][c16] = bad_col;
+    if (dst < 0 && c + 1 == chunks) {              // nobody asks for what S has become
+      here.u[w][1][lane] = high(u[2], u[3]);
+      break;
+    }
+    // S, half of the tokens at a time: the other half's split runs beside, and the reads of the next chunk's K
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
+    here.u[w][1][lane] = high(u[2], u[3]);
+    finish(1);
+    read_turned(1);
+    beside_matrix<2 * RT, 3, 2>();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
+    read_k(k1);
+    beside_matrix<2 * RT, 0, 1>();
+    __builtin_amdgcn_sched_barrier(0);
+    if (__any(bad_col != 0)) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
+    }
     k0 = k1;
     k1 = k1 == 2 ? 0 : k1 + 1;
+    if (c + 1 < chunks) lds_barrier();
   }
+  if (chunks) lds_barrier();                     // of the last chunk,
+  lds_barrier();                                 // and of its outputs
   if (dst >= 0) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
