@@ -303,9 +303,9 @@ __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at)
                : : "s"(__builtin_amdgcn_readfirstlane((int)at)), "v"(off), "s"(base) : "memory", "m0");
 }
 
-// Waves of a work-group: one for every 16 columns of S, one for the outputs of all of them, the others for the loads (a wave starts
-// one to LDS in 75 cycles or more, a chunk takes 56).
-constexpr int kTiles = 2, kScanColumns = 16 * kTiles, kScanThreads = 512, kLoaders = kScanThreads / 64 - kTiles - 1;
+// Waves of a work-group: one for every 16 columns of S, one on each SIMD; one for the outputs of two of those; the others for the
+// loads (a wave starts one to LDS in 75 cycles or more, a chunk takes 44).
+constexpr int kTiles = 4, kScanColumns = 16 * kTiles, kOuts = kTiles / 2, kScanThreads = 512, kLoaders = kScanThreads / 64 - kTiles - kOuts;
 
 // What a chunk has in LDS; in one piece what the waves that carry S read, so that a lane's few addresses reach all of it.
 template <int DK>
@@ -320,7 +320,7 @@ template <int DK>
 struct ScanLds {
   char k[3][kChunk * DK * 2];
   ChunkLds<DK> chunk[2];
-  char q[2][kChunk * DK * 2], second[2][kSecondPages * 1024];
+  char second[2][kSecondPages * 1024];
 };
 
 // 16 bytes of LDS at an address.
@@ -359,24 +359,25 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
   const int chunks = (r.n + kChunk - 1) / kChunk;
   const int col0 = cb * kScanColumns;
 
-  if (w > kTiles) {
-    // ---- loads: of K, Q and V a lane's places in a chunk, of the terms whole pages
-    const int me = w - kTiles - 1;
-    constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kCount = kChunk / kRows, kEach = (kCount + kLoaders - 1) / kLoaders;
+  if (w >= kTiles + kOuts) {
+    // ---- loads: of K and V a lane's places in a chunk, of the terms whole pages
+    const int me = w - kTiles - kOuts;
+    constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kEach = kChunk / kRows / kLoaders;
+    constexpr int kVLanes = kScanColumns / 8, kVRows = 64 / kVLanes, kVEach = kChunk / kVRows / kLoaders;
     const char* const zeros = ws;                // the first row of the workspace
-    const char *kp[kEach], *qp[kEach], *vp;
-    auto row_in = [&](int i) { return (i * kLoaders + me) * kRows + lane / kLanes; };
-    auto piece_in = [&](int i) { return (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes; };
+    const char *kp[kEach], *vp[kVEach];
+    auto row_in = [&](int i) { return (me * kEach + i) * kRows + lane / kLanes; };
+    auto vrow_in = [&](int i) { return (me * kVEach + i) * kVRows + lane / kVLanes; };
     auto from = [&](const uint16_t* m, int64_t ld, int row, int64_t at) { return reinterpret_cast<const char*>(m + row * ld + at); };
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-      const int64_t e = hk * DK + piece_in(i) * 8;
-      kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), e);
-      qp[i] = a.q ? from(a.q, a.ldq, ROWS ? 0 : r.start + row_in(i), e) : nullptr;
+      const int piece = (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes;      // that belongs in this place
+      kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), hk * DK + piece * 8);
     }
-    const int vrow = 16 * me + (lane >> 2);      // of the first four
-    vp = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow, h * a.dv + col0 + (lane & 3) * 8);
-    const int64_t kstep = kChunk * 2 * a.ldk, qstep = kChunk * 2 * a.ldq, vstep = kChunk * 2 * a.ldv;
+#pragma unroll
+    for (int i = 0; i < kVEach; ++i)
+      vp[i] = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow_in(i), h * a.dv + col0 + lane % kVLanes * 8);
+    const int64_t kstep = kChunk * 2 * a.ldk, vstep = kChunk * 2 * a.ldv;
     // `p`: of the chunk that is fetched; with rows, of row 0
     auto send = [&](const char*& p, int64_t step, int64_t ld, int chunk, int row, const char* to) {
       const char* x = p;
@@ -390,31 +391,30 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
       }
       to_lds(x, lds_off(to));
     };
-    auto fetch_rows = [&](const char** p, int64_t step, int64_t ld, int chunk, const char* to) {
+    auto fetch_k = [&](int chunk, int buf) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i)
-        if (i * kLoaders + me < kCount) send(p[i], step, ld, chunk, row_in(i), to + (i * kLoaders + me) * 1024);
+      for (int i = 0; i < kEach; ++i) send(kp[i], kstep, a.ldk, chunk, row_in(i), lds.k[buf] + (me * kEach + i) * 1024);
     };
     auto fetch_v = [&](int chunk) {
-      if (me < 4) send(vp, vstep, a.ldv, chunk, vrow, lds.chunk[chunk & 1].v + me * 1024);
+#pragma unroll
+      for (int i = 0; i < kVEach; ++i) send(vp[i], vstep, a.ldv, chunk, vrow_in(i), lds.chunk[chunk & 1].v + (me * kVEach + i) * 1024);
     };
     const uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
     const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
-    // pages go round from the other end, so that every wave starts about as many loads
-    auto fetch_pages = [&](uint64_t from, int pages, const char* to) {
+    auto fetch_pages = [&](uint64_t from, int pages, int mine, const char* to) {
 #pragma unroll
       for (int i = 0; i < (kFirstPages + kLoaders - 1) / kLoaders; ++i) {
-        const int page = i * kLoaders + kLoaders - 1 - me;
+        const int page = i * kLoaders + mine;
         if (page < pages) to_lds(from, (uint32_t)(page * 1024 + lane * 16), lds_off(to) + page * 1024);
       }
     };
-    auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, lds.chunk[chunk & 1].first); };
+    auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, me, lds.chunk[chunk & 1].first); };
     if (chunks) {
-      fetch_rows(kp, kstep, a.ldk, 0, lds.k[0]);
+      fetch_k(0, 0);
       fetch_first(0);
       fetch_v(0);
     }
-    if (chunks > 1) fetch_rows(kp, kstep, a.ldk, 1, lds.k[1]);
+    if (chunks > 1) fetch_k(1, 1);
     wait_vm_all();
     barrier();
     int k2 = 2;
@@ -423,11 +423,8 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         fetch_first(c + 1);
         fetch_v(c + 1);
       }
-      if (c < chunks && a.q) {
-        fetch_rows(qp, qstep, a.ldq, c, lds.q[c & 1]);
-        fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, lds.second[c & 1]);
-      }
-      if (c + 2 < chunks) fetch_rows(kp, kstep, a.ldk, c + 2, lds.k[k2]);
+      if (c < chunks && a.q) fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, kLoaders - 1 - me, lds.second[c & 1]);
+      if (c + 2 < chunks) fetch_k(c + 2, k2);
       k2 = k2 == 2 ? 0 : k2 + 1;
       wait_vm_all();
       barrier();
@@ -435,71 +432,97 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     return;
   }
 
-  if (w == kTiles) {
-    // ---- outputs of the chunk before, turned: a lane's token (of each 16), 4 neighbouring columns
+  if (w >= kTiles) {
+    // ---- outputs of the chunk before, half of its tokens a wave, turned: a lane's token (of each 16), and of every two tiles 8
+    // neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
+    const int half = w - kTiles;
+    bf8 q[KS][2];
+    // (of tokens that are not there any row will do: a token's query makes its own output only)
+    auto read_q = [&](int chunk) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int token = min(chunk * kChunk + 32 * half + 16 * j + c16, r.n - 1);
+        const int row = ROWS ? max(row_of(s, r.start + token), 0) : r.start + token;
+        const u32x4v* p = reinterpret_cast<const u32x4v*>(a.q + row * a.ldq + hk * DK) + g4;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) q[ks][j] = __builtin_bit_cast(bf8, p[4 * ks]);
+      }
+    };
+    if (a.q && chunks) read_q(0);
     barrier();
     for (int c = 0; c <= chunks; ++c) {
       if (c > 0 && a.q) {
-        const int was = (c - 1) & 1;
-        const bf8* const pf = reinterpret_cast<const bf8*>(lds.second[was]) + lane;
-        const float* const rows = reinterpret_cast<const float*>(lds.second[was] + kFragments * 1024) + c16;
-        f32x4v o[kTiles][4];
+        const ChunkLds<DK>& was = lds.chunk[(c - 1) & 1];
+        const char* const second = lds.second[(c - 1) & 1];
+        const bf8* const pf = reinterpret_cast<const bf8*>(second) + lane;
+        const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + 32 * half + c16;
+        // all of LDS's first, which then answers while the products run
+        bf8 sw[kTiles][KS], uw[kTiles][2], p[2][2];
+        float scale[2];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) sw[n][ks] = was.s[n][ks][lane];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) scale[j] = rows[16 * j];
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) uw[n][0] = was.u[n][0][lane];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) p[j][0] = pf[(half ? fragment_of(2 + j, 0) : fragment_of(j, 0)) * 64];
+        if (half) {
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) uw[n][1] = was.u[n][1][lane];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) p[j][1] = pf[fragment_of(2 + j, 1) * 64];
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        f32x4v o[kTiles][2];
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) o[n][rt] = f32x4v{0, 0, 0, 0};
+          for (int j = 0; j < 2; ++j) o[n][j] = f32x4v{0, 0, 0, 0};
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          bf8 sw[kTiles];
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) sw[n] = lds.chunk[was].s[n][ks][lane];
+          for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            const bf8 q = rows_operand<DK>(lds.q[was], rt, ks);
+            for (int j = 0; j < 2; ++j) o[n][j] = mma(sw[n][ks], q[ks][j], o[n][j]);
+        if (c < chunks) read_q(c);
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) o[n][rt] = mma(sw[n], q, o[n][rt]);
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            o[n][j] *= scale[j];
+            o[n][j] = mma(uw[n][0], p[j][0], o[n][j]);
           }
-        }
+        if (half) {
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const float x = rows[16 * rt];
+          for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) o[n][rt] *= x;
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          bf8 uw[kTiles];
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) uw[n] = lds.chunk[was].u[n][ks][lane];
-#pragma unroll
-          for (int rt = 2 * ks; rt < 4; ++rt) {
-            const bf8 p = pf[fragment_of(rt, ks) * 64];
-#pragma unroll
-            for (int n = 0; n < kTiles; ++n) o[n][rt] = mma(uw[n], p, o[n][rt]);
-          }
+            for (int j = 0; j < 2; ++j) o[n][j] = mma(uw[n][1], p[j][1], o[n][j]);
         }
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
-          const uint64_t* const bad = lds.chunk[was].bad[n];
+          const uint64_t* const bad = was.bad[n];
           if (!__any(bad[c16] != 0)) continue;
 #pragma unroll
-          for (int rt = 0; rt < 4; ++rt) {
-            const int in = 16 * rt + c16;
+          for (int j = 0; j < 2; ++j) {
+            const int in = 32 * half + 16 * j + c16;
             const uint64_t path = (c - 1) * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (path & bad[4 * g4 + i]) o[n][rt][i] = NAN;
+              if (path & bad[4 * g4 + i]) o[n][j][i] = NAN;
           }
         }
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) {
-          const int token = (c - 1) * kChunk + 16 * rt + c16;
+        for (int j = 0; j < 2; ++j) {
+          const int token = (c - 1) * kChunk + 32 * half + 16 * j + c16;
           const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
           if (row >= 0) {
+            uint16_t* const to = a.out + row * a.ldo + h * a.dv + col0 + 8 * g4;
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n)
-              *reinterpret_cast<uint2*>(a.out + row * a.ldo + h * a.dv + col0 + 16 * n + 4 * g4) =
-                  make_uint2(bf16_pair(o[n][rt][0], o[n][rt][1]), bf16_pair(o[n][rt][2], o[n][rt][3]));
+            for (int n = 0; n < kTiles; n += 2)
+              *reinterpret_cast<bf8*>(to + 16 * n) = high(o[n][j], o[n + 1][j]);
           }
         }
       }
@@ -508,9 +531,10 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     return;
   }
 
-  // ---- 16 columns of S through the chunks: what the kernel's time is made of
+  // ---- 16 columns of S through the chunks: what the kernel's time is made of.  Of every 8 columns, two waves have 4 each: so the outputs
+  // have 8 neighbours in a lane.
   const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
-  const int64_t state_at = ((int64_t)h * a.dv + col0 + w * 16 + c16) * DK + 8 * g4;
+  const int64_t state_at = ((int64_t)h * a.dv + col0 + (w >> 1) * 32 + (c16 >> 2) * 8 + (w & 1) * 4 + (c16 & 3)) * DK + 8 * g4;
   f32x4v st[RT];
 #pragma unroll
   for (int i = 0; i < RT; ++i) st[i] = f32x4v{0, 0, 0, 0};
@@ -551,7 +575,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     i16x4 v[4];
     bf8 t[2 * kFragments], sh[KS], sl[KS];
     // V turned: a lane's column of 4 neighbouring tokens
-    const uint32_t vat = lds_off(here.v) + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + w * 32 + (c16 & 3) * 8;
+    const uint32_t vat = lds_off(here.v) + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + (w >> 1) * 64 + (c16 & 3) * 16 + (w & 1) * 8;
 #pragma unroll
     for (int rt = 0; rt < 4; ++rt) {
       taken[rt] = *reinterpret_cast<const f32x4v*>(rows + kTaken + 16 * rt);
