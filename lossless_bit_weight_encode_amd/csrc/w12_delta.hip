@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
 
 // Tokens a sequence has, on average, from which they are taken 64 at a time.
 constexpr int kChunkFrom = 16;
-static bool in_chunks(const w12_sequences& s) { return s.tree_mask || s.T >= (int64_t)kChunkFrom * s.count; }
+static bool in_chunks(const w12_sequences& s) { return s.tree_mask || (!s.lens && s.T >= (int64_t)kChunkFrom * s.count) || (s.lens && s.T > (int64_t)W12_TREE_NODES * s.count); }
 
 uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) {
   return delta_chunk_workspace_bytes(T, count, v_heads);

@@ -6,8 +6,8 @@
 // it; the last of a request's work-groups to arrive walks down the tree.  A chain with the drafter's probabilities needs
 // no row's token but one: its acceptances follow from the sums alone, and the row after which it was cut is gone over in
 // pieces again, with the last work-group to arrive picking the token.
-// Everything that decides is FP64, so that the token does not depend on how the sum was split (a border
-// between two tokens is missed by 2^-40 of the total at the most).
+// Everything that decides is FP64 (which here runs at the rate of FP32), so that the token does not depend on how the sum was split:
+// a border between two tokens is missed by 2^-40 of the total at the most.
 #include <limits.h>
 
 #include "w12_gemm_common.h"
@@ -17,7 +17,9 @@
 namespace w12 {
 
 constexpr int kVerifyThreads = 256;
-constexpr int kVerifyValues = 32;                              // of a thread, neighbours
+constexpr int kVerifyWaves = kVerifyThreads / 64;
+constexpr int kVerifyRounds = 4;                               // of 256 neighbouring values, for each wave
+constexpr int kVerifyValues = 4 * kVerifyRounds;               // of a thread
 constexpr int kVerifyPiece = kVerifyThreads * kVerifyValues;   // values of a piece
 
 // A piece's maximum, where it is first met, and the sum of its weights relative to it.
@@ -74,153 +76,220 @@ __device__ __forceinline__ double random_of(const float* u, int row) {
   const float x = u[row];
   return (double)(x >= 0.0f ? min(x, 0.99999994f) : 0.0f);
 }
+__device__ __forceinline__ float no_nan(float z) { return z == z ? z : -INFINITY; }
 template <bool F32>
 __device__ __forceinline__ float logit(const w12_verify_draft_args& a, int64_t row, int i) {
-  const float z = F32 ? static_cast<const float*>(a.logits)[row * a.ld_logits + i]
-                      : bf16_float(static_cast<const uint16_t*>(a.logits)[row * a.ld_logits + i]);
-  return z == z ? z : -INFINITY;
+  return no_nan(F32 ? static_cast<const float*>(a.logits)[row * a.ld_logits + i]
+                    : bf16_float(static_cast<const uint16_t*>(a.logits)[row * a.ld_logits + i]));
 }
+
+// 2^t of t <= 0, to 2^-42 of itself: 2^f of the rest f in [-1/2, 1/2] by its series, whose first term left out is (ln 2 / 2)^11 / 11!.
+// What is below 2^-1100 is 0.
+__device__ __forceinline__ double power(double t) {
+  t = fmax(t, -1100.0);
+  const double n = rint(t), f = t - n;
+  constexpr double l = 0.69314718055994530942;
+  constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5, c6 = c5 * l / 6, c7 = c6 * l / 7, c8 = c7 * l / 8,
+                   c9 = c8 * l / 9, c10 = c9 * l / 10;
+  double p = fma(f, c10, c9);
+  p = fma(f, p, c8);
+  p = fma(f, p, c7);
+  p = fma(f, p, c6);
+  p = fma(f, p, c5);
+  p = fma(f, p, c4);
+  p = fma(f, p, c3);
+  p = fma(f, p, c2);
+  p = fma(f, p, l);
+  p = fma(f, p, 1.0);
+  return __builtin_amdgcn_ldexp(p, (int)n);
+}
+// log2(e) / temperature
+__device__ __forceinline__ double steepness(float t) { return 1.4426950408889634074 / (double)t; }
 // The weight of a logit beside the row's largest.  A row whose largest is +inf gives all to the first of them, a temperature of 0 to the
 // first of the largest: those are told apart by the place alone.
-__device__ __forceinline__ double weight(float z, float top, double inv_t) {
-  return z == -INFINITY ? 0.0 : exp(((double)z - (double)top) * inv_t);
-}
+__device__ __forceinline__ double weight(float z, float top, double steep) { return power(((double)z - (double)top) * steep); }
 
-// A row's largest logit, its place, and the sum of weights (0: one place has it all, or there is none).
-struct Row {
-  float top;
-  int at;
-  double total, inv_t;
-  bool one;              // the whole weight is in `at`
-};
-
-__device__ __forceinline__ Row row_of_pieces(const Verify& v, int row, float t) {
-  Row r;
-  r.top = -INFINITY;
-  r.at = -1;
-  const Piece* p = v.pieces + (int64_t)row * v.count;
-  for (int i = 0; i < v.count; ++i)
-    if (p[i].at >= 0 && (r.at < 0 || p[i].max > r.top)) r.top = p[i].max, r.at = p[i].at;
-  r.one = t == 0.0f || r.top == INFINITY;
-  r.inv_t = r.one ? 1.0 : 1.0 / (double)t;
-  r.total = 0.0;
-  if (r.at >= 0 && !r.one)
-    for (int i = 0; i < v.count; ++i)
-      if (p[i].at >= 0) r.total += p[i].sum * exp(((double)p[i].max - (double)r.top) * r.inv_t);
-  return r;
-}
-
-// A work-group's sum, and each thread's sum of those before it.
-__device__ __forceinline__ double scan_group(double v, double* lds, double& before) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// A wave's, and a work-group's, sums, and what was before each thread.
+__device__ __forceinline__ double scan_wave(double v, double& before) {
+  const int lane = threadIdx.x & 63;
   double s = v;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
     const double u = __shfl_up(s, o);
     if (lane >= o) s += u;
   }
-  if (lane == 63) lds[w] = s;
+  before = s - v;
+  return __shfl(s, 63);
+}
+__device__ __forceinline__ double scan_group(double v, double* lds, double& before) {
+  const int w = threadIdx.x >> 6;
+  const double mine = scan_wave(v, before);
+  if ((threadIdx.x & 63) == 0) lds[w] = mine;
   __syncthreads();
   double off = 0.0, total = 0.0;
-  for (int i = 0; i < kVerifyThreads / 64; ++i) {
+#pragma unroll
+  for (int i = 0; i < kVerifyWaves; ++i) {
     if (i < w) off += lds[i];
     total += lds[i];
   }
-  before = off + s - v;
+  before += off;
   __syncthreads();
   return total;
 }
-
-template <bool F32>
-__global__ __launch_bounds__(kVerifyThreads) void k_pieces(Verify v) {
-  const w12_verify_draft_args& a = v.a;
-  __shared__ float wmax[kVerifyThreads / 64];
-  __shared__ int wat[kVerifyThreads / 64];
-  __shared__ double lds[kVerifyThreads / 64];
-  const int piece = blockIdx.y, row = blockIdx.x, lane = threadIdx.x & 63;
-  if (row == 0 && piece == 0)
-    for (int i = threadIdx.x; i < a.requests; i += kVerifyThreads) v.arrived[i] = 0;
-  const int b = request_of_row(a, row);
-  const float t = temperature_of(a, b);
-  const int i0 = piece * kVerifyPiece + threadIdx.x * kVerifyValues;
-  float z[kVerifyValues];
-  float m = -INFINITY;
-  int at = INT_MAX;
-#pragma unroll
-  for (int i = 0; i < kVerifyValues; ++i) {
-    z[i] = i0 + i < a.vocab ? logit<F32>(a, row, i0 + i) : -INFINITY;
-    if (z[i] > m) m = z[i], at = i0 + i;
-  }
-  float top = m;
-  int first = at;
+// The largest of a work-group's values, and where it is first met.
+__device__ __forceinline__ void largest(float& top, int& at, float* ldsf, int* ldsi) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
-    const float om = __shfl_xor(top, o);
-    const int oa = __shfl_xor(first, o);
-    if (om > top || (om == top && oa < first)) top = om, first = oa;
+    const float m = __shfl_xor(top, o);
+    const int i = __shfl_xor(at, o);
+    if (m > top || (m == top && i < at)) top = m, at = i;
   }
-  if (lane == 0) wmax[threadIdx.x >> 6] = top, wat[threadIdx.x >> 6] = first;
+  if ((threadIdx.x & 63) == 0) ldsf[threadIdx.x >> 6] = top, ldsi[threadIdx.x >> 6] = at;
   __syncthreads();
-  for (int i = 0; i < kVerifyThreads / 64; ++i)
-    if (wmax[i] > top || (wmax[i] == top && wat[i] < first)) top = wmax[i], first = wat[i];
-  double sum = 0.0, before;
-  if (t > 0.0f && first != INT_MAX && top != INFINITY) {
-    const double inv_t = 1.0 / (double)t;
 #pragma unroll
-    for (int i = 0; i < kVerifyValues; ++i) sum += weight(z[i], top, inv_t);
-  }
-  sum = scan_group(sum, lds, before);
-  if (threadIdx.x == 0) v.pieces[(int64_t)row * v.count + piece] = Piece{sum, top, first == INT_MAX ? -1 : first};
-}
-
-// The place in a piece whose running sum of weights passes `target`; values(i) is the weight of place i of the row, where it is.  If rounding leaves
-// none, the last place with a weight.
-template <typename F>
-__device__ __forceinline__ int find_place(int piece, double target, int* best, double* lds, F value) {
-  const int i0 = piece * kVerifyPiece + threadIdx.x * kVerifyValues;
-  if (threadIdx.x == 0) best[0] = INT_MAX, best[1] = -1;
-  double sum = 0.0, before;
-  int last = -1;
-  for (int i = 0; i < kVerifyValues; ++i) {
-    const double w = value(i0 + i);
-    sum += w;
-    if (w > 0.0) last = i0 + i;
-  }
-  scan_group(sum, lds, before);
-  double run = before;
-  for (int i = 0; i < kVerifyValues; ++i) {
-    const double w = value(i0 + i);
-    run += w;
-    if (w > 0.0 && run > target) {
-      atomicMin(&best[0], i0 + i);
-      break;
-    }
-  }
-  if (last >= 0) atomicMax(&best[1], last);
+  for (int i = 0; i < kVerifyWaves; ++i)
+    if (ldsf[i] > top || (ldsf[i] == top && ldsi[i] < at)) top = ldsf[i], at = ldsi[i];
   __syncthreads();
-  return best[0] != INT_MAX ? best[0] : best[1];
 }
 
-// Which piece the running sum passes `target` in, and the sum before it; the last with a weight if rounding leaves none.
+struct VerifyLds {
+  double d[kVerifyWaves], target;
+  float f[kVerifyWaves];
+  int i[kVerifyWaves], found, last;
+  uint32_t place;
+};
+
+// A row's largest logit, its place (INT_MAX: there is none), and the sum of weights.
+struct Row {
+  float top;
+  int at;
+  double total, steep;
+  bool one;              // the whole weight is in `at`
+};
+
+// A row of its pieces, by a work-group.  Threads take neighbouring pieces; `mine` is the weight of a thread's, `before` of those in front.
+__device__ __forceinline__ int pieces_each(int count) { return (count + kVerifyThreads - 1) / kVerifyThreads; }
+__device__ __forceinline__ double piece_weight(const Piece& p, const Row& r) { return p.at < 0 ? 0.0 : p.sum * weight(p.max, r.top, r.steep); }
+__device__ __forceinline__ Row row_of_pieces(const Verify& v, int row, float t, VerifyLds& lds, double& mine, double& before) {
+  Row r;
+  r.top = -INFINITY;
+  r.at = INT_MAX;
+  const Piece* p = v.pieces + (int64_t)row * v.count;
+  const int each = pieces_each(v.count), p0 = threadIdx.x * each, p1 = min(p0 + each, v.count);
+  for (int i = p0; i < p1; ++i)
+    if (p[i].at >= 0 && (r.at == INT_MAX || p[i].max > r.top)) r.top = p[i].max, r.at = p[i].at;
+  largest(r.top, r.at, lds.f, lds.i);
+  r.one = t == 0.0f || r.top == INFINITY;
+  r.steep = r.one ? 1.0 : steepness(t);
+  mine = 0.0;
+  if (r.at != INT_MAX && !r.one)
+    for (int i = p0; i < p1; ++i) mine += piece_weight(p[i], r);
+  r.total = scan_group(mine, lds.d, before);
+  return r;
+}
+// The same by a thread, for its own row; the sum alone.
+__device__ __forceinline__ Row row_alone(const Verify& v, int row, float t) {
+  Row r;
+  r.top = -INFINITY;
+  r.at = INT_MAX;
+  const Piece* p = v.pieces + (int64_t)row * v.count;
+  for (int i = 0; i < v.count; ++i)
+    if (p[i].at >= 0 && (r.at == INT_MAX || p[i].max > r.top)) r.top = p[i].max, r.at = p[i].at;
+  r.one = t == 0.0f || r.top == INFINITY;
+  r.steep = r.one ? 1.0 : steepness(t);
+  r.total = 0.0;
+  if (r.at != INT_MAX && !r.one)
+    for (int i = 0; i < v.count; ++i) r.total += piece_weight(p[i], r);
+  return r;
+}
+
+// Of work-groups' threads with weights of their own and the weight before them: the one in which the running sum passes `target`, and the
+// last with a weight, should rounding leave none.  The thread then looks at its parts.
 template <typename F>
-__device__ __forceinline__ int find_in(int count, double& target, F sum_of) {
-  double run = 0.0;
-  int last = -1;
-  double last_before = 0.0;
-  for (int i = 0; i < count; ++i) {
-    const double s = sum_of(i);
-    if (s > 0.0) {
-      if (run + s > target) {
-        target -= run;
-        return i;
-      }
-      last = i;
-      last_before = run;
+__device__ __forceinline__ void pass_to(double target, double mine, double before, VerifyLds& lds, F parts) {
+  if (threadIdx.x == 0) lds.found = lds.last = -1;
+  __syncthreads();
+  const bool has = mine > 0.0, in = has && before <= target && target < before + mine;
+  if (in) atomicMax(&lds.found, (int)threadIdx.x);      // two can be it only where sums are rounded apart
+  const uint64_t any = __ballot(has);
+  if (any && (threadIdx.x & 63) == 0) atomicMax(&lds.last, (int)threadIdx.x + 63 - __builtin_clzll(any));
+  __syncthreads();
+  const int who = lds.found >= 0 ? lds.found : lds.last;
+  if ((int)threadIdx.x == who) parts(target - before);
+  __syncthreads();
+}
+
+// Where a thread's values of a piece are: 4 neighbours, every 256.
+__device__ __forceinline__ int place_of(int piece, int round) {
+  return piece * kVerifyPiece + (int)(threadIdx.x >> 6) * (256 * kVerifyRounds) + round * 256 + (int)(threadIdx.x & 63) * 4;
+}
+// Four neighbouring logits, -inf past the end.
+template <bool F32>
+__device__ __forceinline__ void logits4(const w12_verify_draft_args& a, int64_t row, int i, float z[4]) {
+  if (i + 4 <= a.vocab) {
+    if constexpr (F32) {
+      const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(a.logits) + row * a.ld_logits + i);
+      z[0] = x.x; z[1] = x.y; z[2] = x.z; z[3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.logits) + row * a.ld_logits + i);
+      z[0] = bf16_float(x.x); z[1] = __builtin_bit_cast(float, x.x & 0xFFFF0000u);
+      z[2] = bf16_float(x.y); z[3] = __builtin_bit_cast(float, x.y & 0xFFFF0000u);
     }
-    run += s;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = no_nan(z[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) z[e] = i + e < a.vocab ? logit<F32>(a, row, i + e) : -INFINITY;
   }
-  target -= last_before;
-  return last;
+}
+
+// The token of a piece in whose weights the running sum passes lds.target; weights4(i, w) gives those of places i .. i + 3.  By a whole work-group.
+template <typename F>
+__device__ __forceinline__ int find_token(int piece, VerifyLds& lds, F weights4) {
+  double w[kVerifyRounds][4], round[kVerifyRounds], sum = 0.0, before, unused;
+#pragma unroll
+  for (int j = 0; j < kVerifyRounds; ++j) {
+    weights4(place_of(piece, j), w[j]);
+    round[j] = w[j][0] + w[j][1] + w[j][2] + w[j][3];
+    sum += round[j];
+  }
+  const double target = lds.target;
+  const double wave = scan_wave(sum, unused);
+  if ((threadIdx.x & 63) == 0) lds.d[threadIdx.x >> 6] = wave;
+  if (threadIdx.x == 0) lds.found = INT_MAX, lds.last = -1;
+  __syncthreads();
+  double run = 0.0;
+  for (int i = 0; i < (int)(threadIdx.x >> 6); ++i) run += lds.d[i];
+  // every wave goes through its values; the first place that passes is the token
+  int first = INT_MAX, last = -1;
+#pragma unroll
+  for (int j = 0; j < kVerifyRounds; ++j) {
+    const double all = scan_wave(round[j], before);
+    double at = run + before;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      at += w[j][e];
+      if (w[j][e] > 0.0) {
+        if (at > target) first = min(first, place_of(piece, j) + e);
+        last = place_of(piece, j) + e;
+      }
+    }
+    run += all;
+  }
+  // one lane for the wave: atomics on one place go one after another
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    first = min(first, __shfl_xor(first, o));
+    last = max(last, __shfl_xor(last, o));
+  }
+  if ((threadIdx.x & 63) == 0) {
+    atomicMin(&lds.found, first);
+    atomicMax(&lds.last, last);
+  }
+  __syncthreads();
+  const int token = lds.found != INT_MAX ? lds.found : lds.last;
+  __syncthreads();
+  return token;
 }
 
 // Whether this work-group is the last of `of` of a request to arrive; what the others wrote before is then visible.
@@ -234,30 +303,83 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, uint32_t of, u
   return last;
 }
 
+template <bool F32>
+__global__ __launch_bounds__(kVerifyThreads) void k_pieces(Verify v) {
+  const w12_verify_draft_args& a = v.a;
+  __shared__ VerifyLds lds;
+  const int piece = blockIdx.y, row = blockIdx.x;
+  float z[kVerifyRounds][4];
+#pragma unroll
+  for (int j = 0; j < kVerifyRounds; ++j) logits4<F32>(a, row, place_of(piece, j), z[j]);
+  if (row == 0 && piece == 0)
+    for (int i = threadIdx.x; i < a.requests; i += kVerifyThreads) {
+      v.arrived[i] = 0;
+      if (nodes_of(a, i).n == 0) a.count[i] = 0, a.next_token[i] = -1;
+    }
+  const float t = temperature_of(a, request_of_row(a, row));
+  float top = -INFINITY;
+  int at = INT_MAX;
+#pragma unroll
+  for (int j = 0; j < kVerifyRounds; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (z[j][e] > top) top = z[j][e], at = place_of(piece, j) + e;
+  largest(top, at, lds.f, lds.i);
+  double sum = 0.0, before;
+  if (t > 0.0f && at != INT_MAX && top != INFINITY) {
+    const double steep = steepness(t);
+#pragma unroll
+    for (int j = 0; j < kVerifyRounds; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += weight(z[j][e], top, steep);
+  }
+  sum = scan_group(sum, lds.d, before);
+  if (threadIdx.x == 0) v.pieces[(int64_t)row * v.count + piece] = Piece{sum, top, at == INT_MAX ? -1 : at};
+}
+
+// The token that u takes from a row, by a whole work-group.
+template <bool F32>
+__device__ __forceinline__ int take(const Verify& v, int row, float t, VerifyLds& lds) {
+  const w12_verify_draft_args& a = v.a;
+  double mine, before;
+  const Row r = row_of_pieces(v, row, t, lds, mine, before);
+  if (r.at == INT_MAX) return -1;
+  if (r.one) return r.at;
+  const Piece* p = v.pieces + (int64_t)row * v.count;
+  pass_to(random_of(a.u, row) * r.total, mine, before, lds, [&](double target) {
+    const int each = pieces_each(v.count), p0 = threadIdx.x * each, p1 = min(p0 + each, v.count);
+    int in = p0;
+    double run = 0.0, start = 0.0;
+    for (int i = p0; i < p1; ++i) {
+      const double w = piece_weight(p[i], r);
+      if (w > 0.0) in = i, start = run;
+      run += w;
+      if (w > 0.0 && run > target) break;
+    }
+    lds.place = (uint32_t)in;
+    lds.target = target - start;
+  });
+  const int piece = (int)lds.place;
+  return find_token(piece, lds, [&](int i, double w[4]) {
+    float z[4];
+    logits4<F32>(a, row, i, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = weight(z[e], r.top, r.steep);
+  });
+}
+
 // The token of every row, and the walk.
 template <bool F32>
 __global__ __launch_bounds__(kVerifyThreads) void k_take(Verify v) {
   const w12_verify_draft_args& a = v.a;
-  __shared__ double lds[kVerifyThreads / 64];
-  __shared__ int best[2];
-  __shared__ uint32_t place;
+  __shared__ VerifyLds lds;
   __shared__ int child[W12_VERIFY_NODES];
   const int row = blockIdx.x, b = request_of_row(a, row);
   const Nodes nodes = nodes_of(a, b);
   if (row < nodes.start || row >= nodes.start + nodes.n) return;
-  const Row r = row_of_pieces(v, row, temperature_of(a, b));
-  int token = r.at;
-  if (r.at >= 0 && !r.one) {
-    double target = random_of(a.u, row) * r.total;
-    const Piece* p = v.pieces + (int64_t)row * v.count;
-    const int piece = find_in(v.count, target, [&](int i) {
-      return p[i].at >= 0 ? p[i].sum * exp(((double)p[i].max - (double)r.top) * r.inv_t) : 0.0;
-    });
-    if (piece >= 0)
-      token = find_place(piece, target, best, lds, [&](int i) { return i < a.vocab ? weight(logit<F32>(a, row, i), r.top, r.inv_t) : 0.0; });
-  }
+  const int token = take<F32>(v, row, temperature_of(a, b), lds);
   if (threadIdx.x == 0) __hip_atomic_store(&v.taken[row], token, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (!last_to_arrive(&v.arrived[b], (uint32_t)nodes.n, &place)) return;
+  if (!last_to_arrive(&v.arrived[b], (uint32_t)nodes.n, &lds.place)) return;
   for (int i = threadIdx.x; i < nodes.n; i += kVerifyThreads) child[i] = INT_MAX;
   __syncthreads();
   for (int i = 1 + threadIdx.x; i < nodes.n; i += kVerifyThreads) {
@@ -276,19 +398,18 @@ __global__ __launch_bounds__(kVerifyThreads) void k_take(Verify v) {
     }
     a.count[b] = n;
     a.next_token[b] = __hip_atomic_load(&v.taken[nodes.start + at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    best[0] = n;
+    lds.found = n;
   }
   __syncthreads();
-  for (int i = best[0] + threadIdx.x; i < all; i += kVerifyThreads) a.path[nodes.start + i] = -1;
+  for (int i = lds.found + threadIdx.x; i < all; i += kVerifyThreads) a.path[nodes.start + i] = -1;
 }
 
 // A chain with the drafter's probabilities: acceptances, and the token after the cut.
 template <bool F32>
 __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
   const w12_verify_draft_args& a = v.a;
-  __shared__ double lds[kVerifyThreads / 64];
-  __shared__ int best[2], cut;
-  __shared__ uint32_t place;
+  __shared__ VerifyLds lds;
+  __shared__ int cut;
   const int piece = blockIdx.x, b = blockIdx.y;
   const Nodes nodes = nodes_of(a, b);
   if (nodes.n == 0) return;
@@ -299,9 +420,9 @@ __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
     const int row = nodes.start + i, x = a.tokens[row];
     bool good = false;
     if (x >= 0 && x < a.vocab) {
-      const Row r = row_of_pieces(v, row - 1, t);
+      const Row r = row_alone(v, row - 1, t);
       double p = 0.0;
-      if (r.at >= 0) p = r.one ? (x == r.at ? 1.0 : 0.0) : weight(logit<F32>(a, row - 1, x), r.top, r.inv_t) / r.total;
+      if (r.at != INT_MAX) p = r.one ? (x == r.at ? 1.0 : 0.0) : weight(logit<F32>(a, row - 1, x), r.top, r.steep) / r.total;
       good = random_of(a.accept_u, row) * (double)a.q[row * a.ldq + x] < p;
     }
     if (!good) atomicMin(&cut, i);
@@ -309,58 +430,62 @@ __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
   __syncthreads();
   const int n = cut, row = nodes.start + n - 1;
   const bool whole = n == nodes.n;
-  const Row r = row_of_pieces(v, row, t);
-  const float* q = whole ? nullptr : a.q + (row + 1) * a.ldq;
-  auto p_of = [&](int i) -> double {
-    if (i >= a.vocab || r.at < 0) return 0.0;
-    return r.one ? (i == r.at ? 1.0 : 0.0) : weight(logit<F32>(a, row, i), r.top, r.inv_t) / r.total;
+  double mine, before;
+  const Row r = row_of_pieces(v, row, t, lds, mine, before);
+  const double inverse = r.one || r.at == INT_MAX ? 0.0 : 1.0 / r.total;
+  const float* const q = whole ? nullptr : a.q + (row + 1) * a.ldq;
+  // what is left of p over q, which is all of p behind the last node
+  auto rest4 = [&](int i, double w[4]) {
+    float z[4];
+    logits4<F32>(a, row, i, z);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      double p = 0.0;
+      if (i + e < a.vocab && r.at != INT_MAX) p = r.one ? (i + e == r.at ? 1.0 : 0.0) : weight(z[e], r.top, r.steep) * inverse;
+      if (!whole) {
+        p = i + e < a.vocab ? p - (double)q[i + e] : 0.0;
+        p = p > 0.0 ? p : 0.0;
+      }
+      w[e] = p;
+    }
   };
-  auto rest_of = [&](int i) -> double {
-    if (i >= a.vocab) return 0.0;
-    const double d = p_of(i) - (double)q[i];
-    return d > 0.0 ? d : 0.0;
-  };
-  double sum = 0.0, before;
-  for (int i = 0; i < kVerifyValues; ++i) {
-    const int at = piece * kVerifyPiece + threadIdx.x * kVerifyValues + i;
-    sum += whole ? p_of(at) : rest_of(at);
+  double sum = 0.0, w[4];
+#pragma unroll
+  for (int j = 0; j < kVerifyRounds; ++j) {
+    rest4(place_of(piece, j), w);
+    sum += w[0] + w[1] + w[2] + w[3];
   }
-  sum = scan_group(sum, lds, before);
+  sum = scan_group(sum, lds.d, before);
   double* sums = v.rest + (int64_t)b * v.count;
   if (threadIdx.x == 0) __hip_atomic_store(&sums[piece], sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  if (!last_to_arrive(&v.arrived[b], (uint32_t)v.count, &place)) return;
+  if (!last_to_arrive(&v.arrived[b], (uint32_t)v.count, &lds.place)) return;
+  const int each = pieces_each(v.count), p0 = threadIdx.x * each, p1 = min(p0 + each, v.count);
   auto sum_of = [&](int i) { return __hip_atomic_load(&sums[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  double total = 0.0;
-  for (int i = 0; i < v.count; ++i) total += sum_of(i);
-  int token = -1;
-  const double u = random_of(a.u, row);
+  mine = 0.0;
+  for (int i = p0; i < p1; ++i) mine += sum_of(i);
+  const double total = scan_group(mine, lds.d, before);
+  int token;
   if (total > 0.0) {
-    double target = u * total;
-    const int in = find_in(v.count, target, sum_of);
-    token = find_place(in, target, best, lds, [&](int i) { return whole ? p_of(i) : rest_of(i); });
-  } else if (r.at >= 0) {
-    // nothing is left over: from p itself
-    token = r.at;
-    if (!r.one) {
-      const Piece* p = v.pieces + (int64_t)row * v.count;
-      double target = u * r.total;
-      const int in = find_in(v.count, target, [&](int i) {
-        return p[i].at >= 0 ? p[i].sum * exp(((double)p[i].max - (double)r.top) * r.inv_t) : 0.0;
-      });
-      token = find_place(in, target / r.total, best, lds, p_of);
-    }
+    pass_to(random_of(a.u, row) * total, mine, before, lds, [&](double target) {
+      int in = p0;
+      double run = 0.0, start = 0.0;
+      for (int i = p0; i < p1; ++i) {
+        const double x = sum_of(i);
+        if (x > 0.0) in = i, start = run;
+        run += x;
+        if (x > 0.0 && run > target) break;
+      }
+      lds.place = (uint32_t)in;
+      lds.target = target - start;
+    });
+    const int in = (int)lds.place;
+    token = find_token(in, lds, rest4);
+  } else {
+    token = take<F32>(v, row, t, lds);      // nothing is left over: from p itself
   }
   if (threadIdx.x == 0) a.count[b] = n, a.next_token[b] = token;
   const int all = nodes_of(a, b, true).n;
   for (int i = threadIdx.x; i < all; i += kVerifyThreads) a.path[nodes.start + i] = i < n ? nodes.start + i : -1;
-}
-
-// Requests without nodes.
-__global__ __launch_bounds__(kVerifyThreads) void k_empty(Verify v) {
-  const int b = blockIdx.x * kVerifyThreads + threadIdx.x;
-  if (b >= v.a.requests || nodes_of(v.a, b).n) return;
-  v.a.count[b] = 0;
-  v.a.next_token[b] = -1;
 }
 
 static uint64_t round16(uint64_t x) { return (x + 15) / 16 * 16; }
@@ -386,7 +511,6 @@ hipError_t launch_verify_draft(const w12_verify_draft_args& a, void* ws, hipStre
   const dim3 grid((unsigned)a.T, (unsigned)v.count);
   if (f32) k_pieces<true><<<grid, kVerifyThreads, 0, stream>>>(v);
   else k_pieces<false><<<grid, kVerifyThreads, 0, stream>>>(v);
-  k_empty<<<(unsigned)ceil_div(a.requests, kVerifyThreads), kVerifyThreads, 0, stream>>>(v);
   const dim3 chains((unsigned)v.count, (unsigned)a.requests);
   if (a.q) {
     if (f32) k_chain<true><<<chains, kVerifyThreads, 0, stream>>>(v);
