@@ -84,10 +84,11 @@ __device__ __forceinline__ float logit(const w12_verify_draft_args& a, int64_t r
 }
 
 // 2^t of t <= 0, to 2^-42 of itself: 2^f of the rest f in [-1/2, 1/2] by its series, whose first term left out is (ln 2 / 2)^11 / 11!.
-// What is below 2^-1100 is 0.
+// t is rounded by adding 3/2 2^52, which leaves the whole number in the low bits; it goes into the exponent as it is (rounding and
+// scaling instructions of FP64 run at a part of the rate).  What is below 2^-1000 is 0.
 __device__ __forceinline__ double power(double t) {
-  t = fmax(t, -1100.0);
-  const double n = rint(t), f = t - n;
+  constexpr double shift = 6755399441055744.0;
+  const double n = t + shift, f = t - (n - shift);
   constexpr double l = 0.69314718055994530942;
   constexpr double c2 = l * l / 2, c3 = c2 * l / 3, c4 = c3 * l / 4, c5 = c4 * l / 5, c6 = c5 * l / 6, c7 = c6 * l / 7, c8 = c7 * l / 8,
                    c9 = c8 * l / 9, c10 = c9 * l / 10;
@@ -101,7 +102,10 @@ __device__ __forceinline__ double power(double t) {
   p = fma(f, p, c2);
   p = fma(f, p, l);
   p = fma(f, p, 1.0);
-  return __builtin_amdgcn_ldexp(p, (int)n);
+  const uint64_t bits = __builtin_bit_cast(uint64_t, p);
+  const uint32_t whole = (uint32_t)__builtin_bit_cast(uint64_t, n) << 20;
+  const double r = __builtin_bit_cast(double, (uint64_t)((uint32_t)(bits >> 32) + whole) << 32 | (uint32_t)bits);
+  return t > -1000.0 ? r : 0.0;
 }
 // log2(e) / temperature
 __device__ __forceinline__ double steepness(float t) { return 1.4426950408889634074 / (double)t; }
@@ -187,19 +191,28 @@ __device__ __forceinline__ Row row_of_pieces(const Verify& v, int row, float t, 
   r.total = scan_group(mine, lds.d, before);
   return r;
 }
-// The same by a thread, for its own row; the sum alone.
-__device__ __forceinline__ Row row_alone(const Verify& v, int row, float t) {
+// The same by 16 lanes, for a row of their own; the sum alone.
+__device__ __forceinline__ Row row_of_lanes(const Verify& v, int row, float t) {
   Row r;
   r.top = -INFINITY;
   r.at = INT_MAX;
   const Piece* p = v.pieces + (int64_t)row * v.count;
-  for (int i = 0; i < v.count; ++i)
+  const int lane = threadIdx.x & 15;
+  for (int i = lane; i < v.count; i += 16)
     if (p[i].at >= 0 && (r.at == INT_MAX || p[i].max > r.top)) r.top = p[i].max, r.at = p[i].at;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) {
+    const float m = __shfl_xor(r.top, o);
+    const int i = __shfl_xor(r.at, o);
+    if (i != INT_MAX && (r.at == INT_MAX || m > r.top || (m == r.top && i < r.at))) r.top = m, r.at = i;
+  }
   r.one = t == 0.0f || r.top == INFINITY;
   r.steep = r.one ? 1.0 : steepness(t);
   r.total = 0.0;
   if (r.at != INT_MAX && !r.one)
-    for (int i = 0; i < v.count; ++i) r.total += piece_weight(p[i], r);
+    for (int i = lane; i < v.count; i += 16) r.total += piece_weight(p[i], r);
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) r.total += __shfl_xor(r.total, o);
   return r;
 }
 
@@ -292,14 +305,13 @@ __device__ __forceinline__ int find_token(int piece, VerifyLds& lds, F weights4)
   return token;
 }
 
-// Whether this work-group is the last of `of` of a request to arrive; what the others wrote before is then visible.
+// Whether this work-group is the last of `of` of a request to arrive.  What the others' first threads stored before, by atomics of the
+// device's scope, is then there for loads of that scope.
 __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, uint32_t of, uint32_t* lds) {
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) *lds = atomicAdd(counter, 1u);
+  if (threadIdx.x == 0) *lds = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   const bool last = *lds == of - 1;
-  if (last) __threadfence();
+  __syncthreads();
   return last;
 }
 
@@ -416,16 +428,15 @@ __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
   const float t = temperature_of(a, b);
   if (threadIdx.x == 0) cut = nodes.n;
   __syncthreads();
-  for (int i = 1 + threadIdx.x; i < nodes.n; i += kVerifyThreads) {
-    const int row = nodes.start + i, x = a.tokens[row];
-    bool good = false;
-    if (x >= 0 && x < a.vocab) {
-      const Row r = row_alone(v, row - 1, t);
-      double p = 0.0;
-      if (r.at != INT_MAX) p = r.one ? (x == r.at ? 1.0 : 0.0) : weight(logit<F32>(a, row - 1, x), r.top, r.steep) / r.total;
-      good = random_of(a.accept_u, row) * (double)a.q[row * a.ldq + x] < p;
-    }
-    if (!good) atomicMin(&cut, i);
+  for (int i0 = 1; i0 < nodes.n; i0 += kVerifyThreads / 16) {
+    const int i = min(i0 + (int)(threadIdx.x >> 4), nodes.n - 1), row = nodes.start + i, x = a.tokens[row];
+    const bool token = x >= 0 && x < a.vocab;
+    const float z = token ? logit<F32>(a, row - 1, x) : 0.0f, qx = token ? a.q[row * a.ldq + x] : 0.0f;
+    const Row r = row_of_lanes(v, row - 1, t);
+    double p = 0.0;
+    if (r.at != INT_MAX) p = r.one ? (x == r.at ? 1.0 : 0.0) : weight(z, r.top, r.steep) / r.total;
+    const bool good = token && random_of(a.accept_u, row) * (double)qx < p;
+    if (!good && (threadIdx.x & 15) == 0) atomicMin(&cut, i);
   }
   __syncthreads();
   const int n = cut, row = nodes.start + n - 1;
