@@ -504,7 +504,7 @@ typedef struct w12_conv_args {
   int32_t silu;
   const void *x;                 /* [T][ldx]                                                 */
   int64_t ldx;
-  const uint16_t *weight;        /* BF16 [channels][width], 4-byte aligned                   */
+  const uint16_t *weight;        /* BF16 [channels][width], 16-byte aligned                  */
   const uint16_t *bias;          /* BF16 [channels] or NULL                                  */
   void *state;                   /* [slots][width - 1][channels], 16-byte aligned            */
   int64_t slot_stride, tap_stride;   /* elements, multiples of 16 bytes; tap_stride >= channels  */

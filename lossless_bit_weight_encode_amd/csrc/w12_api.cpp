@@ -603,7 +603,7 @@ int w12_short_conv(const w12_conv_args* a, const w12_sequences* s, hipStream_t s
   const int eb = a->dtype == W12_DTYPE_F32 ? 4 : 2;
   if ((rc = check_matrix(a->x, a->ldx, s->T, a->channels, eb, "x"))) return rc;
   if (!a->weight) return fail(W12_ERR_INVALID_ARG, "weight is NULL");
-  if (!aligned(a->weight, 4) || !aligned(a->bias, 2)) return fail(W12_ERR_MISALIGNED, "weight must be 4-byte, bias 2-byte aligned");
+  if (!aligned(a->weight, 16) || !aligned(a->bias, 2)) return fail(W12_ERR_MISALIGNED, "weight must be 16-byte, bias 2-byte aligned");
   if (a->tap_stride < a->channels)
     return fail(W12_ERR_INVALID_ARG, "tap stride %lld < %d channels", (long long)a->tap_stride, a->channels);
   if (a->tap_stride % (16 / eb))

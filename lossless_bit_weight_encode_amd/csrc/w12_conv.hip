@@ -14,83 +14,112 @@
 namespace w12 {
 
 constexpr int kConvThreads = 64;
-constexpr int kConvRows = 16;      // rows of a tile
+// Rows of a tile.  Short tiles make work for the chip of few rows, long ones read fewer rows twice.
+constexpr int kShortTile = 2, kLongTile = 16;
 
-template <bool F32, int W>
+// Weights of a thread's 8 channels.
+template <int W>
+__device__ __forceinline__ void load_weights(const w12_conv_args& a, int c, float w[8][W]) {
+  const uint16_t* p = a.weight + (int64_t)c * W;
+  if (c + 8 <= a.channels) {
+    float v[8 * W];
+#pragma unroll
+    for (int i = 0; i < W; ++i) unpack_bf16x8(reinterpret_cast<const uint4*>(p)[i], v + 8 * i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[e][j] = v[e * W + j];
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+#pragma unroll
+      for (int j = 0; j < W; ++j) w[e][j] = c + e < a.channels ? bf16_float(p[e * W + j]) : 0.0f;
+  }
+}
+
+template <bool F32, int W, int TILE>
 __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w12_sequences s) {
   constexpr int kPast = W - 1, kBytes = F32 ? 4 : 2;
   __shared__ int found[2];
   int b, tile;
   Range r;
-  if (!find_piece(s, blockIdx.x, kConvRows, found, b, r, tile)) return;
+  if (!find_piece(s, blockIdx.x, TILE, found, b, r, tile)) return;
   if (tile > 0 && !a.y) return;                      // only the first tile moves a state
   const int c = (blockIdx.y * kConvThreads + threadIdx.x) * 8;
   if (c >= a.channels) return;
   const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
-  // a token of the past: -1 is the newest
-  auto past = [&](int i, float v[8]) {
-    if (src < 0 || i < -kPast) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    } else {
-      load8<F32>(static_cast<const char*>(a.state) + (src * a.slot_stride + (kPast + i) * a.tap_stride) * kBytes, c, a.channels, v);
-    }
-  };
+  // a token of the sequence, or of its past: -1 is the newest; zeros where there is none
   auto token = [&](int i, float v[8]) {
-    const int row = i < 0 ? -1 : row_of(s, r.start + i);
+    const char* from = nullptr;
     if (i < 0) {
-      past(i, v);
-    } else if (row < 0) {
+      if (src >= 0 && i >= -kPast) from = static_cast<const char*>(a.state) + (src * a.slot_stride + (kPast + i) * a.tap_stride) * kBytes;
+    } else if (i < r.n) {
+      const int row = row_of(s, r.start + i);
+      if (row >= 0) from = static_cast<const char*>(a.x) + row * a.ldx * kBytes;
+    }
+    if (from) {
+      load8<F32>(from, c, a.channels, v);
+    } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    } else {
-      load8<F32>(static_cast<const char*>(a.x) + row * a.ldx * kBytes, c, a.channels, v);
     }
   };
   if (a.y) {
     float w[8][W], bias[8];
+    load_weights<W>(a, c, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) w[e][j] = c + e < a.channels ? bf16_float(a.weight[(int64_t)(c + e) * W + j]) : 0.0f;
-      bias[e] = a.bias && c + e < a.channels ? bf16_float(a.bias[c + e]) : 0.0f;
-    }
-    const int t0 = tile * kConvRows, t1 = min(t0 + kConvRows, r.n);
-    float x[W][8];
-    if (!s.tree_mask)
-#pragma unroll
-      for (int j = 1; j < W; ++j) token(t0 - W + j, x[j]);
-    for (int t = t0; t < t1; ++t) {
-      if (s.tree_mask) {
-        uint64_t before = ancestors(s, r.start, t);
-        int at = t, back = 0;                        // back: how far into the past
-#pragma unroll
-        for (int j = W - 1; j >= 0; --j) {
-          token(at, x[j]);
-          if (before) {
-            at = 63 - __builtin_clzll(before);
-            before &= ~((uint64_t)1 << at);
-          } else {
-            at = --back;
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < W - 1; ++j)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[j][e] = x[j + 1][e];
-        token(t, x[W - 1]);
-      }
+    for (int e = 0; e < 8; ++e) bias[e] = a.bias && c + e < a.channels ? bf16_float(a.bias[c + e]) : 0.0f;
+    // the output of token t from its window, oldest first
+    auto put = [&](int t, auto window) {
+      if (t >= r.n) return;
+      const int row = row_of(s, r.start + t);
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         y[e] = bias[e];
 #pragma unroll
-        for (int j = 0; j < W; ++j) y[e] += w[e][j] * x[j][e];
-        if (a.silu) y[e] = y[e] / (1.0f + __expf(-y[e]));
+        for (int j = 0; j < W; ++j) y[e] += w[e][j] * window(j)[e];
+        if (a.silu) y[e] *= __builtin_amdgcn_rcpf(1.0f + __expf(-y[e]));
       }
-      const int row = row_of(s, r.start + t);
       if (row >= 0) store8<false>(a.y + row * a.ldy, c, a.channels, y);
+    };
+    const int t0 = tile * TILE;
+    if (s.tree_mask) {
+      for (int t = t0; t < t0 + TILE; t += 2) {
+        float x[2][W][8];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint64_t before = t + k < r.n ? ancestors(s, r.start, t + k) : 0;
+          int at = t + k < r.n ? t + k : r.n, back = 0;        // back: how far into the past
+#pragma unroll
+          for (int j = W - 1; j >= 0; --j) {
+            token(at, x[k][j]);
+            if (before) {
+              at = 63 - __builtin_clzll(before);
+              before &= ~((uint64_t)1 << at);
+            } else {
+              at = --back;
+            }
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) put(t + k, [&](int j) { return x[k][j]; });
+      }
+    } else {
+      constexpr int kAtOnce = TILE < 4 ? TILE : 4;      // rows whose loads a thread has in flight
+      float x[kPast + kAtOnce][8];
+#pragma unroll
+      for (int j = 0; j < kPast; ++j) token(t0 - kPast + j, x[j]);
+      for (int t = t0; t < min(t0 + TILE, r.n); t += kAtOnce) {
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) token(t + k, x[kPast + k]);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) put(t + k, [&](int j) { return x[k + j]; });
+#pragma unroll
+        for (int j = 0; j < kPast; ++j)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[j][e] = x[j + kAtOnce][e];
+      }
     }
   }
   if (tile == 0 && dst >= 0) {
@@ -103,19 +132,22 @@ __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w1
   }
 }
 
-template <bool F32>
-static void conv_width(const w12_conv_args& a, const w12_sequences& s, dim3 grid, hipStream_t stream) {
-  switch (a.width) {
-    case 2: k_short_conv<F32, 2><<<grid, kConvThreads, 0, stream>>>(a, s); break;
-    case 3: k_short_conv<F32, 3><<<grid, kConvThreads, 0, stream>>>(a, s); break;
-    default: k_short_conv<F32, 4><<<grid, kConvThreads, 0, stream>>>(a, s); break;
-  }
+template <bool F32, int W>
+static void conv_tiles(const w12_conv_args& a, const w12_sequences& s, hipStream_t stream) {
+  const int64_t blocks = ceil_div(a.channels, 8 * kConvThreads);
+  const bool longer = !s.tree_mask && s.T / kLongTile * blocks >= 2 * 4 * device_cus();      // two waves a SIMD at least
+  const dim3 grid((unsigned)most_pieces(s.T, s.count, longer ? kLongTile : kShortTile), (unsigned)blocks);
+  if (longer) k_short_conv<F32, W, kLongTile><<<grid, kConvThreads, 0, stream>>>(a, s);
+  else k_short_conv<F32, W, kShortTile><<<grid, kConvThreads, 0, stream>>>(a, s);
 }
 
 hipError_t launch_short_conv(const w12_conv_args& a, const w12_sequences& s, hipStream_t stream) {
-  const dim3 grid((unsigned)most_pieces(s.T, s.count, kConvRows), (unsigned)ceil_div(a.channels, 8 * kConvThreads));
-  if (a.dtype == W12_DTYPE_F32) conv_width<true>(a, s, grid, stream);
-  else conv_width<false>(a, s, grid, stream);
+  const bool f32 = a.dtype == W12_DTYPE_F32;
+  switch (a.width) {
+    case 2: f32 ? conv_tiles<true, 2>(a, s, stream) : conv_tiles<false, 2>(a, s, stream); break;
+    case 3: f32 ? conv_tiles<true, 3>(a, s, stream) : conv_tiles<false, 3>(a, s, stream); break;
+    default: f32 ? conv_tiles<true, 4>(a, s, stream) : conv_tiles<false, 4>(a, s, stream); break;
+  }
   return hipGetLastError();
 }
 

@@ -125,9 +125,13 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
   }
 }
 
-// Tokens a sequence has, on average, from which they are taken 64 at a time.
-constexpr int kChunkFrom = 16;
-static bool in_chunks(const w12_sequences& s) { return s.tree_mask || (!s.lens && s.T >= (int64_t)kChunkFrom * s.count) || (s.lens && s.T > (int64_t)W12_TREE_NODES * s.count); }
+// Tokens a sequence has, on average, from which they are taken 64 at a time: between 8 (48 heads of 128, 1 / 4 / 16 / 64 sequences: 14 / 19 /
+// 42 / 144 us token by token, 16 / 25 / 56 / 200 in chunks) and 16 (25 / 31 / 67 / 226 and 16 / 25 / 57 / 205).  With lens the host does
+// not know how many count; accepted paths are far shorter than the trees that they lead through.
+constexpr int kChunkFrom = 12;
+static bool in_chunks(const w12_sequences& s) {
+  return s.tree_mask || s.T >= (int64_t)(s.lens ? W12_TREE_NODES + 1 : kChunkFrom) * s.count;
+}
 
 uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) {
   return delta_chunk_workspace_bytes(T, count, v_heads);

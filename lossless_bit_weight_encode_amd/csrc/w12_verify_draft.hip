@@ -11,6 +11,7 @@
 #include <limits.h>
 
 #include "w12_gemm_common.h"
+#include "w12_lanes.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"
 
@@ -18,9 +19,11 @@ namespace w12 {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / 64;
-constexpr int kVerifyRounds = 4;                               // of 256 neighbouring values, for each wave
-constexpr int kVerifyValues = 4 * kVerifyRounds;               // of a thread
-constexpr int kVerifyPiece = kVerifyThreads * kVerifyValues;   // values of a piece
+// Values of a piece: for each wave so many rounds of 256 neighbours.  Few rows take short pieces, which fill the chip (17 rows of 50257:
+// 19 us, with 4 rounds 24; 63 of 131072: 25 and 27), many rows longer ones, with less to do around them (266 of 131072: 65 and 60 us).
+constexpr int kShortRounds = 2, kLongRounds = 4;
+constexpr int64_t kLongFrom = 4096;                            // long pieces of a call, two rounds of the chip
+constexpr int piece_values(int rounds) { return kVerifyThreads * 4 * rounds; }
 
 // A piece's maximum, where it is first met, and the sum of its weights relative to it.
 struct Piece {
@@ -48,15 +51,16 @@ __device__ __forceinline__ Nodes nodes_of(const w12_verify_draft_args& a, int b,
   if (!all) r.n = min(r.n, W12_VERIFY_NODES);
   return r;
 }
-// The last request that starts at or before a row.
+// The last request that starts at or before a row: a wave looks at 64 of them at once.
 __device__ __forceinline__ int request_of_row(const w12_verify_draft_args& a, int row) {
-  int lo = 0, hi = a.requests;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.node_ptr[mid] <= row) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 63;
+  int b = 0;
+  for (int i = 1; i < a.requests; i += 64) {
+    const uint64_t at = __ballot(i + lane < a.requests && a.node_ptr[i + lane] <= row);
+    b += __builtin_popcountll(at);
+    if (at != ~(uint64_t)0) break;
   }
-  return lo;
+  return b;
 }
 __device__ __forceinline__ float temperature_of(const w12_verify_draft_args& a, int b) {
   const float t = a.temperature ? a.temperature[b] : 1.0f;
@@ -115,15 +119,11 @@ __device__ __forceinline__ double weight(float z, float top, double steep) { ret
 
 // A wave's, and a work-group's, sums, and what was before each thread.
 __device__ __forceinline__ double scan_wave(double v, double& before) {
-  const int lane = threadIdx.x & 63;
-  double s = v;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const double u = __shfl_up(s, o);
-    if (lane >= o) s += u;
-  }
+  const double s = sum_up(v);
   before = s - v;
-  return __shfl(s, 63);
+  const uint64_t u = __builtin_bit_cast(uint64_t, s);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), 63) << 32 |
+                                        (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, 63));
 }
 __device__ __forceinline__ double scan_group(double v, double* lds, double& before) {
   const int w = threadIdx.x >> 6;
@@ -233,8 +233,9 @@ __device__ __forceinline__ void pass_to(double target, double mine, double befor
 }
 
 // Where a thread's values of a piece are: 4 neighbours, every 256.
+template <int R>
 __device__ __forceinline__ int place_of(int piece, int round) {
-  return piece * kVerifyPiece + (int)(threadIdx.x >> 6) * (256 * kVerifyRounds) + round * 256 + (int)(threadIdx.x & 63) * 4;
+  return piece * piece_values(R) + (int)(threadIdx.x >> 6) * (256 * R) + round * 256 + (int)(threadIdx.x & 63) * 4;
 }
 // Four neighbouring logits, -inf past the end.
 template <bool F32>
@@ -257,12 +258,12 @@ __device__ __forceinline__ void logits4(const w12_verify_draft_args& a, int64_t 
 }
 
 // The token of a piece in whose weights the running sum passes lds.target; weights4(i, w) gives those of places i .. i + 3.  By a whole work-group.
-template <typename F>
+template <int R, typename F>
 __device__ __forceinline__ int find_token(int piece, VerifyLds& lds, F weights4) {
-  double w[kVerifyRounds][4], round[kVerifyRounds], sum = 0.0, before, unused;
+  double w[R][4], round[R], sum = 0.0, before, unused;
 #pragma unroll
-  for (int j = 0; j < kVerifyRounds; ++j) {
-    weights4(place_of(piece, j), w[j]);
+  for (int j = 0; j < R; ++j) {
+    weights4(place_of<R>(piece, j), w[j]);
     round[j] = w[j][0] + w[j][1] + w[j][2] + w[j][3];
     sum += round[j];
   }
@@ -276,15 +277,15 @@ __device__ __forceinline__ int find_token(int piece, VerifyLds& lds, F weights4)
   // every wave goes through its values; the first place that passes is the token
   int first = INT_MAX, last = -1;
 #pragma unroll
-  for (int j = 0; j < kVerifyRounds; ++j) {
+  for (int j = 0; j < R; ++j) {
     const double all = scan_wave(round[j], before);
     double at = run + before;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       at += w[j][e];
       if (w[j][e] > 0.0) {
-        if (at > target) first = min(first, place_of(piece, j) + e);
-        last = place_of(piece, j) + e;
+        if (at > target) first = min(first, place_of<R>(piece, j) + e);
+        last = place_of<R>(piece, j) + e;
       }
     }
     run += all;
@@ -315,14 +316,14 @@ __device__ __forceinline__ bool last_to_arrive(uint32_t* counter, uint32_t of, u
   return last;
 }
 
-template <bool F32>
+template <bool F32, int R>
 __global__ __launch_bounds__(kVerifyThreads) void k_pieces(Verify v) {
   const w12_verify_draft_args& a = v.a;
   __shared__ VerifyLds lds;
   const int piece = blockIdx.y, row = blockIdx.x;
-  float z[kVerifyRounds][4];
+  float z[R][4];
 #pragma unroll
-  for (int j = 0; j < kVerifyRounds; ++j) logits4<F32>(a, row, place_of(piece, j), z[j]);
+  for (int j = 0; j < R; ++j) logits4<F32>(a, row, place_of<R>(piece, j), z[j]);
   if (row == 0 && piece == 0)
     for (int i = threadIdx.x; i < a.requests; i += kVerifyThreads) {
       v.arrived[i] = 0;
@@ -332,16 +333,16 @@ __global__ __launch_bounds__(kVerifyThreads) void k_pieces(Verify v) {
   float top = -INFINITY;
   int at = INT_MAX;
 #pragma unroll
-  for (int j = 0; j < kVerifyRounds; ++j)
+  for (int j = 0; j < R; ++j)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (z[j][e] > top) top = z[j][e], at = place_of(piece, j) + e;
+      if (z[j][e] > top) top = z[j][e], at = place_of<R>(piece, j) + e;
   largest(top, at, lds.f, lds.i);
   double sum = 0.0, before;
   if (t > 0.0f && at != INT_MAX && top != INFINITY) {
     const double steep = steepness(t);
 #pragma unroll
-    for (int j = 0; j < kVerifyRounds; ++j)
+    for (int j = 0; j < R; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum += weight(z[j][e], top, steep);
   }
@@ -350,7 +351,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_pieces(Verify v) {
 }
 
 // The token that u takes from a row, by a whole work-group.
-template <bool F32>
+template <bool F32, int R>
 __device__ __forceinline__ int take(const Verify& v, int row, float t, VerifyLds& lds) {
   const w12_verify_draft_args& a = v.a;
   double mine, before;
@@ -372,7 +373,7 @@ __device__ __forceinline__ int take(const Verify& v, int row, float t, VerifyLds
     lds.target = target - start;
   });
   const int piece = (int)lds.place;
-  return find_token(piece, lds, [&](int i, double w[4]) {
+  return find_token<R>(piece, lds, [&](int i, double w[4]) {
     float z[4];
     logits4<F32>(a, row, i, z);
 #pragma unroll
@@ -381,7 +382,7 @@ __device__ __forceinline__ int take(const Verify& v, int row, float t, VerifyLds
 }
 
 // The token of every row, and the walk.
-template <bool F32>
+template <bool F32, int R>
 __global__ __launch_bounds__(kVerifyThreads) void k_take(Verify v) {
   const w12_verify_draft_args& a = v.a;
   __shared__ VerifyLds lds;
@@ -389,7 +390,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_take(Verify v) {
   const int row = blockIdx.x, b = request_of_row(a, row);
   const Nodes nodes = nodes_of(a, b);
   if (row < nodes.start || row >= nodes.start + nodes.n) return;
-  const int token = take<F32>(v, row, temperature_of(a, b), lds);
+  const int token = take<F32, R>(v, row, temperature_of(a, b), lds);
   if (threadIdx.x == 0) __hip_atomic_store(&v.taken[row], token, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (!last_to_arrive(&v.arrived[b], (uint32_t)nodes.n, &lds.place)) return;
   for (int i = threadIdx.x; i < nodes.n; i += kVerifyThreads) child[i] = INT_MAX;
@@ -417,7 +418,7 @@ __global__ __launch_bounds__(kVerifyThreads) void k_take(Verify v) {
 }
 
 // A chain with the drafter's probabilities: acceptances, and the token after the cut.
-template <bool F32>
+template <bool F32, int R>
 __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
   const w12_verify_draft_args& a = v.a;
   __shared__ VerifyLds lds;
@@ -462,8 +463,8 @@ __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
   };
   double sum = 0.0, w[4];
 #pragma unroll
-  for (int j = 0; j < kVerifyRounds; ++j) {
-    rest4(place_of(piece, j), w);
+  for (int j = 0; j < R; ++j) {
+    rest4(place_of<R>(piece, j), w);
     sum += w[0] + w[1] + w[2] + w[3];
   }
   sum = scan_group(sum, lds.d, before);
@@ -490,9 +491,9 @@ __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
       lds.target = target - start;
     });
     const int in = (int)lds.place;
-    token = find_token(in, lds, rest4);
+    token = find_token<R>(in, lds, rest4);
   } else {
-    token = take<F32>(v, row, t, lds);      // nothing is left over: from p itself
+    token = take<F32, R>(v, row, t, lds);      // nothing is left over: from p itself
   }
   if (threadIdx.x == 0) a.count[b] = n, a.next_token[b] = token;
   const int all = nodes_of(a, b, true).n;
@@ -502,14 +503,22 @@ __global__ __launch_bounds__(kVerifyThreads) void k_chain(Verify v) {
 static uint64_t round16(uint64_t x) { return (x + 15) / 16 * 16; }
 
 uint64_t verify_draft_workspace_bytes(int32_t T, int32_t requests, int32_t vocab) {
-  const uint64_t count = ceil_div(vocab, kVerifyPiece);
+  const uint64_t count = ceil_div(vocab, piece_values(kShortRounds));
   return T * count * sizeof(Piece) + round16(requests * count * 8) + round16((uint64_t)T * 4) + round16((uint64_t)requests * 4);
 }
 
+template <bool F32, int R>
+static void verify_launches(const Verify& v, hipStream_t stream) {
+  k_pieces<F32, R><<<dim3((unsigned)v.a.T, (unsigned)v.count), kVerifyThreads, 0, stream>>>(v);
+  if (v.a.q) k_chain<F32, R><<<dim3((unsigned)v.count, (unsigned)v.a.requests), kVerifyThreads, 0, stream>>>(v);
+  else k_take<F32, R><<<(unsigned)v.a.T, kVerifyThreads, 0, stream>>>(v);
+}
+
 hipError_t launch_verify_draft(const w12_verify_draft_args& a, void* ws, hipStream_t stream) {
+  const bool longer = a.T * ceil_div(a.vocab, piece_values(kLongRounds)) >= kLongFrom;
   Verify v;
   v.a = a;
-  v.count = (int)ceil_div(a.vocab, kVerifyPiece);
+  v.count = (int)ceil_div(a.vocab, piece_values(longer ? kLongRounds : kShortRounds));
   char* at = static_cast<char*>(ws);
   v.pieces = reinterpret_cast<Piece*>(at);
   at += (uint64_t)a.T * v.count * sizeof(Piece);
@@ -518,18 +527,8 @@ hipError_t launch_verify_draft(const w12_verify_draft_args& a, void* ws, hipStre
   v.taken = reinterpret_cast<int32_t*>(at);
   at += round16((uint64_t)a.T * 4);
   v.arrived = reinterpret_cast<uint32_t*>(at);
-  const bool f32 = a.logits_dtype == W12_DTYPE_F32;
-  const dim3 grid((unsigned)a.T, (unsigned)v.count);
-  if (f32) k_pieces<true><<<grid, kVerifyThreads, 0, stream>>>(v);
-  else k_pieces<false><<<grid, kVerifyThreads, 0, stream>>>(v);
-  const dim3 chains((unsigned)v.count, (unsigned)a.requests);
-  if (a.q) {
-    if (f32) k_chain<true><<<chains, kVerifyThreads, 0, stream>>>(v);
-    else k_chain<false><<<chains, kVerifyThreads, 0, stream>>>(v);
-  } else {
-    if (f32) k_take<true><<<(unsigned)a.T, kVerifyThreads, 0, stream>>>(v);
-    else k_take<false><<<(unsigned)a.T, kVerifyThreads, 0, stream>>>(v);
-  }
+  if (a.logits_dtype == W12_DTYPE_F32) longer ? verify_launches<true, kLongRounds>(v, stream) : verify_launches<true, kShortRounds>(v, stream);
+  else longer ? verify_launches<false, kLongRounds>(v, stream) : verify_launches<false, kShortRounds>(v, stream);
   return hipGetLastError();
 }
 
