@@ -91,8 +91,8 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   };
   __shared__ __attribute__((aligned(16))) Shared lds;
   __shared__ f32x4v ablk[10][64];                // A's blocks (r, s), r >= s: a lane's column, rows 4 g .. + 3
-  __shared__ __attribute__((aligned(16))) float rk[kChunk], rq[kChunk], beta[kChunk], gh[kChunk], gl[kChunk];
-  __shared__ uint64_t anc[kChunk];
+  __shared__ __attribute__((aligned(16))) float rk[kChunk], rq[kChunk], beta[kChunk], br[kChunk], gh[kChunk], gl[kChunk];
+  __shared__ __attribute__((aligned(16))) uint32_t anc[2][kChunk];      // lower and upper halves
   __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
   const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
@@ -138,14 +138,14 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   };
   const bool diagonal = g4 == c16 >> 2;
   const float kk = square(kt);
-  const float ik = krow < 0 ? 0.0f : a.l2norm ? 1.0f / sqrtf(kk + a.eps) : 1.0f;
+  const float ik = krow < 0 ? 0.0f : a.l2norm ? __builtin_amdgcn_rsqf(kk + a.eps) : 1.0f;
   if (diagonal) rk[16 * w + c16] = finite(kk) && finite(ik) ? ik : NAN;
   if (a.q) {
     const float qq = square(qt[0]);
-    if (diagonal && w < 3) rq[16 * q0 + c16] = qrow < 0 ? 0.0f : a.scale * (a.l2norm ? 1.0f / sqrtf(qq + a.eps) : 1.0f);
+    if (diagonal && w < 3) rq[16 * q0 + c16] = qrow < 0 ? 0.0f : a.scale * (a.l2norm ? __builtin_amdgcn_rsqf(qq + a.eps) : 1.0f);
     if (w == 0) {
       const float qq1 = square(qt[1]);
-      if (diagonal) rq[16 + c16] = qrow1 < 0 ? 0.0f : a.scale * (a.l2norm ? 1.0f / sqrtf(qq1 + a.eps) : 1.0f);
+      if (diagonal) rq[16 + c16] = qrow1 < 0 ? 0.0f : a.scale * (a.l2norm ? __builtin_amdgcn_rsqf(qq1 + a.eps) : 1.0f);
     }
   }
   __syncthreads();
@@ -174,7 +174,10 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
     gh[lane] = hi;
     gl[lane] = (float)(gsum - hi);
     beta[lane] = bad ? 0.0f : bv;
-    anc[lane] = bad ? 0 : path & ~bads;
+    br[lane] = bad ? 0.0f : bv * ikl;
+    const uint64_t mine = bad ? 0 : path & ~bads;
+    anc[0][lane] = (uint32_t)mine;
+    anc[1][lane] = (uint32_t)(mine >> 32);
   } else if (w == 1) {
     const float grown = __builtin_amdgcn_exp2f((float)gsum);
     float* rows = out.rows();
@@ -207,17 +210,28 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
         kk = mma(rows_operand<DK>(lds.k, rt, ks), x, kk);
         if (a.q) kq = mma(x, w == 0 && j ? qt[1][ks] : qt[0][ks], kq);
       }
-      const int col = 16 * t + c16, prow = 16 * rt + c16;
-      const float hc = gh[col], lc = gl[col], rc = rk[col], hp = gh[prow], lp = gl[prow], rp = rq[prow];
-      const uint64_t sees = (anc[prow] | (uint64_t)1 << prow) & ~bads;
+      // A: column 16 t + c16, rows 16 rt + 4 g4 ..; P: row 16 rt + c16, columns 16 t + 4 g4 ..
+      const int half = t >> 1, bit = 16 * (t & 1), arow = 16 * rt + 4 * g4, acol = 16 * t + c16, prow = 16 * rt + c16, pcol = 16 * t + 4 * g4;
+      const auto at4 = [](const float* p) { return *reinterpret_cast<const f32x4v*>(p); };
+      const f32x4v ha = at4(gh + arow), la = at4(gl + arow), ba = at4(br + arow);
+      const u32x4v ma = *reinterpret_cast<const u32x4v*>(anc[half] + arow);
+      const float hc = gh[acol], lc = gl[acol], rc = rk[acol];
       f32x4v ab;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 16 * rt + 4 * g4 + i, pcol = 16 * t + 4 * g4 + i;
-        const float e = __builtin_amdgcn_exp2f((gh[row] - hc) + (gl[row] - lc));
-        ab[i] = anc[row] >> col & 1 ? beta[row] * rk[row] * rc * e * kk[i] : 0.0f;
-        const float f = __builtin_amdgcn_exp2f((hp - gh[pcol]) + (lp - gl[pcol]));
-        pt[n][i] = sees >> pcol & 1 ? rp * rk[pcol] * f * kq[i] : 0.0f;
+        const float e = __builtin_amdgcn_exp2f((ha[i] - hc) + (la[i] - lc));
+        ab[i] = ma[i] >> (bit + c16) & 1 ? ba[i] * rc * e * kk[i] : 0.0f;
+      }
+      if (a.q) {
+        const f32x4v hp = at4(gh + pcol), lp = at4(gl + pcol), rp = at4(rk + pcol);
+        const float hr = gh[prow], lr = gl[prow], rr = rq[prow];
+        const uint32_t self = prow >> 5 == half ? 1u << (prow & 31) : 0u;
+        const uint32_t sees = (anc[half][prow] | self) & ~(uint32_t)(bads >> 32 * half);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = __builtin_amdgcn_exp2f((hr - hp[i]) + (lr - lp[i]));
+          pt[n][i] = sees >> (bit + 4 * g4 + i) & 1 ? rr * rp[i] * f * kq[i] : 0.0f;
+        }
       }
       ablk[block_of(rt, t)][lane] = ab;
     }
