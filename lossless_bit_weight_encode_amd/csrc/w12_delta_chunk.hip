@@ -42,6 +42,16 @@ __device__ __forceinline__ f32x4v mma_block(f32x4v a, f32x4v b, f32x4v c) {
 
 __device__ __forceinline__ bool finite(float v) { return fabsf(v) < INFINITY; }
 
+// v where bit b of m is set, else 0; one of four.  By bits: choices between values become branches here.
+__device__ __forceinline__ float where_bit(uint32_t m, int b, float v) {
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, v) & (uint32_t)__builtin_amdgcn_sbfe((int)m, b, 1));
+}
+__device__ __forceinline__ float pick(int i, float a, float b, float c, float d) {
+  const uint32_t m = 1u << i;
+  return __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, where_bit(m, 0, a)) | __builtin_bit_cast(uint32_t, where_bit(m, 1, b)) |
+                                       __builtin_bit_cast(uint32_t, where_bit(m, 2, c)) | __builtin_bit_cast(uint32_t, where_bit(m, 3, d)));
+}
+
 // Eight FP32 values as BF16, and what that leaves over as BF16.
 __device__ __forceinline__ bf8 high(f32x4v a, f32x4v b) {
   const u32x4v r = {bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(b[0], b[1]), bf16_pair(b[2], b[3])};
@@ -128,13 +138,13 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   const uint64_t path = lane < m ? ancestors(s, r.start + first, lane) : 0;
 #pragma unroll
   for (int ks = 0; ks < KS; ++ks) *reinterpret_cast<bf8*>(lds.k + piece_at<DK>(16 * w + c16, 4 * ks + g4)) = kt[ks];
+  // (the barriers from here on are for LDS alone: stores to memory take their time beside them)
   // squares of the norms: the diagonal of a tile with itself, which lanes of 4 g + i = c16 hold
   auto square = [&](const bf8 x[KS]) {
     f32x4v t = {0, 0, 0, 0};
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) t = mma(x[ks], x[ks], t);
-    const int i = c16 & 3;
-    return i == 0 ? t[0] : i == 1 ? t[1] : i == 2 ? t[2] : t[3];
+    return pick(c16 & 3, t[0], t[1], t[2], t[3]);
   };
   const bool diagonal = g4 == c16 >> 2;
   const float kk = square(kt);
@@ -148,7 +158,7 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
       if (diagonal) rq[16 + c16] = qrow1 < 0 ? 0.0f : a.scale * (a.l2norm ? __builtin_amdgcn_rsqf(qq1 + a.eps) : 1.0f);
     }
   }
-  __syncthreads();
+  lds_barrier();
   // A row whose key, decay or strength is no number is left out here, and made up for where the results are stored.  -inf is a number for
   // a decay: like anything below -1e4 it clears the state.
   const float ikl = rk[lane];
@@ -158,7 +168,7 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   double gsum;
   if (s.tree_mask) {
     if (w == 0) *reinterpret_cast<double*>(&ablk[0][lane]) = g1;
-    __syncthreads();
+    lds_barrier();
     gsum = g1;
     for (uint64_t p = path; p; p &= p - 1) gsum += *reinterpret_cast<const double*>(&ablk[0][__builtin_ctzll(p)]);
   } else {
@@ -190,54 +200,48 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   } else if (w == 2 && a.q) {
     out.out_rows()[lane] = __builtin_amdgcn_exp2f((float)gsum) * rq[lane];
   }
-  __syncthreads();
-  // This wave's fragments of P (rt, ks): (0, 0) and (1, 0), (2, 0) and (2, 1), (3, 0), (3, 1), 2 or 3 tiles each; and the same tiles
-  // of A.  A: a lane's column, 4 neighbouring rows; P turned: a lane's row, 4 neighbouring columns.
+  lds_barrier();
+  // This wave's fragments of P (rt, ks): (0, 0) and (1, 0), (2, 0) and (2, 1), (3, 0), (3, 1), tile by tile; and the same tiles of A.
+  // A: a lane's column, 4 neighbouring rows; P turned: a lane's row, 4 neighbouring columns.  A loop: where work-groups are few, a kernel
+  // that runs through its code once waits for the code.
+#pragma unroll 1
+  for (int j = 0; j < (w < 2 ? 4 : 2); ++j) {
+    const int rt = w == 0 ? j >> 1 : w == 1 ? 2 : 3, t = w == 0 ? j & 1 : w == 3 ? 2 + j : j, half = t >> 1;
+    if (w == 0 && j == 2) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int rt = w == 0 ? j : w == 1 ? 2 : 3, ks0 = w == 1 ? j : w == 3 ? 1 : 0;
-    if (w >= 2 && j) continue;
-    f32x4v pt[2];
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int t = 2 * ks0 + n;
-      pt[n] = f32x4v{0, 0, 0, 0};
-      if (t > rt) continue;
+      for (int ks = 0; ks < KS; ++ks) qt[0][ks] = qt[1][ks];
+    }
+    f32x4v pt = {0, 0, 0, 0};
+    if (t <= rt) {
       f32x4v kk = {0, 0, 0, 0}, kq = kk;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         const bf8 x = rows_operand<DK>(lds.k, t, ks);
         kk = mma(rows_operand<DK>(lds.k, rt, ks), x, kk);
-        if (a.q) kq = mma(x, w == 0 && j ? qt[1][ks] : qt[0][ks], kq);
+        kq = mma(x, qt[0][ks], kq);
       }
       // A: column 16 t + c16, rows 16 rt + 4 g4 ..; P: row 16 rt + c16, columns 16 t + 4 g4 ..
-      const int half = t >> 1, bit = 16 * (t & 1), arow = 16 * rt + 4 * g4, acol = 16 * t + c16, prow = 16 * rt + c16, pcol = 16 * t + 4 * g4;
+      const int bit = 16 * (t & 1), arow = 16 * rt + 4 * g4, acol = 16 * t + c16, prow = 16 * rt + c16, pcol = 16 * t + 4 * g4;
       const auto at4 = [](const float* p) { return *reinterpret_cast<const f32x4v*>(p); };
-      const f32x4v ha = at4(gh + arow), la = at4(gl + arow), ba = at4(br + arow);
+      const f32x4v ha = at4(gh + arow), la = at4(gl + arow), ba = at4(br + arow), hp = at4(gh + pcol), lp = at4(gl + pcol), rp = at4(rk + pcol);
       const u32x4v ma = *reinterpret_cast<const u32x4v*>(anc[half] + arow);
-      const float hc = gh[acol], lc = gl[acol], rc = rk[acol];
+      const float hc = gh[acol], lc = gl[acol], rc = rk[acol], hr = gh[prow], lr = gl[prow], rr = rq[prow];
+      const uint32_t self = prow >> 5 == half ? 1u << (prow & 31) : 0u;
+      const uint32_t sees = (anc[half][prow] | self) & ~(uint32_t)(bads >> 32 * half);
       f32x4v ab;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float e = __builtin_amdgcn_exp2f((ha[i] - hc) + (la[i] - lc));
-        ab[i] = ma[i] >> (bit + c16) & 1 ? ba[i] * rc * e * kk[i] : 0.0f;
-      }
-      if (a.q) {
-        const f32x4v hp = at4(gh + pcol), lp = at4(gl + pcol), rp = at4(rk + pcol);
-        const float hr = gh[prow], lr = gl[prow], rr = rq[prow];
-        const uint32_t self = prow >> 5 == half ? 1u << (prow & 31) : 0u;
-        const uint32_t sees = (anc[half][prow] | self) & ~(uint32_t)(bads >> 32 * half);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float f = __builtin_amdgcn_exp2f((hr - hp[i]) + (lr - lp[i]));
-          pt[n][i] = sees >> (bit + 4 * g4 + i) & 1 ? rr * rp[i] * f * kq[i] : 0.0f;
-        }
+        ab[i] = where_bit(ma[i], bit + c16, ba[i] * rc * e * kk[i]);
+        const float f = __builtin_amdgcn_exp2f((hr - hp[i]) + (lr - lp[i]));
+        pt[i] = where_bit(sees, bit + 4 * g4 + i, rr * rp[i] * f * kq[i]);
       }
       ablk[block_of(rt, t)][lane] = ab;
     }
-    if (a.q) out.p(fragment_of(rt, ks0))[lane] = high(pt[0], pt[1]);
+    if (a.q)
+      reinterpret_cast<uint2*>(out.p(fragment_of(rt, half)) + lane)[t & 1] = make_uint2(bf16_pair(pt[0], pt[1]), bf16_pair(pt[2], pt[3]));
   }
-  __syncthreads();
+  lds_barrier();
   // the inverse of diagonal block w: a lane's column by substitution (the four groups of lanes do the same)
   float d[16];
   {
@@ -256,11 +260,11 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   }
   f32x4v mine;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) mine[i] = g4 == 0 ? d[i] : g4 == 1 ? d[4 + i] : g4 == 2 ? d[8 + i] : d[12 + i];
+  for (int i = 0; i < 4; ++i) mine[i] = pick(g4, d[i], d[4 + i], d[8 + i], d[12 + i]);
   lds.inverse.d[w][lane] = mine;
 #pragma unroll
   for (int i = 0; i < 4; ++i) lds.inverse.turn[w][4 * g4 + i][c16] = mine[i];
-  __syncthreads();
+  lds_barrier();
   // block row w of T, turned: X_w = D_w^T, X_t = -D_t^T sum_{t < u <= w} A_ut^T X_u
   f32x4v x[4];
 #pragma unroll
