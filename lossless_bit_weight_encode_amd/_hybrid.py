@@ -141,9 +141,11 @@ def gated_delta(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, g: tor
     if outputs:
         ld_q = _rows(q, "q", (t, kw), (_BF16,), 8)
         ld_o = _rows(out, "out", (t, h * dv), (_BF16,), 8)
-    if slots and not state[0].is_contiguous():
+    slot, head, column, one = state.stride()
+    if one != 1 or column != dk or (head != dv * dk and h > 1):
         raise ValueError("state: a slot's values must be contiguous")
-    slot = state.stride(0) if slots > 1 else h * dv * dk
+    if slots == 1:
+        slot = h * dv * dk                        # a single slot is never stepped
     s = _sequences(t, slots, seq_ptr, src, dst, tree_mask, lens, rows)
     a = _DeltaArgs(hk, h, dk, dv, int(l2norm), eps, dk ** -0.5 if scale is None else scale, 0, _ptr(q), ld_q,
                    k.data_ptr(), ld_k, v.data_ptr(), ld_v, g.data_ptr(), ld_g, beta.data_ptr(), ld_b, state.data_ptr(), slot,
