@@ -5,7 +5,8 @@
 // A work-group takes a tile of rows of one sequence and 8 neighbouring channels a thread.  In a sequence a thread
 // walks down its rows with the window in registers, so that every value is read once but for a tile's first W - 1; in
 // a tree each row gathers its window along its path (neighbouring rows share most of it, from the cache).
-// The first tile alone reads the state, and writes the new one after it: in place, no other work-group sees either.
+// A sequence's first tile alone reads the state (no tile is shorter than a window's past), and writes the new one after it: in place,
+// no other work-group sees either.
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"
@@ -15,7 +16,7 @@ namespace w12 {
 
 constexpr int kConvThreads = 64;
 // Rows of a tile.  Short tiles make work for the chip of few rows, long ones read fewer rows twice.
-constexpr int kShortTile = 2, kLongTile = 16;
+constexpr int kTreeTile = 2, kShortTile = 4, kLongTile = 16;
 
 // Weights of a thread's 8 channels.
 template <int W>
@@ -37,9 +38,10 @@ __device__ __forceinline__ void load_weights(const w12_conv_args& a, int c, floa
   }
 }
 
-template <bool F32, int W, int TILE>
+template <bool F32, int W, bool TREE, int TILE>
 __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w12_sequences s) {
   constexpr int kPast = W - 1, kBytes = F32 ? 4 : 2;
+  static_assert(TREE || TILE >= kPast, "the second tile would read the state that the first one replaces");
   __shared__ int found[2];
   int b, tile;
   Range r;
@@ -84,7 +86,7 @@ __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w1
       if (row >= 0) store8<false>(a.y + row * a.ldy, c, a.channels, y);
     };
     const int t0 = tile * TILE;
-    if (s.tree_mask) {
+    if constexpr (TREE) {
       for (int t = t0; t < t0 + TILE; t += 2) {
         float x[2][W][8];
 #pragma unroll
@@ -106,7 +108,7 @@ __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w1
         for (int k = 0; k < 2; ++k) put(t + k, [&](int j) { return x[k][j]; });
       }
     } else {
-      constexpr int kAtOnce = TILE < 4 ? TILE : 4;      // rows whose loads a thread has in flight
+      constexpr int kAtOnce = 4;      // rows whose loads a thread has in flight
       float x[kPast + kAtOnce][8];
 #pragma unroll
       for (int j = 0; j < kPast; ++j) token(t0 - kPast + j, x[j]);
@@ -136,9 +138,11 @@ template <bool F32, int W>
 static void conv_tiles(const w12_conv_args& a, const w12_sequences& s, hipStream_t stream) {
   const int64_t blocks = ceil_div(a.channels, 8 * kConvThreads);
   const bool longer = !s.tree_mask && s.T / kLongTile * blocks >= 2 * 4 * device_cus();      // two waves a SIMD at least
-  const dim3 grid((unsigned)most_pieces(s.T, s.count, longer ? kLongTile : kShortTile), (unsigned)blocks);
-  if (longer) k_short_conv<F32, W, kLongTile><<<grid, kConvThreads, 0, stream>>>(a, s);
-  else k_short_conv<F32, W, kShortTile><<<grid, kConvThreads, 0, stream>>>(a, s);
+  const int tile = s.tree_mask ? kTreeTile : longer ? kLongTile : kShortTile;
+  const dim3 grid((unsigned)most_pieces(s.T, s.count, tile), (unsigned)blocks);
+  if (s.tree_mask) k_short_conv<F32, W, true, kTreeTile><<<grid, kConvThreads, 0, stream>>>(a, s);
+  else if (longer) k_short_conv<F32, W, false, kLongTile><<<grid, kConvThreads, 0, stream>>>(a, s);
+  else k_short_conv<F32, W, false, kShortTile><<<grid, kConvThreads, 0, stream>>>(a, s);
 }
 
 hipError_t launch_short_conv(const w12_conv_args& a, const w12_sequences& s, hipStream_t stream) {

@@ -231,3 +231,22 @@ def test_a_step_of_speculative_decoding():
         st = state[i].cuda().clone()[None]
         o = w12.gated_delta(*split(y), gd, bd, st, ints([0, len(rows)]), ints([0]), rows=ints(rows + [-1] * (t - len(rows))))
         assert (o[rows].float() - out[rows].float()).abs().max() <= 0.05 * out[rows].float().abs().max()
+
+
+@pytest.mark.parametrize("width", [2, 3, 4])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_conv_in_place_equals_out_of_place(width, dtype):
+    """A state that is replaced where it stands is read by nobody after: sequences of all lengths about a tile's, at many channels."""
+    lengths = [1, 2, 3, 4, 5, 6, 7, 8, 9, 17] * 12
+    t, b, c = sum(lengths), len(lengths), 2056
+    x = rnd(1, t, c).to(dtype).cuda()
+    weight = rnd(2, c, width).to(BF).cuda()
+    past = torch.zeros(2 * b, width - 1, c, dtype=dtype, device="cuda")
+    past[:b] = rnd(3, b, width - 1, c).to(dtype).cuda()
+    ptr, here, there = ints(starts(lengths)), ints(list(range(b))), ints(list(range(b, 2 * b)))
+    want = w12.short_conv(x, weight, past, ptr, here, dst=there)
+    for _ in range(3):
+        state = past[:b].clone()
+        got = w12.short_conv(x, weight, state, ptr, here, dst=here)
+        assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+        assert torch.equal(state, past[b:])
