@@ -528,8 +528,11 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * q and out NULL: only the states move on.  The result is bitwise the same from run to run.
  * dk: 64 or 128, dv: 64, 128 or 256, v_heads a multiple of k_heads, at most 1024.
  * ws: w12_gated_delta_workspace_size bytes for T rows in count sequences (or more), 16-byte aligned, any content; calls
- * that overlap in time need workspaces of their own.
+ * that overlap in time need workspaces of their own.  Only tokens taken 64 at a time need it: those of a tree, and of a call with
+ * T >= W12_DELTA_CHUNK_FROM * count rows (with lens: W12_DELTA_CHUNK_FROM_LENS * count); else ws may be NULL.
  */
+#define W12_DELTA_CHUNK_FROM 12
+#define W12_DELTA_CHUNK_FROM_LENS 65
 typedef struct w12_delta_args {
   int32_t k_heads, v_heads, dk, dv;
   int32_t l2norm;
@@ -569,7 +572,7 @@ int w12_gated_delta(const w12_delta_args *a, const w12_sequences *s, void *ws, u
  * last row; count[b] their number, next_token[b] the token that follows.  path and count serve as rows and lens of w12_sequences.
  * Weights, sums and comparisons are FP64.  Logits of -inf and NaN have no weight; where one or more are
  * +inf, the first of them has all of it; a row without any weight takes no token (-1), and no child follows it.  A token outside
- * 0 .. vocab - 1 is never accepted.  u is cut to 0 .. the largest number below 1; NaN counts as 0.
+ * 0 .. vocab - 1 is never accepted.  u is cut to 0 .. 1 - 2^-24; NaN counts as 0.
  * A request without nodes gets count 0 and next_token -1; of one with more than 4096 nodes, the first 4096 count.  Rows of no request
  * have their path left as it is; ranges as in w12_sequences.
  * 1 <= T <= 2^20, 1 <= requests <= 1024, 1 <= vocab <= 2^24, T * vocab < 2^40.

@@ -652,7 +652,7 @@ int w12_gated_delta(const w12_delta_args* a, const w12_sequences* s, void* ws, u
   if ((rc = check_state(a->state, a->slot_stride, vw * a->dk, s->slots, 4))) return rc;
   if (a->out && (rc = check_matrix(a->out, a->ldo, s->T, vw, 2, "out"))) return rc;
   if (!a->out && !s->dst) return fail(W12_ERR_INVALID_ARG, "neither outputs nor states are wanted");
-  const uint64_t need = w12::gated_delta_workspace_bytes(s->T, s->count, a->v_heads, a->dk, a->dv);
+  const uint64_t need = w12::gated_delta_call_bytes(*s, a->v_heads);
   if (ws_bytes < need)
     return fail(W12_ERR_WORKSPACE_TOO_SMALL, "workspace %llu bytes < %llu needed", (unsigned long long)ws_bytes,
                 (unsigned long long)need);

@@ -88,7 +88,7 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
     }
     kk = lane_sum<L>(kk);
     float rk = 1.0f, rq = a.scale;
-    if (a.l2norm) rk = 1.0f / sqrtf(kk + a.eps);
+    if (a.l2norm && row >= 0) rk = 1.0f / sqrtf(kk + a.eps);      // zeros that stand for no row stay zeros, with eps 0 too
     if (a.q) {
       qq = lane_sum<L>(qq);
       kq = lane_sum<L>(kq);
@@ -128,13 +128,15 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
 // Tokens a sequence has, on average, from which they are taken 64 at a time: between 8 (48 heads of 128, 1 / 4 / 16 / 64 sequences: 14 / 19 /
 // 42 / 144 us token by token, 16 / 25 / 56 / 200 in chunks) and 16 (25 / 31 / 67 / 226 and 16 / 25 / 57 / 205).  With lens the host does
 // not know how many count; accepted paths are far shorter than the trees that they lead through.
-constexpr int kChunkFrom = 12;
 static bool in_chunks(const w12_sequences& s) {
-  return s.tree_mask || s.T >= (int64_t)(s.lens ? W12_TREE_NODES + 1 : kChunkFrom) * s.count;
+  return s.tree_mask || s.T >= (int64_t)(s.lens ? W12_DELTA_CHUNK_FROM_LENS : W12_DELTA_CHUNK_FROM) * s.count;
 }
 
 uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv) {
   return delta_chunk_workspace_bytes(T, count, v_heads);
+}
+uint64_t gated_delta_call_bytes(const w12_sequences& s, int32_t v_heads) {
+  return in_chunks(s) ? delta_chunk_workspace_bytes(s.T, s.count, v_heads) : 0;
 }
 
 hipError_t launch_gated_delta(const w12_delta_args& a, const w12_sequences& s, void* ws, hipStream_t stream) {

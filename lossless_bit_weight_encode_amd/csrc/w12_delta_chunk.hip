@@ -663,7 +663,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
       for (int rt = 0; rt < 4; ++rt)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (!finite(x[rt][i])) {
+          if (!(fabsf(x[rt][i]) < 0x1.FFp127f)) {      // beyond BF16 is infinite too
             mine |= (uint64_t)1 << (16 * rt + row0 + i);
             x[rt][i] = 0.0f;
           }

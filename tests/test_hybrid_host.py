@@ -2,7 +2,9 @@
 here are made up and never read."""
 import contextlib
 import ctypes
+import os
 import random
+import re
 
 import pytest
 import torch
@@ -256,3 +258,10 @@ def test_bounds_cover_what_they_describe(n, parents):
         states.append(st)
     if parents is None:
         assert (states[-1].double() - s).abs().le(ds).all()
+
+
+def test_rows_from_which_gated_delta_needs_its_workspace():
+    """The binding allocates where the library asks for it."""
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "w12.h")).read()
+    for name in ("DELTA_CHUNK_FROM", "DELTA_CHUNK_FROM_LENS"):
+        assert int(re.search(rf"#define W12_{name} (\d+)", text).group(1)) == getattr(w12, name)
