@@ -18,9 +18,9 @@ __host__ __device__ constexpr int block_of(int r, int s) { return r * (r + 1) / 
 constexpr int kZeroBytes = 256;
 
 // T = (I + A)^-1 diag(beta) as two BF16 matrices (each fragment 16 bytes a lane) and 256 words: e^G / |k| and e^(G_last - G) / |k|
-// of the rows, e^G_last, and a bit for each row that is no number; then P as one matrix, and scale e^G / |q|.
+// of the rows, e^G_last, and a bit for each row that is no number; then P's first BF16 matrix and scale e^G / |q|; then P's second.
 constexpr int kFirstPages = 2 * kFragments + 1, kSecondPages = kFragments + 1;      // of 1 KB
-constexpr int kTermsBytes = (kFirstPages + kSecondPages) * 1024;
+constexpr int kTermsBytes = (kFirstPages + kSecondPages + kFragments) * 1024;
 struct Terms {
   char* at;
   typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
@@ -30,6 +30,7 @@ struct Terms {
   __device__ float* rows() const { return reinterpret_cast<float*>(at + 2 * kFragments * 1024); }
   __device__ char* second() const { return at + kFirstPages * 1024; }
   __device__ bf8* p(int f) const { return reinterpret_cast<bf8*>(second() + f * 1024); }
+  __device__ bf8* p_low(int f) const { return reinterpret_cast<bf8*>(second() + (kSecondPages + f) * 1024); }
   __device__ float* out_rows() const { return reinterpret_cast<float*>(second() + kFragments * 1024); }
 };
 // Words of rows().

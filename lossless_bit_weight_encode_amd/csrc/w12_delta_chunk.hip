@@ -10,8 +10,8 @@
 // (a lane: one column, 8 of the summed index) without a move: where a result's rows are tokens, T and P are laid out in
 // the order that this gives, and where they are S's, the rows of S are numbered so that it is the order of K in memory.
 // k, q and v are BF16 and exact; K S, T R and K^T U take what is FP32 as two BF16 values (hi + lo, off by 2^-16 at most; of T R
-// without the product of the two lows), so that the states keep nearly all of FP32; out, which is rounded to
-// BF16, takes one each of S, U and P.  T is made in FP32 throughout: 16 x 16 blocks by substitution (which does not
+// without the product of the two lows), so that the states keep nearly all of FP32 (2e-6 of their norm); out, which is rounded to
+// BF16, takes P as two, S and U as one each (0.0024 of its norm, of which its own rounding is 0.0017).  T is made in FP32 throughout: 16 x 16 blocks by substitution (which does not
 // cancel as powers of A would), joined by FP32 matrix instructions.
 #include "w12_delta_chunk.h"
 #include "w12_gemm_common.h"
@@ -238,8 +238,13 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
       }
       ablk[block_of(rt, t)][lane] = ab;
     }
-    if (a.q)
-      reinterpret_cast<uint2*>(out.p(fragment_of(rt, half)) + lane)[t & 1] = make_uint2(bf16_pair(pt[0], pt[1]), bf16_pair(pt[2], pt[3]));
+    if (a.q) {
+      const uint2 hi = make_uint2(bf16_pair(pt[0], pt[1]), bf16_pair(pt[2], pt[3]));
+      const auto over = [](float x, float y, uint32_t h) { return bf16_pair(x - bf16_float(h), y - __builtin_bit_cast(float, h & 0xFFFF0000u)); };
+      const int f = fragment_of(rt, half);
+      reinterpret_cast<uint2*>(out.p(f) + lane)[t & 1] = hi;
+      reinterpret_cast<uint2*>(out.p_low(f) + lane)[t & 1] = make_uint2(over(pt[0], pt[1], hi.x), over(pt[2], pt[3], hi.y));
+    }
   }
   lds_barrier();
   // the inverse of diagonal block w: a lane's column by substitution (the four groups of lanes do the same)
@@ -434,48 +439,54 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
   }
 
   if (w >= kTiles) {
-    // ---- outputs of the chunk before, half of its tokens a wave, turned: a lane's token (of each 16), and of every two tiles 8
+    // ---- outputs of the chunk before, half of its tokens a wave (tiles 0 and 3, or 1 and 2: 3 fragments of P each), turned: a lane's token (of each 16), and of every two tiles 8
     // neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
-    const int half = w - kTiles;
-    bf8 q[KS][2];
+    const int half = w - kTiles, tile[2] = {half, 3 - half};
+    bf8 q[KS][2], pl[3];
+    const char* const terms = ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
+    // P's second matrix has no room in LDS
+    auto read_p = [&](int chunk) {
+      const Terms from(const_cast<char*>(terms), (int64_t)chunk * a.v_heads);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) pl[i] = from.p_low(fragment_of(tile[(i + 1) / 2], i / 2))[lane];
+    };
     // (of tokens that are not there any row will do: a token's query makes its own output only)
     auto read_q = [&](int chunk) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int token = min(chunk * kChunk + 32 * half + 16 * j + c16, r.n - 1);
+        const int token = min(chunk * kChunk + 16 * tile[j] + c16, r.n - 1);
         const int row = ROWS ? max(row_of(s, r.start + token), 0) : r.start + token;
         const u32x4v* p = reinterpret_cast<const u32x4v*>(a.q + row * a.ldq + hk * DK) + g4;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) q[ks][j] = __builtin_bit_cast(bf8, p[4 * ks]);
       }
     };
-    if (a.q && chunks) read_q(0);
+    if (a.q && chunks) {
+      read_q(0);
+      read_p(0);
+    }
     barrier();
     for (int c = 0; c <= chunks; ++c) {
       if (c > 0 && a.q) {
         const ChunkLds<DK>& was = lds.chunk[(c - 1) & 1];
         const char* const second = lds.second[(c - 1) & 1];
         const bf8* const pf = reinterpret_cast<const bf8*>(second) + lane;
-        const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + 32 * half + c16;
+        const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + c16;
         // all of LDS's first, which then answers while the products run
-        bf8 sw[kTiles][KS], uw[kTiles][2], p[2][2];
+        bf8 sw[kTiles][KS], uw[kTiles][2], p[3];       // p: of tile[0], of tile[1], and of its later tokens
         float scale[2];
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int n = 0; n < kTiles; ++n) sw[n][ks] = was.s[n][ks][lane];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) scale[j] = rows[16 * j];
+        for (int j = 0; j < 2; ++j) scale[j] = rows[16 * tile[j]];
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) uw[n][0] = was.u[n][0][lane];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) p[j][0] = pf[(half ? fragment_of(2 + j, 0) : fragment_of(j, 0)) * 64];
-        if (half) {
+        for (int i = 0; i < 3; ++i) p[i] = pf[fragment_of(tile[(i + 1) / 2], i / 2) * 64];
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) uw[n][1] = was.u[n][1][lane];
-#pragma unroll
-          for (int j = 0; j < 2; ++j) p[j][1] = pf[fragment_of(2 + j, 1) * 64];
-        }
+        for (int n = 0; n < kTiles; ++n) uw[n][1] = was.u[n][1][lane];
         __builtin_amdgcn_sched_barrier(0);
         f32x4v o[kTiles][2];
 #pragma unroll
@@ -494,21 +505,24 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             o[n][j] *= scale[j];
-            o[n][j] = mma(uw[n][0], p[j][0], o[n][j]);
+            o[n][j] = mma(uw[n][0], p[j], o[n][j]);
           }
-        if (half) {
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n)
+        for (int n = 0; n < kTiles; ++n) o[n][1] = mma(uw[n][1], p[2], o[n][1]);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) o[n][j] = mma(uw[n][1], p[j][1], o[n][j]);
-        }
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) o[n][j] = mma(uw[n][0], pl[j], o[n][j]);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) o[n][1] = mma(uw[n][1], pl[2], o[n][1]);
+        if (c < chunks) read_p(c);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n) {
           const uint64_t* const bad = was.bad[n];
           if (!__any(bad[c16] != 0)) continue;
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int in = 32 * half + 16 * j + c16;
+            const int in = 16 * tile[j] + c16;
             const uint64_t path = (c - 1) * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -517,7 +531,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int token = (c - 1) * kChunk + 32 * half + 16 * j + c16;
+          const int token = (c - 1) * kChunk + 16 * tile[j] + c16;
           const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
           if (row >= 0) {
             uint16_t* const to = a.out + row * a.ldo + h * a.dv + col0 + 8 * g4;
