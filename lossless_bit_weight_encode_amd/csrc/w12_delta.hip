@@ -5,6 +5,10 @@
 // The columns of S (one per element of v) do not depend on one another.  A column lies along the lanes of a wave,
 // 8 values a lane, so that S^T k and S^T q are sums over 8 or 16 lanes (of the old state both: S'^T q = exp(g) S^T q + (k . q) u);
 // a wave holds 16 columns in registers and walks through its tokens without a barrier.
+//
+// Single tokens are bound by the states, which are read and written once: 64 sequences of 48 heads of 128 x 128 take 85 us (405 MB, 4.8 TB/s,
+// what a copy reaches here), one takes 5 us (6.3 MB).  Accepted paths (16 sequences, 40 us for 102 MB) pay for each token besides: 6 waves
+// share a SIMD's vector instructions, and the sums over lanes follow one another (loads a token ahead: 42 before).
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"
@@ -30,10 +34,12 @@ __device__ __forceinline__ float lane_sum(float v) {
   return v;
 }
 
-// A token of one value head: this lane's piece of k and q, its columns' values, and the scalars.
+// A token of one value head: this lane's piece of k and q, its columns' values, and the scalars, as they are in memory.
 template <int PASSES>
 struct Token {
-  float k[8], q[8], v[PASSES], g, beta;
+  uint4 k, q;
+  uint16_t v[PASSES];
+  float g, beta;
 };
 
 template <int DK>
@@ -59,31 +65,45 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
   }
   auto load = [&](int row, Token<PASSES>& t) {
     if (row < 0) {
+      t.k = t.q = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) t.k[e] = t.q[e] = 0.0f;
-#pragma unroll
-      for (int p = 0; p < PASSES; ++p) t.v[p] = 0.0f;
+      for (int p = 0; p < PASSES; ++p) t.v[p] = 0;
       t.g = t.beta = 0.0f;
       return;
     }
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(a.k + row * a.ldk + hk * DK + piece), t.k);
-    if (a.q) unpack_bf16x8(*reinterpret_cast<const uint4*>(a.q + row * a.ldq + hk * DK + piece), t.q);
+    t.k = *reinterpret_cast<const uint4*>(a.k + row * a.ldk + hk * DK + piece);
+    if (a.q) t.q = *reinterpret_cast<const uint4*>(a.q + row * a.ldq + hk * DK + piece);
 #pragma unroll
-    for (int p = 0; p < PASSES; ++p) t.v[p] = bf16_float(a.v[row * a.ldv + h * a.dv + col + p * P]);
+    for (int p = 0; p < PASSES; ++p) t.v[p] = a.v[row * a.ldv + h * a.dv + col + p * P];
     t.g = a.g[row * a.ldg + h];
     t.beta = a.beta[row * a.ldbeta + h];
   };
+  // a token's loads run beside the one before it, and its row's number beside the one before that
+  Token<PASSES> next;
+  int next_row = -1, row_after = -1;
+  if (r.n > 0) {
+    next_row = row_of(s, r.start);
+    load(next_row, next);
+  }
+  if (r.n > 1) row_after = row_of(s, r.start + 1);
   for (int i = 0; i < r.n; ++i) {
-    const int row = row_of(s, r.start + i);
-    Token<PASSES> t;
-    load(row, t);
+    const int row = next_row;
+    const Token<PASSES> t = next;
+    if (i + 1 < r.n) {
+      next_row = row_after;
+      load(next_row, next);
+      if (i + 2 < r.n) row_after = row_of(s, r.start + i + 2);
+    }
+    float k[8], q[8];
+    unpack_bf16x8(t.k, k);
+    if (a.q) unpack_bf16x8(t.q, q);
     float kk = 0.0f, qq = 0.0f, kq = 0.0f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      kk += t.k[e] * t.k[e];
+      kk += k[e] * k[e];
       if (a.q) {
-        qq += t.q[e] * t.q[e];
-        kq += t.k[e] * t.q[e];
+        qq += q[e] * q[e];
+        kq += k[e] * q[e];
       }
     }
     kk = lane_sum<L>(kk);
@@ -100,13 +120,13 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
       float sk = 0.0f, sq = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        sk += st[p][e] * t.k[e];
-        if (a.q) sq += st[p][e] * t.q[e];
+        sk += st[p][e] * k[e];
+        if (a.q) sq += st[p][e] * q[e];
       }
       sk = lane_sum<L>(sk);
-      const float u = t.beta * (t.v[p] - grown * rk * sk);
+      const float u = t.beta * (bf16_float(t.v[p]) - grown * rk * sk);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) st[p][e] = grown * st[p][e] + rk * t.k[e] * u;
+      for (int e = 0; e < 8; ++e) st[p][e] = grown * st[p][e] + rk * k[e] * u;
       if (a.q) {
         sq = lane_sum<L>(sq);
         const float o = rq * (grown * sq + rk * kq * u);
