@@ -460,7 +460,7 @@ int w12_gemm_e4m3(const uint8_t *X, int32_t M, int64_t ldx, const float *x_scale
  * Which rows of a call belong to which sequence, and where the sequences' states are.  Token i of
  * sequence b is row ptr[b] + i of the call's matrices, or row rows[ptr[b] + i] of them, for
  * i < ptr[b + 1] - ptr[b], and with lens for i < lens[b] besides.  A row outside 0 .. T - 1 counts
- * as zeros in every input, and has no output.  A sequence starts from the state in slot src[b] (zeros for
+ * as zeros in every input, and has no output.  Outputs overlap no input.  A sequence starts from the state in slot src[b] (zeros for
  * a slot outside 0 .. slots - 1) and its new state goes to slot dst[b] (nowhere for a slot outside),
  * which may be src[b]; a sequence without tokens has its old state put there.  dst NULL: no state is stored.
  * Slots of dst must differ from one another, and from the src of other sequences; several may share
@@ -521,8 +521,8 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * With l2norm, k and q are divided by sqrt(sum of squares + eps) first.  In a tree S is the state behind the node's parent.
  * The states are FP32 throughout.  Tokens of a long range are taken 64 at a time, as a triangular system
  *   u_i + beta_i sum_{j before i} exp(G_i - G_j) (k_i . k_j) u_j = beta_i (v_i - exp(G_i) S^T k_i),  G_i the sum of g up to i,
- * with BF16 matrix instructions: q, k and v are exact in them, what is FP32 (S, u, the system's inverse) goes
- * in as two BF16 values, off by 2^-16 of each value at most; for out, S, u and the q . k factors as one (2^-8).
+ * with BF16 matrix instructions: q, k and v are exact in them, what is FP32 (S, u, the system's inverse and the q . k factors) goes
+ * in as two BF16 values, off by 2^-16 of each value at most; for out, S and u as one (2^-8).  Squares of norms are FP32.
  * g <= 0 is expected.  The rule itself grows without bound where beta |k|^2 passes 2.  A NaN or infinity in a row reaches
  * that row and those that come after it in its sequence (in a tree: its descendants), and the new state; nothing else.
  * q and out NULL: only the states move on.  The result is bitwise the same from run to run.

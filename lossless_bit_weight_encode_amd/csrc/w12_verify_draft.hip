@@ -8,6 +8,10 @@
 // pieces again, with the last work-group to arrive picking the token.
 // Everything that decides is FP64 (which here runs at the rate of FP32), so that the token does not depend on how the sum was split:
 // a border between two tokens is missed by 2^-40 of the total at the most.
+//
+// Measured: 266 rows of 131072 logits of FP32 take 56 us, 44 of them the first kernel (139 MB, 3.2 TB/s: the FP64 weights, 13 operations each,
+// run partly beside the loads), 13 the second; 63 rows 23 us (15 and 8), a chain of 17 rows of 50257 with the drafter's
+// probabilities 19 (4 and 15: acceptances, the cut row's pieces and the last arriver's pick, one after another).
 #include <limits.h>
 
 #include "w12_gemm_common.h"
