@@ -25,7 +25,7 @@
 // compute units), a tree of 63 nodes 16 (10 and 6), 16 trees of 24 nodes 45.  The scan is bound by the instructions that a state wave issues
 // for a chunk (300 vector ones, 74 reads of LDS, 82 matrix instructions in 3700 cycles; a wave issues every 5th cycle at
 // best), hence the waves for loads and outputs beside it.  32 columns a work-group took 142 us for one prompt, but 467 instead of
-// 346 for seven (35003 tokens of 32 heads, now 370 us), whose work-groups fill the chip; the terms wait for their loads and for one another's phases, at 5
+// 346 for seven (35003 tokens of 32 heads, now 372 us), whose work-groups fill the chip; the terms wait for their loads and for one another's phases, at 5
 // work-groups a compute unit.
 namespace w12 {
 
