@@ -696,6 +696,10 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     if (g4 == 0) here.bad[w][c16] = bad_col;
     if (dst < 0 && c + 1 == chunks) {              // nobody asks for what S has become
       here.u[w][1][lane] = high(u[2], u[3]);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) asm volatile("" : "=v"(k[ks][rt]));      // not needed again: else one is kept, in memory
       break;
     }
     // S, half of the tokens at a time: the other half's split runs beside, and the reads of the next chunk's K
