@@ -144,14 +144,14 @@ __device__ __forceinline__ double scan_group(double v, double* lds, double& befo
   __syncthreads();
   return total;
 }
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ int first_of(int a, int b) { return min(a, b); }
+__device__ __forceinline__ int last_of(int a, int b) { return max(a, b); }
 // The largest of a work-group's values, and where it is first met.
 __device__ __forceinline__ void largest(float& top, int& at, float* ldsf, int* ldsi) {
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const float m = __shfl_xor(top, o);
-    const int i = __shfl_xor(at, o);
-    if (m > top || (m == top && i < at)) top = m, at = i;
-  }
+  const float m = over_wave(top, larger);
+  at = over_wave(top == m ? at : INT_MAX, first_of);
+  top = m;
   if ((threadIdx.x & 63) == 0) ldsf[threadIdx.x >> 6] = top, ldsi[threadIdx.x >> 6] = at;
   __syncthreads();
 #pragma unroll
@@ -204,19 +204,15 @@ __device__ __forceinline__ Row row_of_lanes(const Verify& v, int row, float t) {
   const int lane = threadIdx.x & 15;
   for (int i = lane; i < v.count; i += 16)
     if (p[i].at >= 0 && (r.at == INT_MAX || p[i].max > r.top)) r.top = p[i].max, r.at = p[i].at;
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) {
-    const float m = __shfl_xor(r.top, o);
-    const int i = __shfl_xor(r.at, o);
-    if (i != INT_MAX && (r.at == INT_MAX || m > r.top || (m == r.top && i < r.at))) r.top = m, r.at = i;
-  }
+  const float m = over_row(r.top, larger);
+  r.at = over_row(r.top == m ? r.at : INT_MAX, first_of);
+  r.top = m;
   r.one = t == 0.0f || r.top == INFINITY;
   r.steep = r.one ? 1.0 : steepness(t);
   r.total = 0.0;
   if (r.at != INT_MAX && !r.one)
     for (int i = lane; i < v.count; i += 16) r.total += piece_weight(p[i], r);
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) r.total += __shfl_xor(r.total, o);
+  r.total = over_row(r.total, [](double a, double b) { return a + b; });
   return r;
 }
 
@@ -295,11 +291,8 @@ __device__ __forceinline__ int find_token(int piece, VerifyLds& lds, F weights4)
     run += all;
   }
   // one lane for the wave: atomics on one place go one after another
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    first = min(first, __shfl_xor(first, o));
-    last = max(last, __shfl_xor(last, o));
-  }
+  first = over_wave(first, first_of);
+  last = over_wave(last, last_of);
   if ((threadIdx.x & 63) == 0) {
     atomicMin(&lds.found, first);
     atomicMax(&lds.last, last);
