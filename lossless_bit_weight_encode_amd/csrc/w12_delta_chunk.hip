@@ -21,11 +21,11 @@
 #include "w12_sequences.h"
 
 //
-// Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 164 us (terms 46, scan 124: 64 chunks of 1.9 us, one after another, on 96 of 256
+// Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 159 us (terms 46, scan 120: 64 chunks of 1.9 us, one after another, on 96 of 256
 // compute units), a tree of 63 nodes 16 (10 and 6), 16 trees of 24 nodes 45.  The scan is bound by the instructions that a state wave issues
 // for a chunk (300 vector ones, 74 reads of LDS, 82 matrix instructions in 3700 cycles; a wave issues every 5th cycle at
 // best), hence the waves for loads and outputs beside it.  32 columns a work-group took 142 us for one prompt, but 467 instead of
-// 346 for seven (35003 tokens of 32 heads, now 372 us), whose work-groups fill the chip; the terms wait for their loads and for one another's phases, at 5
+// 346 for seven (35003 tokens of 32 heads, now 367 us), whose work-groups fill the chip; the terms wait for their loads and for one another's phases, at 5
 // work-groups a compute unit.
 namespace w12 {
 

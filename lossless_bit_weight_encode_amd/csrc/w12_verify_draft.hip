@@ -9,9 +9,9 @@
 // Everything that decides is FP64 (which here runs at the rate of FP32), so that the token does not depend on how the sum was split:
 // a border between two tokens is missed by 2^-40 of the total at the most.
 //
-// Measured: 266 rows of 131072 logits of FP32 take 56 us, 44 of them the first kernel (139 MB, 3.2 TB/s: the FP64 weights, 13 operations each,
-// run partly beside the loads), 13 the second; 63 rows 23 us (15 and 8), a chain of 17 rows of 50257 with the drafter's
-// probabilities 19 (4 and 15: acceptances, the cut row's pieces and the last arriver's pick, one after another).
+// Measured: 266 rows of 131072 logits of FP32 take 53 us, 41 of them the first kernel (139 MB, 3.4 TB/s: the FP64 weights, 13 operations each,
+// run partly beside the loads), 12 the second; 63 rows 21 us (14 and 8), a chain of 17 rows of 50257 with the drafter's
+// probabilities 18 (4 and 14: acceptances, the cut row's pieces and the last arriver's pick, one after another).
 #include <limits.h>
 
 #include "w12_gemm_common.h"
@@ -23,8 +23,8 @@ namespace w12 {
 
 constexpr int kVerifyThreads = 256;
 constexpr int kVerifyWaves = kVerifyThreads / 64;
-// Values of a piece: for each wave so many rounds of 256 neighbours.  Few rows take short pieces, which fill the chip (17 rows of 50257:
-// 19 us, with 4 rounds 24; 63 of 131072: 25 and 27), many rows longer ones, with less to do around them (266 of 131072: 65 and 60 us).
+// Values of a piece: for each wave so many rounds of 256 neighbours.  Few rows take short pieces, which fill the chip (when the rule was measured,
+// 17 rows of 50257: 19 us, with 4 rounds 24; 63 of 131072: 25 and 27), many rows longer ones, with less to do around them (266 of 131072: 65 and 60 us).
 constexpr int kShortRounds = 2, kLongRounds = 4;
 constexpr int64_t kLongFrom = 4096;                            // long pieces of a call, two rounds of the chip
 constexpr int piece_values(int rounds) { return kVerifyThreads * 4 * rounds; }
