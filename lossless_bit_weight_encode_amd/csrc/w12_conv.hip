@@ -8,8 +8,8 @@
 // A sequence's first tile alone reads the state (no tile is shorter than a window's past), and writes the new one after it: in place,
 // no other work-group sees either.
 //
-// Bound by memory where rows are many: 4096 rows of 10240 channels of FP32 take 60 us (252 MB, 4.2 TB/s; the norm's pass over as much reaches
-// 5.1), in tiles of 16 rows with 4 rows' loads in flight (one row's at a time: 87).  63 nodes take 5.6 us in tiles of 2 (with the
+// Bound by memory where rows are many: 4096 rows of 10240 channels of FP32 take 58 us (252 MB, 4.3 TB/s; the norm's pass over as much reaches
+// 5.1), in tiles of 32 rows with 4 rows' loads in flight (tiles of 16: 63).  63 nodes take 5.6 us in tiles of 2 (with the
 // call 8.7; in tiles of 16 21): too few bytes to matter, the loads of a window follow the mask's.
 #include "w12_gemm_common.h"
 #include "w12_kernels.h"
@@ -20,7 +20,7 @@ namespace w12 {
 
 constexpr int kConvThreads = 64;
 // Rows of a tile.  Short tiles make work for the chip of few rows, long ones read fewer rows twice.
-constexpr int kTreeTile = 2, kShortTile = 4, kLongTile = 16;
+constexpr int kTreeTile = 2, kShortTile = 4, kLongTile = 32;
 
 // Weights of a thread's 8 channels.
 template <int W>
@@ -49,9 +49,13 @@ __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w1
   __shared__ int found[2];
   int b, tile;
   Range r;
-  if (!find_piece(s, blockIdx.x, TILE, found, b, r, tile)) return;
+  // long tiles: the blocks of a tile's channels are neighbours, so that work-groups at work together read whole rows
+  constexpr bool kFlat = TILE == kLongTile;
+  const int blocks = kFlat ? (a.channels + 8 * kConvThreads - 1) / (8 * kConvThreads) : 1;
+  const int block = kFlat ? blockIdx.x % blocks : blockIdx.y;
+  if (!find_piece(s, blockIdx.x / blocks, TILE, found, b, r, tile)) return;
   if (tile > 0 && !a.y) return;                      // only the first tile moves a state
-  const int c = (blockIdx.y * kConvThreads + threadIdx.x) * 8;
+  const int c = (block * kConvThreads + threadIdx.x) * 8;
   if (c >= a.channels) return;
   const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
   // a token of the sequence, or of its past: -1 is the newest; zeros where there is none
@@ -141,9 +145,11 @@ __global__ __launch_bounds__(kConvThreads) void k_short_conv(w12_conv_args a, w1
 template <bool F32, int W>
 static void conv_tiles(const w12_conv_args& a, const w12_sequences& s, hipStream_t stream) {
   const int64_t blocks = ceil_div(a.channels, 8 * kConvThreads);
-  const bool longer = !s.tree_mask && s.T / kLongTile * blocks >= 2 * 4 * device_cus();      // two waves a SIMD at least
+  // Two waves a SIMD at least: between 2048 rows of 10240 channels (short tiles 36 us, long ones 39) and 4096 of 8192 (54 and 51; of 10240 64 and 59).
+  const bool longer = !s.tree_mask && s.T / kLongTile * blocks >= 2 * 4 * device_cus();
   const int tile = s.tree_mask ? kTreeTile : longer ? kLongTile : kShortTile;
-  const dim3 grid((unsigned)most_pieces(s.T, s.count, tile), (unsigned)blocks);
+  const int64_t pieces = most_pieces(s.T, s.count, tile);
+  const dim3 grid((unsigned)(longer ? pieces * blocks : pieces), (unsigned)(longer ? 1 : blocks));
   if (s.tree_mask) k_short_conv<F32, W, true, kTreeTile><<<grid, kConvThreads, 0, stream>>>(a, s);
   else if (longer) k_short_conv<F32, W, false, kLongTile><<<grid, kConvThreads, 0, stream>>>(a, s);
   else k_short_conv<F32, W, false, kShortTile><<<grid, kConvThreads, 0, stream>>>(a, s);

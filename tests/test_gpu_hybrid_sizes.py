@@ -102,11 +102,12 @@ def test_delta_workspace_where_it_is_needed():
 
 
 @pytest.mark.parametrize("src", [F32, BF])
-def test_conv_long_tiles(src):
+@pytest.mark.parametrize("c", [4100, 8200])
+def test_conv_long_tiles(src, c):
     """Rows and channels enough for the long tiles; sequences that end inside of them."""
-    lengths, c, w = [2500, 0, 1, 15, 16, 17, 1547], 4100, 4
+    lengths, w = [2500, 0, 1, 15, 16, 17, 1547], 4
     t, b, ptr = sum(lengths), len(lengths), starts(lengths)
-    ld = 4104
+    ld = (c + 8) // 8 * 8
     x = torch.zeros(t, ld, dtype=src)
     x[:, :c] = rnd(1, t, c).to(src)
     past = torch.zeros(2 * b, w - 1, ld, dtype=src)
