@@ -216,18 +216,21 @@ __device__ __forceinline__ Row row_of_lanes(const Verify& v, int row, float t) {
   return r;
 }
 
-// Of work-groups' threads with weights of their own and the weight before them: the one in which the running sum passes `target`, and the
-// last with a weight, should rounding leave none.  The thread then looks at its parts.
+// Of a work-group's threads with weights of their own and the weight before them: the first whose running sum passes `target`, and the
+// last with a weight, should rounding leave none.  The thread then looks at its parts.  What is before a thread counts for nothing: it
+// may be an ulp above the running sum of the thread in front, and a target between the two belongs to either.
 template <typename F>
 __device__ __forceinline__ void pass_to(double target, double mine, double before, VerifyLds& lds, F parts) {
-  if (threadIdx.x == 0) lds.found = lds.last = -1;
+  if (threadIdx.x == 0) lds.found = INT_MAX, lds.last = -1;
   __syncthreads();
-  const bool has = mine > 0.0, in = has && before <= target && target < before + mine;
-  if (in) atomicMax(&lds.found, (int)threadIdx.x);      // two can be it only where sums are rounded apart
-  const uint64_t any = __ballot(has);
-  if (any && (threadIdx.x & 63) == 0) atomicMax(&lds.last, (int)threadIdx.x + 63 - __builtin_clzll(any));
+  const bool has = mine > 0.0;
+  const uint64_t any = __ballot(has), in = __ballot(has && target < before + mine);
+  if ((threadIdx.x & 63) == 0) {
+    if (in) atomicMin(&lds.found, (int)threadIdx.x + __builtin_ctzll(in));
+    if (any) atomicMax(&lds.last, (int)threadIdx.x + 63 - __builtin_clzll(any));
+  }
   __syncthreads();
-  const int who = lds.found >= 0 ? lds.found : lds.last;
+  const int who = lds.found != INT_MAX ? lds.found : lds.last;
   if ((int)threadIdx.x == who) parts(target - before);
   __syncthreads();
 }
