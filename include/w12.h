@@ -522,9 +522,11 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * The states are FP32 throughout.  Tokens of a long range are taken 64 at a time, as a triangular system
  *   u_i + beta_i sum_{j before i} exp(G_i - G_j) (k_i . k_j) u_j = beta_i (v_i - exp(G_i) S^T k_i),  G_i the sum of g up to i,
  * with BF16 matrix instructions: q, k and v are exact in them, what is FP32 (S, u, the system's inverse and the q . k factors) goes
- * in as two BF16 values, off by 2^-16 of each value at most; for out, S and u as one (2^-8).  Squares of norms are FP32.
+ * in as two BF16 values, off by 2^-16 of each value at most; for out, S and u as one (2^-8).  Sums of squares are FP32:
+ * a key whose sum passes that is no number, and with l2norm also a key or query whose sum + eps is under 2^-126 (eps 0).
  * g <= 0 is expected.  The rule itself grows without bound where beta |k|^2 passes 2.  A NaN or infinity in a row reaches
  * that row and those that come after it in its sequence (in a tree: its descendants), and the new state; nothing else.
+ * (Finite values whose u passes FP32 may reach tokens before theirs among the 64 that are taken together.)
  * q and out NULL: only the states move on.  The result is bitwise the same from run to run.
  * dk: 64 or 128, dv: 64, 128 or 256, v_heads a multiple of k_heads, at most 1024.
  * ws: w12_gated_delta_workspace_size bytes for T rows in count sequences (or more), 16-byte aligned, any content; calls

@@ -108,11 +108,13 @@ __global__ __launch_bounds__(kDeltaThreads) void k_delta_steps(w12_delta_args a,
     }
     kk = lane_sum<L>(kk);
     float rk = 1.0f, rq = a.scale;
-    if (a.l2norm && row >= 0) rk = 1.0f / sqrtf(kk + a.eps);      // zeros that stand for no row stay zeros, with eps 0 too
+    // zeros that stand for no row stay zeros, with eps 0 too; a key whose squares are past FP32 is no number
+    if (a.l2norm && row >= 0) rk = has_norm(kk + a.eps) ? 1.0f / sqrtf(kk + a.eps) : NAN;
+    if (!(kk < INFINITY)) rk = NAN;
     if (a.q) {
       qq = lane_sum<L>(qq);
       kq = lane_sum<L>(kq);
-      if (a.l2norm) rq *= 1.0f / sqrtf(qq + a.eps);
+      if (a.l2norm) rq *= has_norm(qq + a.eps) ? 1.0f / sqrtf(qq + a.eps) : NAN;
     }
     const float grown = expf(t.g);
 #pragma unroll

@@ -154,15 +154,18 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
     return pick(c16 & 3, t[0], t[1], t[2], t[3]);
   };
   const bool diagonal = g4 == c16 >> 2;
+  auto over_norm = [&](float squares) {
+    const float sum = squares + a.eps;
+    return !a.l2norm ? 1.0f : has_norm(sum) ? __builtin_amdgcn_rsqf(sum) : NAN;
+  };
   const float kk = square(kt);
-  const float ik = krow < 0 ? 0.0f : a.l2norm ? __builtin_amdgcn_rsqf(kk + a.eps) : 1.0f;
-  if (diagonal) rk[16 * w + c16] = finite(kk) && finite(ik) ? ik : NAN;
+  if (diagonal) rk[16 * w + c16] = krow < 0 ? 0.0f : finite(kk) ? over_norm(kk) : NAN;
   if (a.q) {
     const float qq = square(qt[0]);
-    if (diagonal && w < 3) rq[16 * q0 + c16] = qrow < 0 ? 0.0f : a.scale * (a.l2norm ? __builtin_amdgcn_rsqf(qq + a.eps) : 1.0f);
+    if (diagonal && w < 3) rq[16 * q0 + c16] = qrow < 0 ? 0.0f : a.scale * over_norm(qq);
     if (w == 0) {
       const float qq1 = square(qt[1]);
-      if (diagonal) rq[16 + c16] = qrow1 < 0 ? 0.0f : a.scale * (a.l2norm ? __builtin_amdgcn_rsqf(qq1 + a.eps) : 1.0f);
+      if (diagonal) rq[16 + c16] = qrow1 < 0 ? 0.0f : a.scale * over_norm(qq1);
     }
   }
   lds_barrier();

@@ -43,6 +43,9 @@ __device__ __forceinline__ uint64_t ancestors(const w12_sequences& s, int start,
   return s.tree_mask ? s.tree_mask[(int64_t)(start + i) * s.ld_mask] & below : below;
 }
 
+// Whether a sum of squares (with eps) has a norm in FP32: not one of zeros or of what is too small for the type, nor one past it or NaN.
+__device__ __forceinline__ bool has_norm(float sum) { return sum >= 0x1p-126f && sum < INFINITY; }
+
 // Pieces of `step` rows: sequence b's are numbered from start / step + b on, which keeps the numbers of
 // different sequences apart without a sum over their lengths; T / step + count numbers are enough for all.
 __host__ __device__ inline int64_t most_pieces(int64_t T, int64_t count, int step) { return T / step + count; }
