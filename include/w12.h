@@ -522,7 +522,7 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * The states are FP32 throughout.  Tokens of a long range are taken 64 at a time, as a triangular system
  *   u_i + beta_i sum_{j before i} exp(G_i - G_j) (k_i . k_j) u_j = beta_i (v_i - exp(G_i) S^T k_i),  G_i the sum of g up to i,
  * with BF16 matrix instructions: q, k and v are exact in them, what is FP32 (S, u, the system's inverse and the q . k factors) goes
- * in as two BF16 values, off by 2^-16 of each value at most; for out, S and u as one (2^-8).  Sums of squares are FP32:
+ * in as two BF16 values, off by 2^-16 of each value at most; out is rounded once, as token by token.  Sums of squares are FP32:
  * a key whose sum passes that is no number, and with l2norm also a key or query whose sum + eps is under 2^-126 (eps 0).
  * g <= 0 is expected.  The rule itself grows without bound where beta |k|^2 passes 2.  A NaN or infinity in a row reaches
  * that row and those that come after it in its sequence (in a tree: its descendants), and the new state; nothing else.

@@ -9,10 +9,11 @@
 // Matrix instructions: 16x16x32 BF16.  Their results (a lane: one column, 4 neighbouring rows) are the next ones' right operand
 // (a lane: one column, 8 of the summed index) without a move: where a result's rows are tokens, T and P are laid out in
 // the order that this gives, and where they are S's, the rows of S are numbered so that it is the order of K in memory.
-// k, q and v are BF16 and exact; K S, T R and K^T U take what is FP32 as two BF16 values (hi + lo, off by 2^-16 at most; of T R
-// without the product of the two lows), so that the states keep nearly all of FP32 (2e-6 of their norm); out, which is rounded to
-// BF16, takes P as two, S and U as one each (0.0024 of its norm, of which its own rounding is 0.0017).  T is made in FP32 throughout: 16 x 16 blocks by substitution (which does not
-// cancel as powers of A would), joined by FP32 matrix instructions.
+// k, q and v are BF16 and exact; what is FP32 (S, R, T, U, P) goes in as two BF16 values (hi + lo, off by 2^-16 at most; of T R and P U
+// without the product of the two lows).  So the states keep nearly all of FP32 (2.7e-6 of their norm after 4096 tokens; the recurrence in
+// FP32 1e-7), and out is off by its rounding to BF16 alone (0.0017 of its norm; with S and U as one value each 0.0026, and a tree's outputs
+// further from those of its tokens one by one than their rounding).  T is made in FP32 throughout: 16 x 16 blocks by substitution (which
+// does not cancel as powers of A would), joined by FP32 matrix instructions.
 #include "w12_delta_chunk.h"
 #include "w12_gemm_common.h"
 #include "w12_lanes.h"
@@ -21,12 +22,12 @@
 #include "w12_sequences.h"
 
 //
-// Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 159 us (terms 46, scan 120: 64 chunks of 1.9 us, one after another, on 96 of 256
-// compute units), a tree of 63 nodes 16 (10 and 6), 16 trees of 24 nodes 45.  The scan is bound by the instructions that a state wave issues
-// for a chunk (300 vector ones, 74 reads of LDS, 82 matrix instructions in 3700 cycles; a wave issues every 5th cycle at
-// best), hence the waves for loads and outputs beside it.  32 columns a work-group took 142 us for one prompt, but 467 instead of
-// 346 for seven (35003 tokens of 32 heads, now 367 us), whose work-groups fill the chip; the terms wait for their loads and for one another's phases, at 5
-// work-groups a compute unit.
+// Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 191 us (64 chunks, one after another, on 96 of 256 compute units), a tree of
+// 63 nodes 16, 16 trees of 24 nodes 47, seven prompts of 21834 tokens together, 32 heads, 405.  The scan is bound by the waves that carry S
+// (of a chunk's 5000 cycles 2000 are K S and S's split, 1000 U, 1600 S', 400 the search for values that are no numbers), hence the waves for
+// loads and outputs beside them, whose reads of LDS they wait for: with S and U as one value each for out, half of those reads, 159, 16, 45
+// and 363 us.  32 columns a work-group are faster for a prompt alone and slower where work-groups fill the chip.  The terms wait for their
+// loads and for one another's phases, at 5 work-groups a compute unit.
 namespace w12 {
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
@@ -323,19 +324,18 @@ __device__ __forceinline__ void to_lds(uint64_t base, uint32_t off, uint32_t at)
 // loads (a wave starts one to LDS in 75 cycles or more, a chunk takes 44).
 constexpr int kTiles = 4, kScanColumns = 16 * kTiles, kOuts = kTiles / 2, kScanThreads = 512, kLoaders = kScanThreads / 64 - kTiles - kOuts;
 
-// What a chunk has in LDS; in one piece what the waves that carry S read, so that a lane's few addresses reach all of it.
-template <int DK>
-struct ChunkLds {
-  char first[kFirstPages * 1024];                // terms
-  bf8 s[kTiles][DK / 32][64];                    // for the outputs: S before the chunk,
-  bf8 u[kTiles][2][64];                          // U,
-  uint64_t bad[kTiles][16];                      // and by column the tokens that were no numbers
-  char v[kChunk * kScanColumns * 2];
-};
+// What a chunk has in LDS.  A step has two barriers.  S before the chunk is written before the one in its middle and read after it, U the other
+// way round, so that neither needs a second buffer, for which there would be no room.
 template <int DK>
 struct ScanLds {
   char k[3][kChunk * DK * 2];
-  ChunkLds<DK> chunk[2];
+  struct {
+    char first[kFirstPages * 1024];              // terms
+    char v[kChunk * kScanColumns * 2];
+  } chunk[2];
+  bf8 s[2][kTiles][DK / 32][64];                 // for the outputs: S before the chunk (high, low),
+  bf8 u[2][kTiles][2][64];                       // U (high, low),
+  uint64_t bad[kTiles][16];                      // and by column the tokens that were no numbers
   char second[2][kSecondPages * 1024];
 };
 
@@ -434,14 +434,15 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     wait_vm_all();
     barrier();
     int k2 = 2;
-    for (int c = 0; c <= chunks; ++c) {
+    for (int c = 0; c < chunks; ++c) {
       if (c + 1 < chunks) {
         fetch_first(c + 1);
         fetch_v(c + 1);
       }
-      if (c < chunks && a.q) fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, kLoaders - 1 - me, lds.second[c & 1]);
+      if (a.q) fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, kLoaders - 1 - me, lds.second[c & 1]);
       if (c + 2 < chunks) fetch_k(c + 2, k2);
       k2 = k2 == 2 ? 0 : k2 + 1;
+      barrier();
       wait_vm_all();
       barrier();
     }
@@ -449,8 +450,8 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
   }
 
   if (w >= kTiles) {
-    // ---- outputs of the chunk before, half of its tokens a wave (tiles 0 and 3, or 1 and 2: 3 fragments of P each), turned: a lane's token (of each 16), and of every two tiles 8
-    // neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
+    // ---- outputs, half of the tokens a wave (tiles 0 and 3, or 1 and 2: 3 fragments of P each), turned: a lane's token (of each 16), and of
+    // every two tiles 8 neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
     const int half = w - kTiles, tile[2] = {half, 3 - half};
     bf8 q[KS][2], pl[3];
     const char* const terms = ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
@@ -476,82 +477,104 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
       read_p(0);
     }
     barrier();
-    for (int c = 0; c <= chunks; ++c) {
-      if (c > 0 && a.q) {
-        const ChunkLds<DK>& was = lds.chunk[(c - 1) & 1];
-        const char* const second = lds.second[(c - 1) & 1];
-        const bf8* const pf = reinterpret_cast<const bf8*>(second) + lane;
-        const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + c16;
-        // all of LDS's first, which then answers while the products run
-        bf8 sw[kTiles][KS], uw[kTiles][2], p[3];       // p: of tile[0], of tile[1], and of its later tokens
-        float scale[2];
+    f32x4v o[kTiles][2];
+    bf8 sw[2][kTiles][KS];
+    auto add_qs = [&](int part) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+      for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int n = 0; n < kTiles; ++n) sw[n][ks] = was.s[n][ks][lane];
+        for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) scale[j] = rows[16 * tile[j]];
+          for (int j = 0; j < 2; ++j) o[n][j] = mma(sw[part][n][ks], q[ks][j], o[n][j]);
+    };
+    // The rest of the chunk's Q S, e^G of it, and P U (U first from LDS, which answers while the lows of S run).
+    auto add_pu = [&](int chunk) {
+      const char* const second = lds.second[chunk & 1];
+      const bf8* const pf = reinterpret_cast<const bf8*>(second) + lane;
+      const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + c16;
+      bf8 uw[2][kTiles][2], p[3];       // p: of tile[0], of tile[1], and of its later tokens
+      float scale[2];
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) uw[n][0] = was.u[n][0][lane];
+      for (int j = 0; j < 2; ++j) scale[j] = rows[16 * tile[j]];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) p[i] = pf[fragment_of(tile[(i + 1) / 2], i / 2) * 64];
+      for (int i = 0; i < 3; ++i) p[i] = pf[fragment_of(tile[(i + 1) / 2], i / 2) * 64];
 #pragma unroll
-        for (int n = 0; n < kTiles; ++n) uw[n][1] = was.u[n][1][lane];
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) uw[part][n][ks] = lds.u[part][n][ks][lane];
+      __builtin_amdgcn_sched_barrier(0);
+      add_qs(1);
+      if (chunk + 1 < chunks) read_q(chunk + 1);
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) o[n][j] *= scale[j];
+#pragma unroll
+      for (int part = 0; part < 3; ++part) {
+        const bf8(&x)[kTiles][2] = uw[part == 2];
+        const bf8* const y = part == 1 ? pl : p;
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) o[n][j] = mma(x[n][0], y[j], o[n][j]);
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) o[n][1] = mma(x[n][1], y[2], o[n][1]);
+      }
+#pragma unroll
+      for (int n = 0; n < kTiles; ++n) {
+        const uint64_t* const bad = lds.bad[n];
+        if (!__any(bad[c16] != 0)) continue;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int in = 16 * tile[j] + c16;
+          const uint64_t path = chunk * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (path & bad[4 * g4 + i]) o[n][j][i] = NAN;
+        }
+      }
+    };
+    auto put = [&](int chunk) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int token = chunk * kChunk + 16 * tile[j] + c16;
+        const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
+        if (row >= 0) {
+          uint16_t* const to = a.out + row * a.ldo + h * a.dv + col0 + 8 * g4;
+#pragma unroll
+          for (int n = 0; n < kTiles; n += 2)
+            *reinterpret_cast<bf8*>(to + 16 * n) = high(o[n][j], o[n + 1][j]);
+        }
+      }
+    };
+    for (int c = 0; c < chunks; ++c) {
+      if (c > 0 && a.q) add_pu(c - 1);
+      lds_barrier();                               // S is there, U has been read
+      if (a.q) {
+#pragma unroll
+        for (int part = 0; part < 2; ++part)
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int n = 0; n < kTiles; ++n) sw[part][n][ks] = lds.s[part][n][ks][lane];
         __builtin_amdgcn_sched_barrier(0);
-        f32x4v o[kTiles][2];
+        if (c > 0) {
+          read_p(c);
+          put(c - 1);
+        }
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) o[n][j] = f32x4v{0, 0, 0, 0};
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) o[n][j] = mma(sw[n][ks], q[ks][j], o[n][j]);
-        if (c < chunks) read_q(c);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            o[n][j] *= scale[j];
-            o[n][j] = mma(uw[n][0], p[j], o[n][j]);
-          }
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) o[n][1] = mma(uw[n][1], p[2], o[n][1]);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) o[n][j] = mma(uw[n][0], pl[j], o[n][j]);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) o[n][1] = mma(uw[n][1], pl[2], o[n][1]);
-        if (c < chunks) read_p(c);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) {
-          const uint64_t* const bad = was.bad[n];
-          if (!__any(bad[c16] != 0)) continue;
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int in = 16 * tile[j] + c16;
-            const uint64_t path = (c - 1) * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (path & bad[4 * g4 + i]) o[n][j][i] = NAN;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int token = (c - 1) * kChunk + 16 * tile[j] + c16;
-          const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
-          if (row >= 0) {
-            uint16_t* const to = a.out + row * a.ldo + h * a.dv + col0 + 8 * g4;
-#pragma unroll
-            for (int n = 0; n < kTiles; n += 2)
-              *reinterpret_cast<bf8*>(to + 16 * n) = high(o[n][j], o[n + 1][j]);
-          }
-        }
+        add_qs(0);
       }
       lds_barrier();
+    }
+    if (chunks && a.q) {
+      add_pu(chunks - 1);
+      put(chunks - 1);
     }
     return;
   }
@@ -589,7 +612,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
   int k0 = 0, k1 = 1;                            // the buffers of this chunk's K, and the next one's
   for (int c = 0; c < chunks; ++c) {
     asm volatile("" : "+v"(kplace), "+v"(tplace));
-    ChunkLds<DK>& here = lds.chunk[c & 1];
+    const auto& here = lds.chunk[c & 1];
     const float* const rows = reinterpret_cast<const float*>(here.first + 2 * kFragments * 1024) + 4 * g4;
     const bf8* const tf = reinterpret_cast<const bf8*>(here.first) + lane;
     // K S, and beside it the rest of S's split, its decay, and what the next step reads from LDS
@@ -613,7 +636,8 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     for (int ks = 0; ks < KS; ++ks) {
       sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
       sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
-      here.s[w][ks][lane] = sh[ks];
+      lds.s[0][w][ks][lane] = sh[ks];
+      lds.s[1][w][ks][lane] = sl[ks];
       st[2 * ks] *= grown;
       st[2 * ks + 1] *= grown;
 #pragma unroll
@@ -639,7 +663,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
         kt[i] = turned((tplace ^ ((i >> 1) * 64)) + k0 * (kChunk * DK * 2) + ks * 32 * DK * 2 + (i & 1) * 8, 16 * DK * 2);
     };
     f32x4v left[4], u[4];
-    bf8 uh, ul;
+    bf8 uh, ul, first_high, first_low;             // scaled for S; of the first half as it is, for the outputs
     auto finish = [&](int ks) {
       u[2 * ks] *= left[2 * ks];
       u[2 * ks + 1] *= left[2 * ks + 1];
@@ -662,7 +686,8 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
 #pragma unroll
           for (int rt = 2 * ks; rt < 4; ++rt)
             u[rt] = mma(t[fragment_of(rt, ks) + (part == 2 ? kFragments : 0)], part == 1 ? rl[ks] : rh[ks], u[rt]);
-      here.u[w][0][lane] = high(u[0], u[1]);
+      first_high = high(u[0], u[1]);
+      first_low = low(u[0], u[1], first_high);
       finish(0);
     };
 #pragma unroll
@@ -677,6 +702,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     beside_matrix<12, 3, 2>();
     beside_matrix<6, 6, 0>();
     __builtin_amdgcn_sched_barrier(0);
+    lds_barrier();                                 // the outputs have read the U before
     // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out then, as
     // it would reach tokens that do not follow its own, and remembered.
     if (__any(!finite(u[3][0]))) {
@@ -696,13 +722,21 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
       bad_col |= mine;
       solve();
     }
-    if (g4 == 0) here.bad[w][c16] = bad_col;
+    auto put_u = [&] {
+      const bf8 hi = high(u[2], u[3]);
+      if (g4 == 0) lds.bad[w][c16] = bad_col;
+      lds.u[0][w][0][lane] = first_high;
+      lds.u[1][w][0][lane] = first_low;
+      lds.u[0][w][1][lane] = hi;
+      lds.u[1][w][1][lane] = low(u[2], u[3], hi);
+    };
     if (dst < 0 && c + 1 == chunks) {              // nobody asks for what S has become
-      here.u[w][1][lane] = high(u[2], u[3]);
+      put_u();
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
         for (int rt = 0; rt < 4; ++rt) asm volatile("" : "=v"(k[ks][rt]));      // not needed again: else one is kept, in memory
+      lds_barrier();
       break;
     }
     // S, half of the tokens at a time: the other half's split runs beside, and the reads of the next chunk's K
@@ -711,10 +745,10 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
 #pragma unroll
     for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
-    here.u[w][1][lane] = high(u[2], u[3]);
+    put_u();
     finish(1);
     read_turned(1);
-    beside_matrix<2 * RT, 3, 2>();
+    beside_matrix<2 * RT, 4, 2>();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
@@ -731,10 +765,8 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     }
     k0 = k1;
     k1 = k1 == 2 ? 0 : k1 + 1;
-    if (c + 1 < chunks) lds_barrier();
+    lds_barrier();
   }
-  if (chunks) lds_barrier();                     // of the last chunk,
-  lds_barrier();                                 // and of its outputs
   if (dst >= 0) {
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
