@@ -519,7 +519,7 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * log decay g, strength beta and query q turns it into
  *   S' = exp(g) S + k (beta (v - exp(g) S^T k))^T      and gives      out = scale S'^T q.
  * With l2norm, k and q are divided by sqrt(sum of squares + eps) first.  In a tree S is the state behind the node's parent.
- * The states are FP32 throughout.  Tokens of a long range are taken 64 at a time, as a triangular system
+ * The states are FP32 throughout.  Tokens of a tree or a long range are taken 64 at a time, as a triangular system
  *   u_i + beta_i sum_{j before i} exp(G_i - G_j) (k_i . k_j) u_j = beta_i (v_i - exp(G_i) S^T k_i),  G_i the sum of g up to i,
  * with BF16 matrix instructions: q, k and v are exact in them, what is FP32 (S, u, the system's inverse and the q . k factors) goes
  * in as two BF16 values, off by 2^-16 of each value at most; out is rounded once, as token by token.  Sums of squares are FP32:
@@ -531,10 +531,16 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * dk: 64 or 128, dv: 64, 128 or 256, v_heads a multiple of k_heads, at most 1024.
  * ws: w12_gated_delta_workspace_size bytes for T rows in count sequences (or more), 16-byte aligned, any content; calls
  * that overlap in time need workspaces of their own.  Only tokens taken 64 at a time need it: those of a tree, and of a call with
- * T >= W12_DELTA_CHUNK_FROM * count rows (with lens: W12_DELTA_CHUNK_FROM_LENS * count); else ws may be NULL.
+ * T >= W12_DELTA_CHUNK_FROM * count rows (with lens: W12_DELTA_CHUNK_FROM_LENS * count).  A call of fewer rows may have a NULL ws, or a small
+ * one, and takes all tokens one by one; without lens and with T - count + 1 >= W12_DELTA_CHUNK_LONG, where one sequence can be long beside the
+ * others, a ws is worth its bytes.  A call that has what it takes for 64 at a time takes a tree so, and each sequence that has
+ * W12_DELTA_CHUNK_FROM tokens or more itself (after lens), whatever the others have; the others token by token.  So a sequence's result does
+ * not depend, bit for bit, on those that share its call, but for one of W12_DELTA_CHUNK_FROM tokens or more in a call that takes all one by one:
+ * out is rounded once in either form.
  */
 #define W12_DELTA_CHUNK_FROM 12
 #define W12_DELTA_CHUNK_FROM_LENS 65
+#define W12_DELTA_CHUNK_LONG 64
 typedef struct w12_delta_args {
   int32_t k_heads, v_heads, dk, dv;
   int32_t l2norm;

@@ -13,7 +13,8 @@ from ._ops import _BF16, _F32, _FLOATS, _MASKS, _device, _matrix2, _on, _raw_str
 
 TREE_NODES = 64         # nodes of a tree for short_conv() and gated_delta()
 VERIFY_NODES = 4096     # nodes of a request for verify_draft()
-DELTA_CHUNK_FROM, DELTA_CHUNK_FROM_LENS = 12, 65      # rows a sequence from which gated_delta() takes 64 at a time, without and with lens
+DELTA_CHUNK_FROM, DELTA_CHUNK_FROM_LENS = 12, 65      # rows a sequence from which gated_delta() needs its workspace, without and with lens
+DELTA_CHUNK_LONG = 64   # rows past one a sequence from which it has use for one, without lens
 
 _I32 = torch.int32
 
@@ -115,8 +116,9 @@ def gated_delta(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, g: tor
 
     seq_ptr, src, dst, tree_mask, lens, rows: as for short_conv(); prompts, single tokens and accepted paths move the
     states from src to dst, chains and trees of drafted tokens leave them (no dst).  With outputs false only the states move on,
-    and q may be None.  ws: gated_delta_workspace(); allocated here when
-    omitted and needed (for trees, and from DELTA_CHUNK_FROM rows a sequence on).  Returns out (None without outputs)."""
+    and q may be None.  ws: gated_delta_workspace(); allocated here when omitted and of use (for trees, from DELTA_CHUNK_FROM rows a
+    sequence on, or where a long sequence can share the call with short ones; an empty one, with fewer rows, takes all tokens one by one).
+    A sequence's result does not depend on those that share its call.  Returns out (None without outputs)."""
     slots, h, dv, dk = _delta_state(state)
     t, kw = _matrix2(k, "k")
     _device(q, k, v, g, beta, state, seq_ptr, src, dst, tree_mask, lens, rows, out, ws)
@@ -129,13 +131,15 @@ def gated_delta(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, g: tor
         raise ValueError(f"k: {kw} columns are not whole heads of {dk} that {h} value heads can share")
     if not outputs:
         q = None
-    chunks = tree_mask is not None or t >= src.numel() * (DELTA_CHUNK_FROM if lens is None else DELTA_CHUNK_FROM_LENS)
+    b = src.numel()
+    chunks = (tree_mask is not None or t >= b * (DELTA_CHUNK_FROM if lens is None else DELTA_CHUNK_FROM_LENS) or
+              (lens is None and t - b + 1 >= DELTA_CHUNK_LONG))
     if (outputs and out is None) or (chunks and ws is None):
         with _on(stream):
             if outputs and out is None:
                 out = torch.empty(t, h * dv, dtype=_BF16, device=k.device)
             if chunks and ws is None:
-                ws = gated_delta_workspace(t, src.numel(), state)
+                ws = gated_delta_workspace(t, b, state)
     ld_k = _rows(k, "k", (t, kw), (_BF16,), 8)
     ld_v = _rows(v, "v", (t, h * dv), (_BF16,), 8)
     ld_g = _rows(g, "g", (t, h), (_F32,), 1)

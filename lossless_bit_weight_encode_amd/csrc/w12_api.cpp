@@ -658,7 +658,7 @@ int w12_gated_delta(const w12_delta_args* a, const w12_sequences* s, void* ws, u
                 (unsigned long long)need);
   if (need && !ws) return fail(W12_ERR_INVALID_ARG, "ws is NULL");
   if (ws && !aligned(ws, 16)) return fail(W12_ERR_MISALIGNED, "ws must be 16-byte aligned");
-  return hip_status(w12::launch_gated_delta(*a, *s, ws, stream), "gated_delta");
+  return hip_status(w12::launch_gated_delta(*a, *s, ws, ws_bytes, stream), "gated_delta");
 }
 
 static int check_verify_draft_shape(int32_t T, int32_t requests, int32_t vocab) {

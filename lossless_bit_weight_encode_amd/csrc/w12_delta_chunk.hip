@@ -15,11 +15,14 @@
 // further from those of its tokens one by one than their rounding).  T is made in FP32 throughout: 16 x 16 blocks by substitution (which
 // does not cancel as powers of A would), joined by FP32 matrix instructions.
 #include "w12_delta_chunk.h"
+#include "w12_delta_steps.h"
 #include "w12_gemm_common.h"
 #include "w12_lanes.h"
 #include "w12_kernels.h"
 #include "w12_rows.h"
 #include "w12_sequences.h"
+
+#include <algorithm>
 
 //
 // Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 191 us (64 chunks, one after another, on 96 of 256 compute units), a tree of
@@ -94,10 +97,42 @@ __device__ __forceinline__ bf8 rows_operand(const char* m, int rt, int ks) {
   return *reinterpret_cast<const bf8*>(m + piece_at<DK>(16 * rt + (lane & 15), 4 * ks + (lane >> 4)));
 }
 
+// Whether a sequence's tokens are taken 64 at a time, which goes by their own number (and the form) alone: between 8 (48 heads of 128, 1 / 4 /
+// 16 / 64 sequences: 14 / 19 / 42 / 144 us token by token, 16 / 25 / 56 / 200 in chunks) and 16 (25 / 31 / 67 / 226 and 16 / 25 / 57 / 205).
+__device__ __forceinline__ bool taken_in_chunks(const w12_sequences& s, const Range& r) { return s.tree_mask || r.n >= W12_DELTA_CHUNK_FROM; }
+
+// Sequence number j of those; false where there are fewer.  A wave looks at 64 at a time.
+__device__ __forceinline__ bool find_long(const w12_sequences& s, int j, int& b, Range& r) {
+  if (s.tree_mask) {
+    b = j;
+    if (j < s.count) r = range_of(s, b);
+    return j < s.count;
+  }
+  for (int b0 = 0; b0 < s.count; b0 += 64) {
+    const int i = b0 + (threadIdx.x & 63);
+    Range mine = {0, 0};
+    if (i < s.count) mine = range_of(s, i);
+    uint64_t longs = __ballot(taken_in_chunks(s, mine));
+    const int n = __builtin_popcountll(longs);
+    if (j < n) {
+      while (j-- > 0) longs &= longs - 1;
+      const int l = __builtin_ctzll(longs);
+      b = b0 + l;
+      r.start = __builtin_amdgcn_readlane(mine.start, l);
+      r.n = __builtin_amdgcn_readlane(mine.n, l);
+      return true;
+    }
+    j -= n;
+  }
+  return false;
+}
+
 // ------------------------------------------------------------------------------------------- terms
 
+// Work-groups from `pieces` on have no chunk: they take the short sequences, beside the others.
 template <int DK>
-__global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args a, w12_sequences s, char* ws) {
+__global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args a, w12_sequences s, char* ws, int pieces) {
+  static_assert(kChunkThreads == kDeltaThreads, "a work-group takes either");
   constexpr int KS = DK / 32;
   // keys, and once they are used the inverses of A's diagonal blocks
   union Shared {
@@ -114,12 +149,17 @@ __global__ __launch_bounds__(kChunkThreads, 4) void k_delta_terms(w12_delta_args
   __shared__ int found[2];
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), c16 = lane & 15, g4 = lane >> 4;
   const int h = blockIdx.y, hk = h / (a.v_heads / a.k_heads);
+  if ((int)blockIdx.x >= pieces) {
+    const int i = blockIdx.x - pieces, blocks = a.dv / kGroupColumns;
+    delta_steps<DK>(a, s, i / blocks, h, i % blocks, W12_DELTA_CHUNK_FROM - 1);
+    return;
+  }
   if (blockIdx.x == 0 && h == 0 && tid < kZeroBytes / 16) reinterpret_cast<uint4*>(ws)[tid] = make_uint4(0, 0, 0, 0);
   int b, chunk;
   Range r;
   if (!find_piece(s, blockIdx.x, kChunk, found, b, r, chunk)) return;
   const int first = chunk * kChunk, m = min(kChunk, r.n - first);
-  if (m <= 0) return;
+  if (m <= 0 || !taken_in_chunks(s, r)) return;
   auto row_at = [&](int i) { return i < m ? row_of(s, r.start + first + i) : -1; };
   auto operand = [&](const uint16_t* p, int64_t ld, int row, bf8 x[KS]) {
 #pragma unroll
@@ -360,7 +400,7 @@ __device__ __forceinline__ void beside_matrix() {
   }
 }
 
-template <int DK, bool ROWS>
+template <int DK, bool ROWS, bool MANY>
 __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w12_sequences s, const char* ws) {
   constexpr int KS = DK / 32, RT = DK / 16;
   __shared__ __attribute__((aligned(1024))) ScanLds<DK> lds;
@@ -368,411 +408,430 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
   // the column blocks of a head read the same rows and terms: neighbours, on one XCD
   const int blocks = a.dv / kScanColumns;
   // (and every sequence on all of them: lengths differ)
-  const int of = blocks * a.v_heads, b = blockIdx.x / of, at = (int)logical_wg(blockIdx.x % of, of);
+  const int of = blocks * a.v_heads, at = (int)logical_wg(blockIdx.x % of, of);
   const int cb = at % blocks, h = at / blocks;
   const int hk = h / (a.v_heads / a.k_heads);
-  const Range r = range_of(s, b);
-  const int chunks = (r.n + kChunk - 1) / kChunk;
   const int col0 = cb * kScanColumns;
+  // The sequences that are taken 64 at a time: this work-group's, one, or with MANY one after another.  Of LDS, what a sequence's waves read
+  // last, the next one's write behind its first barrier.
+  int number = blockIdx.x / of, b;
+  Range r;
+  bool there = find_long(s, number, b, r);
+  auto next = [&] {
+    if constexpr (!MANY) return false;
+    number += gridDim.x / of;
+    return find_long(s, number, b, r);
+  };
 
   if (w >= kTiles + kOuts) {
-    // ---- loads: of K and V a lane's places in a chunk, of the terms whole pages
-    const int me = w - kTiles - kOuts;
-    constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kEach = kChunk / kRows / kLoaders;
-    constexpr int kVLanes = kScanColumns / 8, kVRows = 64 / kVLanes, kVEach = kChunk / kVRows / kLoaders;
-    const char* const zeros = ws;                // the first row of the workspace
-    const char *kp[kEach], *vp[kVEach];
-    auto row_in = [&](int i) { return (me * kEach + i) * kRows + lane / kLanes; };
-    auto vrow_in = [&](int i) { return (me * kVEach + i) * kVRows + lane / kVLanes; };
-    auto from = [&](const uint16_t* m, int64_t ld, int row, int64_t at) { return reinterpret_cast<const char*>(m + row * ld + at); };
+    for (; there; there = next()) {
+      const int chunks = (r.n + kChunk - 1) / kChunk;
+      // ---- loads: of K and V a lane's places in a chunk, of the terms whole pages
+      const int me = w - kTiles - kOuts;
+      constexpr int kLanes = DK / 8, kRows = 64 / kLanes, kEach = kChunk / kRows / kLoaders;
+      constexpr int kVLanes = kScanColumns / 8, kVRows = 64 / kVLanes, kVEach = kChunk / kVRows / kLoaders;
+      const char* const zeros = ws;                // the first row of the workspace
+      const char *kp[kEach], *vp[kVEach];
+      auto row_in = [&](int i) { return (me * kEach + i) * kRows + lane / kLanes; };
+      auto vrow_in = [&](int i) { return (me * kVEach + i) * kVRows + lane / kVLanes; };
+      auto from = [&](const uint16_t* m, int64_t ld, int row, int64_t at) { return reinterpret_cast<const char*>(m + row * ld + at); };
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int piece = (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes;      // that belongs in this place
-      kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), hk * DK + piece * 8);
-    }
-#pragma unroll
-    for (int i = 0; i < kVEach; ++i)
-      vp[i] = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow_in(i), h * a.dv + col0 + lane % kVLanes * 8);
-    const int64_t kstep = kChunk * 2 * a.ldk, vstep = kChunk * 2 * a.ldv;
-    // `p`: of the chunk that is fetched; with rows, of row 0
-    auto send = [&](const char*& p, int64_t step, int64_t ld, int chunk, int row, const char* to) {
-      const char* x = p;
-      const int token = chunk * kChunk + row;
-      if constexpr (ROWS) {
-        const int in = token < r.n ? row_of(s, r.start + token) : -1;
-        x = in >= 0 ? p + in * (2 * ld) : zeros;
-      } else {
-        if ((chunk + 1) * kChunk > r.n) x = token < r.n ? p : zeros;
-        p += step;
+      for (int i = 0; i < kEach; ++i) {
+        const int piece = (piece_at<DK>(row_in(i), lane % kLanes) >> 4) % kLanes;      // that belongs in this place
+        kp[i] = from(a.k, a.ldk, ROWS ? 0 : r.start + row_in(i), hk * DK + piece * 8);
       }
-      to_lds(x, lds_off(to));
-    };
-    auto fetch_k = [&](int chunk, int buf) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) send(kp[i], kstep, a.ldk, chunk, row_in(i), lds.k[buf] + (me * kEach + i) * 1024);
-    };
-    auto fetch_v = [&](int chunk) {
+      for (int i = 0; i < kVEach; ++i)
+        vp[i] = from(a.v, a.ldv, ROWS ? 0 : r.start + vrow_in(i), h * a.dv + col0 + lane % kVLanes * 8);
+      const int64_t kstep = kChunk * 2 * a.ldk, vstep = kChunk * 2 * a.ldv;
+      // `p`: of the chunk that is fetched; with rows, of row 0
+      auto send = [&](const char*& p, int64_t step, int64_t ld, int chunk, int row, const char* to) {
+        const char* x = p;
+        const int token = chunk * kChunk + row;
+        if constexpr (ROWS) {
+          const int in = token < r.n ? row_of(s, r.start + token) : -1;
+          x = in >= 0 ? p + in * (2 * ld) : zeros;
+        } else {
+          if ((chunk + 1) * kChunk > r.n) x = token < r.n ? p : zeros;
+          p += step;
+        }
+        to_lds(x, lds_off(to));
+      };
+      auto fetch_k = [&](int chunk, int buf) {
 #pragma unroll
-      for (int i = 0; i < kVEach; ++i) send(vp[i], vstep, a.ldv, chunk, vrow_in(i), lds.chunk[chunk & 1].v + (me * kVEach + i) * 1024);
-    };
-    const uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
-    const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
-    auto fetch_pages = [&](uint64_t from, int pages, int mine, const char* to) {
+        for (int i = 0; i < kEach; ++i) send(kp[i], kstep, a.ldk, chunk, row_in(i), lds.k[buf] + (me * kEach + i) * 1024);
+      };
+      auto fetch_v = [&](int chunk) {
 #pragma unroll
-      for (int i = 0; i < (kFirstPages + kLoaders - 1) / kLoaders; ++i) {
-        const int page = i * kLoaders + mine;
-        if (page < pages) to_lds(from, (uint32_t)(page * 1024 + lane * 16), lds_off(to) + page * 1024);
+        for (int i = 0; i < kVEach; ++i) send(vp[i], vstep, a.ldv, chunk, vrow_in(i), lds.chunk[chunk & 1].v + (me * kVEach + i) * 1024);
+      };
+      const uint64_t terms = (uint64_t)(uintptr_t)ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
+      const uint64_t terms_step = (uint64_t)a.v_heads * kTermsBytes;
+      auto fetch_pages = [&](uint64_t from, int pages, int mine, const char* to) {
+#pragma unroll
+        for (int i = 0; i < (kFirstPages + kLoaders - 1) / kLoaders; ++i) {
+          const int page = i * kLoaders + mine;
+          if (page < pages) to_lds(from, (uint32_t)(page * 1024 + lane * 16), lds_off(to) + page * 1024);
+        }
+      };
+      auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, me, lds.chunk[chunk & 1].first); };
+      if (chunks) {
+        fetch_k(0, 0);
+        fetch_first(0);
+        fetch_v(0);
       }
-    };
-    auto fetch_first = [&](int chunk) { fetch_pages(terms + chunk * terms_step, kFirstPages, me, lds.chunk[chunk & 1].first); };
-    if (chunks) {
-      fetch_k(0, 0);
-      fetch_first(0);
-      fetch_v(0);
-    }
-    if (chunks > 1) fetch_k(1, 1);
-    wait_vm_all();
-    barrier();
-    int k2 = 2;
-    for (int c = 0; c < chunks; ++c) {
-      if (c + 1 < chunks) {
-        fetch_first(c + 1);
-        fetch_v(c + 1);
-      }
-      if (a.q) fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, kLoaders - 1 - me, lds.second[c & 1]);
-      if (c + 2 < chunks) fetch_k(c + 2, k2);
-      k2 = k2 == 2 ? 0 : k2 + 1;
-      barrier();
+      if (chunks > 1) fetch_k(1, 1);
       wait_vm_all();
       barrier();
+      int k2 = 2;
+      for (int c = 0; c < chunks; ++c) {
+        if (c + 1 < chunks) {
+          fetch_first(c + 1);
+          fetch_v(c + 1);
+        }
+        if (a.q) fetch_pages(terms + c * terms_step + kFirstPages * 1024, kSecondPages, kLoaders - 1 - me, lds.second[c & 1]);
+        if (c + 2 < chunks) fetch_k(c + 2, k2);
+        k2 = k2 == 2 ? 0 : k2 + 1;
+        barrier();
+        wait_vm_all();
+        barrier();
+      }
     }
     return;
   }
 
   if (w >= kTiles) {
-    // ---- outputs, half of the tokens a wave (tiles 0 and 3, or 1 and 2: 3 fragments of P each), turned: a lane's token (of each 16), and of
-    // every two tiles 8 neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
-    const int half = w - kTiles, tile[2] = {half, 3 - half};
-    bf8 q[KS][2], pl[3];
-    const char* const terms = ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
-    // P's second matrix has no room in LDS
-    auto read_p = [&](int chunk) {
-      const Terms from(const_cast<char*>(terms), (int64_t)chunk * a.v_heads);
+    for (; there; there = next()) {
+      const int chunks = (r.n + kChunk - 1) / kChunk;
+      // ---- outputs, half of the tokens a wave (tiles 0 and 3, or 1 and 2: 3 fragments of P each), turned: a lane's token (of each 16), and of
+      // every two tiles 8 neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
+      const int half = w - kTiles, tile[2] = {half, 3 - half};
+      bf8 q[KS][2], pl[3];
+      const char* const terms = ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
+      // P's second matrix has no room in LDS
+      auto read_p = [&](int chunk) {
+        const Terms from(const_cast<char*>(terms), (int64_t)chunk * a.v_heads);
 #pragma unroll
-      for (int i = 0; i < 3; ++i) pl[i] = from.p_low(fragment_of(tile[(i + 1) / 2], i / 2))[lane];
-    };
-    // (of tokens that are not there any row will do: a token's query makes its own output only)
-    auto read_q = [&](int chunk) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int token = min(chunk * kChunk + 16 * tile[j] + c16, r.n - 1);
-        const int row = ROWS ? max(row_of(s, r.start + token), 0) : r.start + token;
-        const u32x4v* p = reinterpret_cast<const u32x4v*>(a.q + row * a.ldq + hk * DK) + g4;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) q[ks][j] = __builtin_bit_cast(bf8, p[4 * ks]);
-      }
-    };
-    if (a.q && chunks) {
-      read_q(0);
-      read_p(0);
-    }
-    barrier();
-    f32x4v o[kTiles][2];
-    bf8 sw[2][kTiles][KS];
-    auto add_qs = [&](int part) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) o[n][j] = mma(sw[part][n][ks], q[ks][j], o[n][j]);
-    };
-    // The rest of the chunk's Q S, e^G of it, and P U (U first from LDS, which answers while the lows of S run).
-    auto add_pu = [&](int chunk) {
-      const char* const second = lds.second[chunk & 1];
-      const bf8* const pf = reinterpret_cast<const bf8*>(second) + lane;
-      const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + c16;
-      bf8 uw[2][kTiles][2], p[3];       // p: of tile[0], of tile[1], and of its later tokens
-      float scale[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) scale[j] = rows[16 * tile[j]];
-#pragma unroll
-      for (int i = 0; i < 3; ++i) p[i] = pf[fragment_of(tile[(i + 1) / 2], i / 2) * 64];
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int n = 0; n < kTiles; ++n) uw[part][n][ks] = lds.u[part][n][ks][lane];
-      __builtin_amdgcn_sched_barrier(0);
-      add_qs(1);
-      if (chunk + 1 < chunks) read_q(chunk + 1);
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) o[n][j] *= scale[j];
-#pragma unroll
-      for (int part = 0; part < 3; ++part) {
-        const bf8(&x)[kTiles][2] = uw[part == 2];
-        const bf8* const y = part == 1 ? pl : p;
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) o[n][j] = mma(x[n][0], y[j], o[n][j]);
-#pragma unroll
-        for (int n = 0; n < kTiles; ++n) o[n][1] = mma(x[n][1], y[2], o[n][1]);
-      }
-#pragma unroll
-      for (int n = 0; n < kTiles; ++n) {
-        const uint64_t* const bad = lds.bad[n];
-        if (!__any(bad[c16] != 0)) continue;
+        for (int i = 0; i < 3; ++i) pl[i] = from.p_low(fragment_of(tile[(i + 1) / 2], i / 2))[lane];
+      };
+      // (of tokens that are not there any row will do: a token's query makes its own output only)
+      auto read_q = [&](int chunk) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int in = 16 * tile[j] + c16;
-          const uint64_t path = chunk * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
+          const int token = min(chunk * kChunk + 16 * tile[j] + c16, r.n - 1);
+          const int row = ROWS ? max(row_of(s, r.start + token), 0) : r.start + token;
+          const u32x4v* p = reinterpret_cast<const u32x4v*>(a.q + row * a.ldq + hk * DK) + g4;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (path & bad[4 * g4 + i]) o[n][j][i] = NAN;
+          for (int ks = 0; ks < KS; ++ks) q[ks][j] = __builtin_bit_cast(bf8, p[4 * ks]);
         }
+      };
+      if (a.q && chunks) {
+        read_q(0);
+        read_p(0);
       }
-    };
-    auto put = [&](int chunk) {
+      barrier();
+      f32x4v o[kTiles][2];
+      bf8 sw[2][kTiles][KS];
+      auto add_qs = [&](int part) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int token = chunk * kChunk + 16 * tile[j] + c16;
-        const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
-        if (row >= 0) {
-          uint16_t* const to = a.out + row * a.ldo + h * a.dv + col0 + 8 * g4;
+        for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-          for (int n = 0; n < kTiles; n += 2)
-            *reinterpret_cast<bf8*>(to + 16 * n) = high(o[n][j], o[n + 1][j]);
-        }
-      }
-    };
-    for (int c = 0; c < chunks; ++c) {
-      if (c > 0 && a.q) add_pu(c - 1);
-      lds_barrier();                               // S is there, U has been read
-      if (a.q) {
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) o[n][j] = mma(sw[part][n][ks], q[ks][j], o[n][j]);
+      };
+      // The rest of the chunk's Q S, e^G of it, and P U (U first from LDS, which answers while the lows of S run).
+      auto add_pu = [&](int chunk) {
+        const char* const second = lds.second[chunk & 1];
+        const bf8* const pf = reinterpret_cast<const bf8*>(second) + lane;
+        const float* const rows = reinterpret_cast<const float*>(second + kFragments * 1024) + c16;
+        bf8 uw[2][kTiles][2], p[3];       // p: of tile[0], of tile[1], and of its later tokens
+        float scale[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) scale[j] = rows[16 * tile[j]];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) p[i] = pf[fragment_of(tile[(i + 1) / 2], i / 2) * 64];
 #pragma unroll
         for (int part = 0; part < 2; ++part)
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
+          for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int n = 0; n < kTiles; ++n) sw[part][n][ks] = lds.s[part][n][ks][lane];
+            for (int n = 0; n < kTiles; ++n) uw[part][n][ks] = lds.u[part][n][ks][lane];
         __builtin_amdgcn_sched_barrier(0);
-        if (c > 0) {
-          read_p(c);
-          put(c - 1);
-        }
+        add_qs(1);
+        if (chunk + 1 < chunks) read_q(chunk + 1);
 #pragma unroll
         for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) o[n][j] = f32x4v{0, 0, 0, 0};
-        add_qs(0);
+          for (int j = 0; j < 2; ++j) o[n][j] *= scale[j];
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          const bf8(&x)[kTiles][2] = uw[part == 2];
+          const bf8* const y = part == 1 ? pl : p;
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) o[n][j] = mma(x[n][0], y[j], o[n][j]);
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n) o[n][1] = mma(x[n][1], y[2], o[n][1]);
+        }
+#pragma unroll
+        for (int n = 0; n < kTiles; ++n) {
+          const uint64_t* const bad = lds.bad[n];
+          if (!__any(bad[c16] != 0)) continue;
+          int token0 = c16;
+          asm volatile("" : "+v"(token0));           // else what follows is made before the loop, and kept
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int in = 16 * tile[j] + token0;
+            const uint64_t path = chunk * kChunk + in < r.n ? ancestors(s, r.start, in) | (uint64_t)1 << in : 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (path & bad[4 * g4 + i]) o[n][j][i] = NAN;
+          }
+        }
+      };
+      auto put = [&](int chunk) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int token = chunk * kChunk + 16 * tile[j] + c16;
+          const int row = token < r.n ? (ROWS ? row_of(s, r.start + token) : r.start + token) : -1;
+          if (row >= 0) {
+            uint16_t* const to = a.out + row * a.ldo + h * a.dv + col0 + 8 * g4;
+#pragma unroll
+            for (int n = 0; n < kTiles; n += 2)
+              *reinterpret_cast<bf8*>(to + 16 * n) = high(o[n][j], o[n + 1][j]);
+          }
+        }
+      };
+      for (int c = 0; c < chunks; ++c) {
+        if (c > 0 && a.q) add_pu(c - 1);
+        lds_barrier();                               // S is there, U has been read
+        if (a.q) {
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+              for (int n = 0; n < kTiles; ++n) sw[part][n][ks] = lds.s[part][n][ks][lane];
+          __builtin_amdgcn_sched_barrier(0);
+          if (c > 0) {
+            read_p(c);
+            put(c - 1);
+          }
+#pragma unroll
+          for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) o[n][j] = f32x4v{0, 0, 0, 0};
+          add_qs(0);
+        }
+        lds_barrier();
       }
-      lds_barrier();
-    }
-    if (chunks && a.q) {
-      add_pu(chunks - 1);
-      put(chunks - 1);
+      if (chunks && a.q) {
+        add_pu(chunks - 1);
+        put(chunks - 1);
+      }
     }
     return;
   }
 
-  // ---- 16 columns of S through the chunks: what the kernel's time is made of.  Of every 8 columns, two waves have 4 each: so the outputs
-  // have 8 neighbours in a lane.
-  const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
-  const int64_t state_at = ((int64_t)h * a.dv + col0 + (w >> 1) * 32 + (c16 >> 2) * 8 + (w & 1) * 4 + (c16 & 3)) * DK + 8 * g4;
-  f32x4v st[RT];
+  for (; there; there = next()) {
+    const int chunks = (r.n + kChunk - 1) / kChunk;
+    // ---- 16 columns of S through the chunks: what the kernel's time is made of.  Of every 8 columns, two waves have 4 each: so the outputs
+    // have 8 neighbours in a lane.
+    const int src = slot_of(s, s.src, b), dst = slot_of(s, s.dst, b);
+    const int64_t state_at = ((int64_t)h * a.dv + col0 + (w >> 1) * 32 + (c16 >> 2) * 8 + (w & 1) * 4 + (c16 & 3)) * DK + 8 * g4;
+    f32x4v st[RT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) st[i] = f32x4v{0, 0, 0, 0};
-  if (src >= 0) {
+    for (int i = 0; i < RT; ++i) st[i] = f32x4v{0, 0, 0, 0};
+    if (src >= 0) {
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const f32x4v* p = reinterpret_cast<const f32x4v*>(a.state + src * a.slot_stride + state_at + 32 * ks);
-      st[2 * ks] = p[0];
-      st[2 * ks + 1] = p[1];
-    }
-  }
-  bf8 k[KS][4];
-  // A lane's places in the first buffer of K, of the operands of K S and of those of K turned (pieces 4 ks further lie where these bits
-  // differ).  The compiler is not to know that they stay the same: it would keep every address made from them.
-  uint32_t kplace = lds_off(lds.k[0]) + piece_at<DK>(c16, g4);
-  uint32_t tplace = lds_off(lds.k[0]) + piece_at<DK>(4 * g4 + (c16 >> 2), c16 & 3);
-  auto read_k = [&](int buf) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-        k[ks][rt] = __builtin_bit_cast(bf8, lds_at((kplace ^ (ks * 64)) + buf * (kChunk * DK * 2) + rt * 16 * DK * 2));
-  };
-  barrier();
-  __builtin_amdgcn_s_setprio(2);
-  if (chunks) read_k(0);
-  int k0 = 0, k1 = 1;                            // the buffers of this chunk's K, and the next one's
-  for (int c = 0; c < chunks; ++c) {
-    asm volatile("" : "+v"(kplace), "+v"(tplace));
-    const auto& here = lds.chunk[c & 1];
-    const float* const rows = reinterpret_cast<const float*>(here.first + 2 * kFragments * 1024) + 4 * g4;
-    const bf8* const tf = reinterpret_cast<const bf8*>(here.first) + lane;
-    // K S, and beside it the rest of S's split, its decay, and what the next step reads from LDS
-    const float grown = rows[kGrown - 4 * g4];
-    uint64_t bad_col = reinterpret_cast<const uint64_t*>(here.first + 2 * kFragments * 1024)[kBad / 2];
-    __builtin_amdgcn_sched_barrier(0);
-    f32x4v taken[4];
-    i16x4 v[4];
-    bf8 t[2 * kFragments], sh[KS], sl[KS];
-    // V turned: a lane's column of 4 neighbouring tokens
-    const uint32_t vat = lds_off(here.v) + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + (w >> 1) * 64 + (c16 & 3) * 16 + (w & 1) * 8;
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) {
-      taken[rt] = *reinterpret_cast<const f32x4v*>(rows + kTaken + 16 * rt);
-      v[rt] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_i16x4*>(vat + rt * 16 * kScanColumns * 2));
-    }
-    f32x4v x[4];
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4v{0, 0, 0, 0};
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
-      sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
-      lds.s[0][w][ks][lane] = sh[ks];
-      lds.s[1][w][ks][lane] = sl[ks];
-      st[2 * ks] *= grown;
-      st[2 * ks + 1] *= grown;
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
-      if (ks == KS / 2 - 1) {
-        __builtin_amdgcn_sched_group_barrier(0x002, 24, 0);
-        beside_matrix<4 * KS, 4, 1>();
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int i = 0; i < 2 * kFragments; ++i) t[i] = tf[i * 64];
+      for (int ks = 0; ks < KS; ++ks) {
+        const f32x4v* p = reinterpret_cast<const f32x4v*>(a.state + src * a.slot_stride + state_at + 32 * ks);
+        st[2 * ks] = p[0];
+        st[2 * ks + 1] = p[1];
       }
     }
-    beside_matrix<4 * KS, 4, 1>();
-    __builtin_amdgcn_sched_barrier(0);
-    // R = V - e^G K S / |k|, U = T R, and beside them K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows
-    // of S's tile i are
-    bf8 kt[RT];
-    auto read_turned = [&](int ks) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-        kt[i] = turned((tplace ^ ((i >> 1) * 64)) + k0 * (kChunk * DK * 2) + ks * 32 * DK * 2 + (i & 1) * 8, 16 * DK * 2);
-    };
-    f32x4v left[4], u[4];
-    bf8 uh, ul, first_high, first_low;             // scaled for S; of the first half as it is, for the outputs
-    auto finish = [&](int ks) {
-      u[2 * ks] *= left[2 * ks];
-      u[2 * ks + 1] *= left[2 * ks + 1];
-      uh = high(u[2 * ks], u[2 * ks + 1]);
-      ul = low(u[2 * ks], u[2 * ks + 1], uh);
-    };
-    auto solve = [&] {
-      bf8 rh[2], rl[2];
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        rh[ks] = high(x[2 * ks], x[2 * ks + 1]);
-        rl[ks] = low(x[2 * ks], x[2 * ks + 1], rh[ks]);
-      }
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-        for (int part = 0; part < 3; ++part)
-#pragma unroll
-          for (int rt = 2 * ks; rt < 4; ++rt)
-            u[rt] = mma(t[fragment_of(rt, ks) + (part == 2 ? kFragments : 0)], part == 1 ? rl[ks] : rh[ks], u[rt]);
-      first_high = high(u[0], u[1]);
-      first_low = low(u[0], u[1], first_high);
-      finish(0);
-    };
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[rt][i] = __builtin_fmaf(-taken[rt][i], x[rt][i], bf16_float((uint16_t)v[rt][i]));
-#pragma unroll
-    for (int rt = 0; rt < 4; ++rt) left[rt] = *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
-    read_turned(0);
-    solve();
-    __builtin_amdgcn_sched_group_barrier(0x002, 40, 0);
-    beside_matrix<12, 3, 2>();
-    beside_matrix<6, 6, 0>();
-    __builtin_amdgcn_sched_barrier(0);
-    lds_barrier();                                 // the outputs have read the U before
-    // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out then, as
-    // it would reach tokens that do not follow its own, and remembered.
-    if (__any(!finite(u[3][0]))) {
-      uint64_t mine = 0;
-      int row0 = 4 * g4;
-      asm volatile("" : "+v"(row0));               // else the bits of all rows are made before the loop, and kept
-#pragma unroll
-      for (int rt = 0; rt < 4; ++rt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!(fabsf(x[rt][i]) < 0x1.FFp127f)) {      // beyond BF16 is infinite too
-            mine |= (uint64_t)1 << (16 * rt + row0 + i);
-            x[rt][i] = 0.0f;
-          }
-      mine |= __shfl_xor(mine, 16);
-      mine |= __shfl_xor(mine, 32);
-      bad_col |= mine;
-      solve();
-    }
-    auto put_u = [&] {
-      const bf8 hi = high(u[2], u[3]);
-      if (g4 == 0) lds.bad[w][c16] = bad_col;
-      lds.u[0][w][0][lane] = first_high;
-      lds.u[1][w][0][lane] = first_low;
-      lds.u[0][w][1][lane] = hi;
-      lds.u[1][w][1][lane] = low(u[2], u[3], hi);
-    };
-    if (dst < 0 && c + 1 == chunks) {              // nobody asks for what S has become
-      put_u();
+    bf8 k[KS][4];
+    // A lane's places in the first buffer of K, of the operands of K S and of those of K turned (pieces 4 ks further lie where these bits
+    // differ).  The compiler is not to know that they stay the same: it would keep every address made from them.
+    uint32_t kplace = lds_off(lds.k[0]) + piece_at<DK>(c16, g4);
+    uint32_t tplace = lds_off(lds.k[0]) + piece_at<DK>(4 * g4 + (c16 >> 2), c16 & 3);
+    auto read_k = [&](int buf) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int rt = 0; rt < 4; ++rt) asm volatile("" : "=v"(k[ks][rt]));      // not needed again: else one is kept, in memory
+        for (int rt = 0; rt < 4; ++rt)
+          k[ks][rt] = __builtin_bit_cast(bf8, lds_at((kplace ^ (ks * 64)) + buf * (kChunk * DK * 2) + rt * 16 * DK * 2));
+    };
+    barrier();
+    __builtin_amdgcn_s_setprio(2);
+    if (chunks) read_k(0);
+    int k0 = 0, k1 = 1;                            // the buffers of this chunk's K, and the next one's
+    for (int c = 0; c < chunks; ++c) {
+      asm volatile("" : "+v"(kplace), "+v"(tplace));
+      const auto& here = lds.chunk[c & 1];
+      const float* const rows = reinterpret_cast<const float*>(here.first + 2 * kFragments * 1024) + 4 * g4;
+      const bf8* const tf = reinterpret_cast<const bf8*>(here.first) + lane;
+      // K S, and beside it the rest of S's split, its decay, and what the next step reads from LDS
+      const float grown = rows[kGrown - 4 * g4];
+      uint64_t bad_col = reinterpret_cast<const uint64_t*>(here.first + 2 * kFragments * 1024)[kBad / 2];
+      __builtin_amdgcn_sched_barrier(0);
+      f32x4v taken[4];
+      i16x4 v[4];
+      bf8 t[2 * kFragments], sh[KS], sl[KS];
+      // V turned: a lane's column of 4 neighbouring tokens
+      const uint32_t vat = lds_off(here.v) + (4 * g4 + (c16 >> 2)) * (kScanColumns * 2) + (w >> 1) * 64 + (c16 & 3) * 16 + (w & 1) * 8;
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) {
+        taken[rt] = *reinterpret_cast<const f32x4v*>(rows + kTaken + 16 * rt);
+        v[rt] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(reinterpret_cast<lds_i16x4*>(vat + rt * 16 * kScanColumns * 2));
+      }
+      f32x4v x[4];
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) x[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        sh[ks] = high(st[2 * ks], st[2 * ks + 1]);
+        sl[ks] = low(st[2 * ks], st[2 * ks + 1], sh[ks]);
+        lds.s[0][w][ks][lane] = sh[ks];
+        lds.s[1][w][ks][lane] = sl[ks];
+        st[2 * ks] *= grown;
+        st[2 * ks + 1] *= grown;
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sh[ks], x[rt]);
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) x[rt] = mma(k[ks][rt], sl[ks], x[rt]);
+        if (ks == KS / 2 - 1) {
+          __builtin_amdgcn_sched_group_barrier(0x002, 24, 0);
+          beside_matrix<4 * KS, 4, 1>();
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int i = 0; i < 2 * kFragments; ++i) t[i] = tf[i * 64];
+        }
+      }
+      beside_matrix<4 * KS, 4, 1>();
+      __builtin_amdgcn_sched_barrier(0);
+      // R = V - e^G K S / |k|, U = T R, and beside them K turned: of tokens 32 ks + 4 g .. + 3 (and 16 further) the values that the rows
+      // of S's tile i are
+      bf8 kt[RT];
+      auto read_turned = [&](int ks) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+          kt[i] = turned((tplace ^ ((i >> 1) * 64)) + k0 * (kChunk * DK * 2) + ks * 32 * DK * 2 + (i & 1) * 8, 16 * DK * 2);
+      };
+      f32x4v left[4], u[4];
+      bf8 uh, ul, first_high, first_low;             // scaled for S; of the first half as it is, for the outputs
+      auto finish = [&](int ks) {
+        u[2 * ks] *= left[2 * ks];
+        u[2 * ks + 1] *= left[2 * ks + 1];
+        uh = high(u[2 * ks], u[2 * ks + 1]);
+        ul = low(u[2 * ks], u[2 * ks + 1], uh);
+      };
+      auto solve = [&] {
+        bf8 rh[2], rl[2];
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt) u[rt] = f32x4v{0, 0, 0, 0};
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          rh[ks] = high(x[2 * ks], x[2 * ks + 1]);
+          rl[ks] = low(x[2 * ks], x[2 * ks + 1], rh[ks]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int part = 0; part < 3; ++part)
+#pragma unroll
+            for (int rt = 2 * ks; rt < 4; ++rt)
+              u[rt] = mma(t[fragment_of(rt, ks) + (part == 2 ? kFragments : 0)], part == 1 ? rl[ks] : rh[ks], u[rt]);
+        first_high = high(u[0], u[1]);
+        first_low = low(u[0], u[1], first_high);
+        finish(0);
+      };
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[rt][i] = __builtin_fmaf(-taken[rt][i], x[rt][i], bf16_float((uint16_t)v[rt][i]));
+#pragma unroll
+      for (int rt = 0; rt < 4; ++rt) left[rt] = *reinterpret_cast<const f32x4v*>(rows + kLeft + 16 * rt);
+      read_turned(0);
+      solve();
+      __builtin_amdgcn_sched_group_barrier(0x002, 40, 0);
+      beside_matrix<12, 3, 2>();
+      beside_matrix<6, 6, 0>();
+      __builtin_amdgcn_sched_barrier(0);
+      lds_barrier();                                 // the outputs have read the U before
+      // Every row of the last tile takes every value of R, if only 0 times: one that is no number shows there.  It is taken out then, as
+      // it would reach tokens that do not follow its own, and remembered.
+      if (__any(!finite(u[3][0]))) {
+        uint64_t mine = 0;
+        int row0 = 4 * g4;
+        asm volatile("" : "+v"(row0));               // else the bits of all rows are made before the loop, and kept
+#pragma unroll
+        for (int rt = 0; rt < 4; ++rt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!(fabsf(x[rt][i]) < 0x1.FFp127f)) {      // beyond BF16 is infinite too
+              mine |= (uint64_t)1 << (16 * rt + row0 + i);
+              x[rt][i] = 0.0f;
+            }
+        mine |= __shfl_xor(mine, 16);
+        mine |= __shfl_xor(mine, 32);
+        bad_col |= mine;
+        solve();
+      }
+      auto put_u = [&] {
+        const bf8 hi = high(u[2], u[3]);
+        if (g4 == 0) lds.bad[w][c16] = bad_col;
+        lds.u[0][w][0][lane] = first_high;
+        lds.u[1][w][0][lane] = first_low;
+        lds.u[0][w][1][lane] = hi;
+        lds.u[1][w][1][lane] = low(u[2], u[3], hi);
+      };
+      if (dst < 0 && c + 1 == chunks) {              // nobody asks for what S has become
+        put_u();
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+          for (int rt = 0; rt < 4; ++rt) asm volatile("" : "=v"(k[ks][rt]));      // not needed again: else one is kept, in memory
+        lds_barrier();
+        break;
+      }
+      // S, half of the tokens at a time: the other half's split runs beside, and the reads of the next chunk's K
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
+      put_u();
+      finish(1);
+      read_turned(1);
+      beside_matrix<2 * RT, 4, 2>();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
+#pragma unroll
+      for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
+      read_k(k1);
+      beside_matrix<2 * RT, 0, 1>();
+      __builtin_amdgcn_sched_barrier(0);
+      if (__any(bad_col != 0)) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
+      }
+      k0 = k1;
+      k1 = k1 == 2 ? 0 : k1 + 1;
       lds_barrier();
-      break;
     }
-    // S, half of the tokens at a time: the other half's split runs beside, and the reads of the next chunk's K
-    __builtin_amdgcn_sched_barrier(0);
+    if (dst >= 0) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
-    put_u();
-    finish(1);
-    read_turned(1);
-    beside_matrix<2 * RT, 4, 2>();
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], uh, st[i]);
-#pragma unroll
-    for (int i = 0; i < RT; ++i) st[i] = mma(kt[i], ul, st[i]);
-    read_k(k1);
-    beside_matrix<2 * RT, 0, 1>();
-    __builtin_amdgcn_sched_barrier(0);
-    if (__any(bad_col != 0)) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) st[i][e] = bad_col ? NAN : st[i][e];
-    }
-    k0 = k1;
-    k1 = k1 == 2 ? 0 : k1 + 1;
-    lds_barrier();
-  }
-  if (dst >= 0) {
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      f32x4v* p = reinterpret_cast<f32x4v*>(a.state + dst * a.slot_stride + state_at + 32 * ks);
-      p[0] = st[2 * ks];
-      p[1] = st[2 * ks + 1];
+      for (int ks = 0; ks < KS; ++ks) {
+        f32x4v* p = reinterpret_cast<f32x4v*>(a.state + dst * a.slot_stride + state_at + 32 * ks);
+        p[0] = st[2 * ks];
+        p[1] = st[2 * ks + 1];
+      }
     }
   }
 }
@@ -783,11 +842,18 @@ uint64_t delta_chunk_workspace_bytes(int32_t T, int32_t count, int32_t v_heads) 
 
 template <int DK>
 static hipError_t chunk_launches(const w12_delta_args& a, const w12_sequences& s, char* ws, hipStream_t stream) {
-  const dim3 terms((unsigned)most_pieces(s.T, s.count, kChunk), (unsigned)a.v_heads);
-  k_delta_terms<DK><<<terms, kChunkThreads, 0, stream>>>(a, s, ws);
-  const unsigned scans = (unsigned)((int64_t)s.count * a.v_heads * (a.dv / kScanColumns));
-  if (s.rows) k_delta_scan<DK, true><<<scans, kScanThreads, 0, stream>>>(a, s, ws);
-  else k_delta_scan<DK, false><<<scans, kScanThreads, 0, stream>>>(a, s, ws);
+  const int64_t pieces = most_pieces(s.T, s.count, kChunk), shorts = s.tree_mask ? 0 : (int64_t)s.count * (a.dv / kGroupColumns);
+  k_delta_terms<DK><<<dim3((unsigned)(pieces + shorts), (unsigned)a.v_heads), kChunkThreads, 0, stream>>>(a, s, ws, (int)pieces);
+  // A work-group for every long sequence there can be; where most are short, one round of the chip, which takes them in turn: a
+  // work-group that finds none keeps a compute unit, for its LDS, as long as it takes to look.
+  const int64_t of = a.v_heads * (a.dv / kScanColumns);
+  const bool many = !s.tree_mask && s.T < (int64_t)W12_DELTA_CHUNK_FROM * s.count;
+  const int64_t sequences = many ? std::min((int64_t)s.T / W12_DELTA_CHUNK_FROM, ceil_div(device_cus(), of)) : s.count;
+  const unsigned scans = (unsigned)(sequences * of);
+  if (many) s.rows ? k_delta_scan<DK, true, true><<<scans, kScanThreads, 0, stream>>>(a, s, ws)
+                   : k_delta_scan<DK, false, true><<<scans, kScanThreads, 0, stream>>>(a, s, ws);
+  else s.rows ? k_delta_scan<DK, true, false><<<scans, kScanThreads, 0, stream>>>(a, s, ws)
+              : k_delta_scan<DK, false, false><<<scans, kScanThreads, 0, stream>>>(a, s, ws);
   return hipGetLastError();
 }
 

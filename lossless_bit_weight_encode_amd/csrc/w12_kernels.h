@@ -93,10 +93,10 @@ hipError_t launch_gemm_e4m3(const uint8_t* X, int32_t M, int64_t ldx, const floa
 // Operators of a hybrid target (w12_conv.hip, w12_delta.hip, w12_delta_chunk.hip, w12_verify_draft.hip).
 hipError_t launch_short_conv(const w12_conv_args& a, const w12_sequences& s, hipStream_t stream);
 uint64_t gated_delta_workspace_bytes(int32_t T, int32_t count, int32_t v_heads, int32_t dk, int32_t dv);
-uint64_t gated_delta_call_bytes(const w12_sequences& s, int32_t v_heads);      // what a call needs of it
+uint64_t gated_delta_call_bytes(const w12_sequences& s, int32_t v_heads);      // what a call has to have of it
 uint64_t delta_chunk_workspace_bytes(int32_t T, int32_t count, int32_t v_heads);
 hipError_t launch_delta_chunks(const w12_delta_args& a, const w12_sequences& s, void* ws, hipStream_t stream);
-hipError_t launch_gated_delta(const w12_delta_args& a, const w12_sequences& s, void* ws, hipStream_t stream);
+hipError_t launch_gated_delta(const w12_delta_args& a, const w12_sequences& s, void* ws, uint64_t ws_bytes, hipStream_t stream);
 uint64_t verify_draft_workspace_bytes(int32_t T, int32_t requests, int32_t vocab);
 hipError_t launch_verify_draft(const w12_verify_draft_args& a, void* ws, hipStream_t stream);
 
