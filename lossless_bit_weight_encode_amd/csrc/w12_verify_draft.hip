@@ -91,7 +91,8 @@ __device__ __forceinline__ float logit(const w12_verify_draft_args& a, int64_t r
                     : bf16_float(static_cast<const uint16_t*>(a.logits)[row * a.ld_logits + i]));
 }
 
-// 2^t of t <= 0, to 2^-42 of itself: 2^f of the rest f in [-1/2, 1/2] by its series, whose first term left out is (ln 2 / 2)^11 / 11!.
+// 2^t of t <= 0, to 2^-41.6 of itself: 2^f of the rest f in [-1/2, 1/2] by its series, whose first term left out is (ln 2 / 2)^11 / 11! =
+// 2^-42.1, of 2^(-1/2) at the least.
 // t is rounded by adding 3/2 2^52, which leaves the whole number in the low bits; it goes into the exponent as it is (rounding and
 // scaling instructions of FP64 run at a part of the rate).  What is below 2^-1000 is 0.
 __device__ __forceinline__ double power(double t) {
