@@ -14,6 +14,14 @@
 // FP32 1e-7), and out is off by its rounding to BF16 alone (0.0017 of its norm; with S and U as one value each 0.0026, and a tree's outputs
 // further from those of its tokens one by one than their rounding).  T is made in FP32 throughout: 16 x 16 blocks by substitution (which
 // does not cancel as powers of A would), joined by FP32 matrix instructions.
+//
+// Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 186 us (terms 46, scan 143: 64 chunks, one after another, on 96 of 256
+// compute units), a tree of 63 nodes 16 (10 and 6), 16 trees of 24 nodes 47, seven prompts of 21834 tokens together, 32 heads, 405.  The scan
+// is bound by the waves that carry S: of a chunk's 5600 cycles, with the cycle counter noted, K S and S's split are 1700 to 2000, U 1000, the
+// search for values that are no numbers 500, S' 1500.  Hence the waves for loads and outputs beside them, whose traffic in LDS they
+// wait for: with S and U as one value each for out, half of that, the times were 159, 16, 45 and 363 us.  32 columns a work-group
+// were faster then for a prompt alone (142 against 158) and slower where work-groups fill the chip (467 against 346).  The terms wait for their loads and for one another's phases, at 5
+// work-groups a compute unit.
 #include "w12_delta_chunk.h"
 #include "w12_delta_steps.h"
 #include "w12_gemm_common.h"
@@ -24,13 +32,6 @@
 
 #include <algorithm>
 
-//
-// Measured, 48 heads of 128 x 128 over 16 of keys: a prompt of 4096 191 us (64 chunks, one after another, on 96 of 256 compute units), a tree of
-// 63 nodes 16, 16 trees of 24 nodes 47, seven prompts of 21834 tokens together, 32 heads, 405.  The scan is bound by the waves that carry S
-// (of a chunk's 5000 cycles 2000 are K S and S's split, 1000 U, 1600 S', 400 the search for values that are no numbers), hence the waves for
-// loads and outputs beside them, whose reads of LDS they wait for: with S and U as one value each for out, half of those reads, 159, 16, 45
-// and 363 us.  32 columns a work-group are faster for a prompt alone and slower where work-groups fill the chip.  The terms wait for their
-// loads and for one another's phases, at 5 work-groups a compute unit.
 namespace w12 {
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
@@ -98,7 +99,7 @@ __device__ __forceinline__ bf8 rows_operand(const char* m, int rt, int ks) {
 }
 
 // Whether a sequence's tokens are taken 64 at a time, which goes by their own number (and the form) alone: between 8 (48 heads of 128, 1 / 4 /
-// 16 / 64 sequences: 14 / 19 / 42 / 144 us token by token, 16 / 25 / 56 / 200 in chunks) and 16 (25 / 31 / 67 / 226 and 16 / 25 / 57 / 205).
+// 16 / 64 sequences: 13 / 18 / 41 / 131 us token by token, 15 / 24 / 60 / 212 in chunks) and 16 (21 / 29 / 65 / 215 and 15 / 25 / 59 / 216).
 __device__ __forceinline__ bool taken_in_chunks(const w12_sequences& s, const Range& r) { return s.tree_mask || r.n >= W12_DELTA_CHUNK_FROM; }
 
 // Sequence number j of those; false where there are fewer.  A wave looks at 64 at a time.
@@ -504,7 +505,7 @@ __global__ __launch_bounds__(kScanThreads) void k_delta_scan(w12_delta_args a, w
     for (; there; there = next()) {
       const int chunks = (r.n + kChunk - 1) / kChunk;
       // ---- outputs, half of the tokens a wave (tiles 0 and 3, or 1 and 2: 3 fragments of P each), turned: a lane's token (of each 16), and of
-      // every two tiles 8 neighbouring columns.  Few loads and stores: each takes a wave some 75 cycles to start.
+      // every two tiles 8 neighbouring columns, so that it stores 16 bytes.
       const int half = w - kTiles, tile[2] = {half, 3 - half};
       bf8 q[KS][2], pl[3];
       const char* const terms = ws + kZeroBytes + ((int64_t)first_piece(r, b, kChunk) * a.v_heads + h) * kTermsBytes;
