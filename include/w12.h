@@ -530,13 +530,12 @@ int w12_short_conv(const w12_conv_args *a, const w12_sequences *s, hipStream_t s
  * q and out NULL: only the states move on.  The result is bitwise the same from run to run.
  * dk: 64 or 128, dv: 64, 128 or 256, v_heads a multiple of k_heads, at most 1024.
  * ws: w12_gated_delta_workspace_size bytes for T rows in count sequences (or more), 16-byte aligned, any content; calls
- * that overlap in time need workspaces of their own.  Only tokens taken 64 at a time need it: those of a tree, and of a call with
- * T >= W12_DELTA_CHUNK_FROM * count rows (with lens: W12_DELTA_CHUNK_FROM_LENS * count).  A call of fewer rows may have a NULL ws, or a small
- * one, and takes all tokens one by one; without lens and with T - count + 1 >= W12_DELTA_CHUNK_LONG, where one sequence can be long beside the
- * others, a ws is worth its bytes.  A call that has what it takes for 64 at a time takes a tree so, and each sequence that has
- * W12_DELTA_CHUNK_FROM tokens or more itself (after lens), whatever the others have; the others token by token.  So a sequence's result does
- * not depend, bit for bit, on those that share its call, but for one of W12_DELTA_CHUNK_FROM tokens or more in a call that takes all one by one:
- * out is rounded once in either form.
+ * that overlap in time need workspaces of their own.  A call with a tree or of T >= W12_DELTA_CHUNK_FROM * count rows (with lens:
+ * W12_DELTA_CHUNK_FROM_LENS * count) has to have it, and one without lens and with T - count + 1 >= W12_DELTA_CHUNK_LONG, in which a sequence can be
+ * long beside short ones, should.  Such a call takes trees, and each sequence that has W12_DELTA_CHUNK_FROM tokens or more itself (after lens),
+ * 64 at a time and the others token by token: a sequence's result does not depend, bit for bit, on those that share the call.  Every
+ * other call, and one of fewer than W12_DELTA_CHUNK_FROM * count rows whose ws is NULL or too small, takes all tokens one by one and needs no
+ * workspace.  Either form rounds out once.
  */
 #define W12_DELTA_CHUNK_FROM 12
 #define W12_DELTA_CHUNK_FROM_LENS 65

@@ -20,8 +20,8 @@
 // is bound by the waves that carry S: of a chunk's 5600 cycles, with the cycle counter noted, K S and S's split are 1700 to 2000, U 1000, the
 // search for values that are no numbers 500, S' 1500.  Hence the waves for loads and outputs beside them, whose traffic in LDS they
 // wait for: with S and U as one value each for out, half of that, the times were 159, 16, 45 and 363 us.  32 columns a work-group
-// were faster then for a prompt alone (142 against 158) and slower where work-groups fill the chip (467 against 346).  The terms wait for their loads and for one another's phases, at 5
-// work-groups a compute unit.
+// were faster then for a prompt alone (142 against 158) and slower where work-groups fill the chip (467 against 346).  The terms wait for their
+// loads and for one another's phases, at 5 work-groups a compute unit.
 #include "w12_delta_chunk.h"
 #include "w12_delta_steps.h"
 #include "w12_gemm_common.h"

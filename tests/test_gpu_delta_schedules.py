@@ -149,3 +149,55 @@ def test_many_long_sequences_among_short_ones():
         else:
             alone[b + i] = alone[i]
         assert torch.equal(state[b + i], alone[b + i])
+
+
+@pytest.mark.parametrize("lengths", [[70, 1, 13, 0, 2] + [1] * 30, [14] * 120 + [1, 0] * 40])
+def test_rows_of_long_and_short_sequences(lengths):
+    """Rows that are named, in any order, some of them none; with and without new states."""
+    r = random.Random(3)
+    t, b, ptr = sum(lengths), len(lengths), starts(lengths)
+    d = Delta(t, 2 * b, 4, 4, 64, 128, seed=260)
+    mats, state = d.on_gpu()
+    rows = list(range(t))
+    r.shuffle(rows)
+    for i in r.sample(range(t), 5):
+        rows[i] = r.choice((-1, t, -7))
+    src, dst, named = ints(list(range(b))), ints([b + i if i % 5 else -1 for i in range(b)]), ints(rows)
+    out, ok = out_buf(t, 512, 512, BF)
+    w12.gated_delta(*mats, state, ints(ptr), src, dst=dst, rows=named, out=out)
+    assert ok()
+    # the rows laid out in their order, zeros for none of them
+    there = torch.tensor([0 <= x < t for x in rows])
+    at = torch.tensor([x if 0 <= x < t else 0 for x in rows]).cuda()
+    laid = [m[at] * there.cuda()[:, None] for m in mats]
+    _, alone = d.on_gpu()
+    want = w12.gated_delta(*laid, alone, ints(ptr), src, dst=dst)
+    assert torch.equal(state, alone) and same(out[at[there.cuda()]], want[there.cuda()])
+    left = sorted(set(range(t)) - {x for x in rows if 0 <= x < t})
+    assert (out.cpu()[left].view(torch.int16) == 0x55).all()
+    stays = w12.gated_delta(*mats, state, ints(ptr), src, rows=named)
+    assert torch.equal(state, alone) and same(stays[at[there.cuda()]], want[there.cuda()])
+
+
+def test_what_is_no_number_stays_in_its_sequence():
+    """Among many long and short sequences, of which a work-group takes several one after another."""
+    lengths = [14] * 120 + [3] * 60
+    random.Random(4).shuffle(lengths)
+    t, b, ptr = sum(lengths), len(lengths), starts(lengths)
+    d = Delta(t, 2 * b, 4, 4, 64, 128, seed=270)
+    mats, state = d.on_gpu()
+    clean_state = state.clone()
+    args = (ints(ptr), ints(list(range(b))))
+    clean = w12.gated_delta(*mats, clean_state, *args, dst=ints(list(range(b, 2 * b))))
+    hit = [5, 50, 51, 100, 170]
+    for i in hit:
+        mats[1][ptr[i] + 1, 0] = float("nan")
+    dirty = w12.gated_delta(*mats, state, *args, dst=ints(list(range(b, 2 * b))))
+    bad_rows = torch.zeros(t, dtype=torch.bool)
+    for i in hit:
+        bad_rows[ptr[i] + 1:ptr[i + 1]] = True
+        assert state[b + i, 0].isnan().all() and torch.equal(state[b + i, 1:], clean_state[b + i, 1:])
+    assert dirty[bad_rows][:, :128].isnan().all() and same(dirty[:, 128:], clean[:, 128:])
+    assert same(dirty[~bad_rows], clean[~bad_rows])
+    others = [b + i for i in range(b) if i not in hit]
+    assert torch.equal(state[others], clean_state[others])
